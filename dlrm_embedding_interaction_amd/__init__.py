@@ -13,6 +13,7 @@ Functions take CUDA (HIP) torch tensors:
 * ``linear_bias_act(x, W, bias, act)`` -> (M, N)
 * ``Model(...)`` holding DLRMv1 parameters, with ``forward(dense, indices, offsets)``
 * ``check_indices(...)``, ``pair_index_map(F)``, ``workspace_bytes``
+* ``history_attention(q, k, v, offsets, window, sinks)`` and ``HistoryCache``, the event-history operators
 """
 from __future__ import annotations
 
@@ -128,6 +129,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
               "dlrm_pair_index_map",
               "dlrm_probe_read_stream", "dlrm_probe_gather_rows", "dlrm_probe_l2_stream"):
         getattr(L, f).restype = ctypes.c_int
+    declare_history(L)
     if L.dlrm_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIBRARY}: ABI version {L.dlrm_abi_version()} != {ABI_VERSION}")
     _LIB = L
@@ -581,3 +583,6 @@ def probe_l2_stream(src: torch.Tensor, blocks: int = 256, sink: Optional[torch.T
     _check(L.dlrm_probe_l2_stream(src.data_ptr(), src.numel(), int(blocks), sink.data_ptr(), _stream(src.device)),
            "dlrm_probe_l2_stream")
     return sink
+
+
+from .history import HistoryCache, declare as declare_history, history_attention  # noqa: E402,F401

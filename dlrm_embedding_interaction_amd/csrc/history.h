@@ -1,0 +1,133 @@
+// history.h -- launch functions and device helpers of the event-history
+// operators: windowed attention over ragged histories, the 8-bit paged cache
+// and the management of its pages.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/dlrm_mi355x.h"
+#include "dlrm_device.h"
+
+namespace dlrm {
+
+constexpr int kScaleFloor = -100;    // smallest exponent of a page's power-of-two scale
+constexpr int kRebuildChunk = 4096;  // pages per block of the free-list rebuild
+
+typedef __bf16 bf16;
+typedef _Float16 f16;
+
+// Arguments of the attention over ragged histories.
+struct EncodeArgs {
+    const void *q, *k, *v, *offsets;
+    const uint8_t* padding;
+    void* out;
+    int64_t ld_q, ld_k, ld_v, ld_out, n_events, window, sinks;
+    int batch, n_heads, n_kv, idx32;
+    float scale;
+};
+
+// Arguments of the attention over the cache.
+struct LookupArgs {
+    dlrm_history_cache_t c;
+    const int32_t* slots;
+    const void* q;
+    void* out;
+    float* partial;
+    int64_t ld_q, ld_out, window, sinks;
+    int batch, queries, n_heads;
+    float scale;
+};
+
+// What the reservation decided for one history of an append: its events
+// before (-1: refused), the free-list position of its first new page, the page
+// that holds its last part (-1: none), and whether that page is copied because
+// other histories hold it too.
+struct Grant {
+    int old_len, pos, src, copy;
+};
+
+struct AppendArgs {
+    dlrm_history_cache_t c;
+    const int32_t* slots;
+    const void *k, *v, *offsets;
+    Grant* grants;
+    int64_t ld_k, ld_v, n_events;
+    int batch, idx32;
+};
+
+hipError_t launch_history_attention(const EncodeArgs& a, int dtype, int dim, hipStream_t s);
+hipError_t launch_history_lookup(const LookupArgs& a, int dtype, hipStream_t s);
+size_t lookup_workspace_bytes(const dlrm_history_cache_t& c, int64_t batch, int queries, int n_heads);
+
+hipError_t launch_history_init(const dlrm_history_cache_t& c, hipStream_t s);
+hipError_t launch_history_append(const AppendArgs& a, int dtype, hipStream_t s);
+hipError_t launch_history_fork(const dlrm_history_cache_t& c, int n, const int32_t* src, const int32_t* dst,
+                               int32_t* counts, hipStream_t s);
+hipError_t launch_history_truncate(const dlrm_history_cache_t& c, int n, const int32_t* slots,
+                                   const int32_t* new_lens, int32_t* counts, hipStream_t s);
+hipError_t launch_history_trim(const dlrm_history_cache_t& c, int n, const int32_t* slots, int64_t window,
+                               int64_t sinks, int32_t* counts, hipStream_t s);
+hipError_t launch_history_compact(const dlrm_history_cache_t& c, int32_t* ws, hipStream_t s);
+inline int rebuild_chunks(int n_pages) { return (n_pages + kRebuildChunk - 1) / kRebuildChunk; }
+
+// Bounds of history b in the packed events, kept inside [0, n] whatever the
+// offsets hold.
+__device__ __forceinline__ int64_t history_begin(const void* off, int idx32, int64_t b, int64_t n) {
+    const int64_t o = ld_index(off, b, idx32);
+    return o < 0 ? 0 : (o > n ? n : o);
+}
+__device__ __forceinline__ int64_t history_end(const void* off, int idx32, int64_t b, int64_t batch, int64_t begin,
+                                               int64_t n) {
+    const int64_t o = b + 1 < batch ? ld_index(off, b + 1, idx32) : n;
+    return o < begin ? begin : (o > n ? n : o);
+}
+
+// The history that owns unit u when history b's units begin at
+// floor(off[b] / width) + extra * b.  That start grows by at least
+// floor(len / width) + extra from one history to the next, so no count of units
+// has to be summed over the batch: with extra = 1 there is room for
+// ceil(len / width) units, with extra = 2 for the pages an append of len events
+// can touch.  Returns the history and u's number within it.
+__device__ __forceinline__ int history_of_unit(const void* off, int idx32, int batch, int64_t n, int width,
+                                               int extra, int64_t u, int64_t* nth) {
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (history_begin(off, idx32, mid, n) / width + (int64_t)extra * mid <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    *nth = u - (history_begin(off, idx32, lo, n) / width + (int64_t)extra * lo);
+    return lo;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
+
+// One element of T as fp32 and back (round to nearest even).
+template <typename T>
+__device__ __forceinline__ float ld_f32(const T* p) {
+    return (float)*p;
+}
+
+// e4m3 codes: two floats to two codes in the low half, and one code to fp32.
+__device__ __forceinline__ unsigned pk_e4m3(float a, float b) {
+    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xffffu;
+}
+__device__ __forceinline__ float e4m3_f32(unsigned code) { return __builtin_amdgcn_cvt_f32_fp8((int)code, 0); }
+
+// The smallest power of two s >= 2^kScaleFloor with amax / s <= 448 (the
+// largest e4m3 value, 0.875 x 2^9).  Read off the bits, so exact: amax =
+// m 2^x with m in [1, 2) gives 2^(x - 8) for m <= 1.75 and 2^(x - 7) above.
+__device__ __forceinline__ float page_scale(float amax) {
+    const unsigned bits = __float_as_uint(amax);
+    int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = e < kScaleFloor ? kScaleFloor : e;
+    return __uint_as_float((unsigned)(e + 127) << 23);
+}
+
+}  // namespace dlrm

@@ -416,6 +416,174 @@ dlrm_status_t dlrm_embbag_check_indices(int32_t num_tables, int64_t batch, const
 dlrm_status_t dlrm_pair_index_map(int32_t n_feat, int32_t* i_out, int32_t* j_out, void* stream);
 
 /*
+ * Event histories
+ * ---------------
+ * Attention over a user's past events, where the bags above only pool them: an
+ * encoder over whole histories, a paged cache of keys and values in 8 bits
+ * that grows by one event at a time, and the lookup of a query (the newest
+ * event, or a candidate item) in it.  Forward only, like the rest of the
+ * library.  Heads of one event lie side by side: element (head h, d) of row r
+ * is at r * ld + h * head_dim + d, so q, k and v may be columns of one
+ * dlrm_linear_bias_act output.  Query head h reads kv head
+ * h / (n_heads / n_kv_heads).
+ */
+
+/* Element types of the history calls. */
+#define DLRM_DTYPE_F32 0
+#define DLRM_DTYPE_BF16 1
+#define DLRM_DTYPE_F16 2
+
+/*
+ * What an event sees.  An event at position i of its history sees the events
+ * j <= i with i - j < window or j < sinks: the last `window` events, itself
+ * included, and the first `sinks`.  A row that sees nothing gives zeros, as an
+ * empty bag does.
+ *   dtype       of q, k, v and out; products, softmax statistics and sums are
+ *               held in fp32 (fp32 inputs lose nothing to the matrix cores:
+ *               they are multiplied as sums of bf16 parts)
+ *   n_heads     a multiple of n_kv_heads, at most 4096
+ *   head_dim    32, 64 or 128, else DLRM_E_UNSUPPORTED
+ *   window      >= 1 (a value no history reaches: all earlier events)
+ *   sinks       >= 0
+ *   scale       of the products, usually head_dim^-1/2; finite
+ */
+typedef struct dlrm_attention {
+    int32_t dtype;
+    int32_t n_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int64_t window;
+    int64_t sinks;
+    float scale;
+    int32_t reserved;
+} dlrm_attention_t;
+
+/*
+ * dlrm_history_attention -- every event of `batch` ragged histories attends to
+ * its own history.  History b is the rows [offsets[b], offsets[b+1]) of q, k,
+ * v and out, the last one ending at n_events (the bags' convention; histories
+ * may be empty).
+ *   n_events   total rows, >= 0 (0: nothing is enqueued)
+ *   offsets    device (batch) integers of index_bytes
+ *   q, out     device (n_events, ld_q / ld_out), n_heads * head_dim columns used
+ *   k, v       device (n_events, ld_k / ld_v), n_kv_heads * head_dim columns used
+ *   padding    device (n_events) bytes or NULL; events with a nonzero byte are
+ *              seen by no one.  Infinities and NaN in events a row does not
+ *              see do not reach it.
+ * out must not overlap q, k or v.  Rows of 16-byte aligned tensors whose ld is
+ * a multiple of 16 bytes are read 16 bytes at a time, others by element.
+ */
+dlrm_status_t dlrm_history_attention(const dlrm_attention_t* a, int64_t batch, int64_t n_events,
+                                     const void* offsets, int32_t index_bytes, const void* q, int64_t ld_q,
+                                     const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                                     const uint8_t* padding, void* out, int64_t ld_out, void* stream);
+
+/*
+ * The history cache: n_slots histories over a pool of n_pages pages of
+ * page_events (16, 32 or 64) events each.  All arrays are device memory of the
+ * caller; the calls change what they hold in stream order.
+ *   k           (n_pages, n_kv_heads, page_events, head_dim) e4m3 codes
+ *   v           (n_pages, n_kv_heads, head_dim, page_events) e4m3 codes: events
+ *               innermost, the order the weighted sum reads them in
+ *   k_scale, v_scale  (n_pages, n_kv_heads): a value is its code times the scale
+ *               of its page and head, the smallest power of two >= 2^-100 under
+ *               which the largest finite value of the block is at most 448.
+ *               It only grows while a page fills; the codes the page holds are
+ *               then rounded again.  Values that are not finite are held as NaN.
+ *   table       (n_slots, max_pages): page of each history's events
+ *               [i * page_events, (i + 1) * page_events), -1 where there is none
+ *   lens        (n_slots) events of each history, <= max_pages * page_events
+ *   refs        (n_pages) histories that hold the page
+ *   free_pages  (n_pages): its first counters[0] entries are the pages without a
+ *               holder, in descending order; the last one is taken first
+ *   counters    (4): pages in free_pages; histories refused so far (below); two
+ *               reserved
+ * k and v are 16-byte aligned (DLRM_E_SHAPE otherwise).  In every call, slots
+ * outside [0, n_slots) are refused: nothing happens for them and counters[1]
+ * grows by one; table entries outside [0, n_pages) are events that nothing
+ * sees.  No slot may appear twice in one call, nor as source and destination
+ * of one fork.
+ *
+ * dlrm_history_workspace_bytes -- workspace of the calls below for up to
+ *   `batch` histories and, for dlrm_history_lookup, `queries` per history of
+ *   n_heads heads (0, 0: the other calls alone); 0 on invalid arguments.  Host
+ *   only.  Workspaces are 256-byte aligned and may be shared by calls in order
+ *   on one stream.
+ *
+ * dlrm_history_init -- an empty cache: no events, every page free.
+ */
+typedef struct dlrm_history_cache {
+    int32_t n_pages;
+    int32_t page_events;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t n_slots;
+    int32_t max_pages;
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int32_t* table;
+    int32_t* lens;
+    int32_t* refs;
+    int32_t* free_pages;
+    int32_t* counters;
+} dlrm_history_cache_t;
+
+size_t dlrm_history_workspace_bytes(const dlrm_history_cache_t* c, int64_t batch, int32_t queries,
+                                    int32_t n_heads);
+dlrm_status_t dlrm_history_init(const dlrm_history_cache_t* c, void* stream);
+
+/*
+ * dlrm_history_append -- events behind `batch` histories.  History slots[b] (b
+ * itself when slots is NULL) grows by the rows [offsets[b], offsets[b+1]) of k
+ * and v, the last one ending at n_events; a history may get none, one or many.
+ * Pages are taken as needed; a part-filled last page that other histories hold
+ * too is copied first.  Pages are granted in batch order; a history that would
+ * pass the last free page or max_pages, or whose part-filled last page is not
+ * there, is refused whole: it stays as it was and counters[1] grows by one.
+ *   dtype   of k and v; ld_k, ld_v as in dlrm_history_attention
+ */
+dlrm_status_t dlrm_history_append(const dlrm_history_cache_t* c, int64_t batch, const int32_t* slots,
+                                  int32_t dtype, int64_t n_events, const void* offsets, int32_t index_bytes,
+                                  const void* k, int64_t ld_k, const void* v, int64_t ld_v, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/*
+ * dlrm_history_lookup -- `queries` query rows for each of `batch` histories
+ * attend to the cached events of slots[b] (b when slots is NULL).  Every query
+ * stands at the history's last position: it sees the last `window` events and
+ * the first `sinks`.  Row b * queries + c of q and out is query c of history b.
+ * An empty history gives zeros.  a->n_kv_heads and a->head_dim are the cache's.
+ */
+dlrm_status_t dlrm_history_lookup(const dlrm_history_cache_t* c, const dlrm_attention_t* a, int64_t batch,
+                                  const int32_t* slots, int32_t queries, const void* q, int64_t ld_q, void* out,
+                                  int64_t ld_out, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Pages.  Each of these calls takes n device slots.
+ *
+ * dlrm_history_fork      dst[i] lets go of what it held and takes over src[i]'s
+ *                        events by sharing its pages; nothing is copied until one
+ *                        of them appends.  One source may be forked many times.
+ * dlrm_history_truncate  cuts slots[i] to its first new_lens[i] events (NULL: 0,
+ *                        the history is freed).  A length below 0, above the
+ *                        history's or inside a page that was trimmed is refused.
+ * dlrm_history_trim      lets go of the pages of which no later query with this
+ *                        window and these sinks sees an event; the length stays.
+ * dlrm_history_compact   with m pages in use, moves the i-th used page at or above
+ *                        m to the i-th free one below m, so that the first m pages
+ *                        hold everything.
+ */
+dlrm_status_t dlrm_history_fork(const dlrm_history_cache_t* c, int64_t n, const int32_t* src, const int32_t* dst,
+                                void* workspace, size_t ws_bytes, void* stream);
+dlrm_status_t dlrm_history_truncate(const dlrm_history_cache_t* c, int64_t n, const int32_t* slots,
+                                    const int32_t* new_lens, void* workspace, size_t ws_bytes, void* stream);
+dlrm_status_t dlrm_history_trim(const dlrm_history_cache_t* c, int64_t n, const int32_t* slots, int64_t window,
+                                int64_t sinks, void* workspace, size_t ws_bytes, void* stream);
+dlrm_status_t dlrm_history_compact(const dlrm_history_cache_t* c, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Measurement helpers (not part of the forward).  They set the bandwidth
  * ceilings the bag and interaction kernels are reported against, from kernels
  * of this library rather than a vendor copy.  Both only read memory; sink is
