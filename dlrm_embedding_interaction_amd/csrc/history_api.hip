@@ -47,6 +47,14 @@ dlrm_status_t check_cache_pointers(const dlrm_history_cache_t* c) {
     return DLRM_OK;
 }
 
+// Whether the lookup's tiles fit an int and its chunks of query rows a grid.
+bool lookup_fits(const dlrm_history_cache_t* c, int64_t batch, int32_t queries, int32_t n_heads) {
+    const int64_t rows = (int64_t)queries * (n_heads / c->n_kv_heads);
+    const int64_t tiles = ((int64_t)c->max_pages * c->page_events + 63) / 64;
+    return (int64_t)queries * batch <= kIntLimit && (rows + 15) / 16 * c->n_kv_heads <= 65535 &&
+           batch * tiles <= kIntLimit;
+}
+
 // Bytes for the chunk counts and the lists of a compaction.
 size_t compact_bytes(const dlrm_history_cache_t* c) {
     return round256(((size_t)3 * c->n_pages + rebuild_chunks(c->n_pages) + 1) * sizeof(int32_t));
@@ -102,7 +110,7 @@ DLRM_API size_t dlrm_history_workspace_bytes(const dlrm_history_cache_t* c, int6
                                              int32_t n_heads) {
     if (check_cache(c) != DLRM_OK || batch < 1 || batch > kIntLimit || queries < 0 || n_heads < 0) return 0;
     if (queries > 0 && (n_heads < 1 || n_heads > 4096 || n_heads % c->n_kv_heads != 0)) return 0;
-    if ((int64_t)queries * batch > kIntLimit) return 0;
+    if (queries > 0 && !lookup_fits(c, batch, queries, n_heads)) return 0;
     return workspace_bytes(c, batch, queries, n_heads);
 }
 
@@ -148,7 +156,7 @@ DLRM_API dlrm_status_t dlrm_history_lookup(const dlrm_history_cache_t* c, const 
     if (at->n_kv_heads != c->n_kv_heads || at->head_dim != c->head_dim || batch < 1 || queries < 1)
         return DLRM_E_SHAPE;
     if (!slots && batch > c->n_slots) return DLRM_E_SHAPE;
-    if (batch > kIntLimit || (int64_t)queries * batch > kIntLimit) return DLRM_E_UNSUPPORTED;
+    if (batch > kIntLimit || !lookup_fits(c, batch, queries, at->n_heads)) return DLRM_E_UNSUPPORTED;
     const int64_t w = (int64_t)at->n_heads * at->head_dim;
     if (ld_q < w || ld_out < w) return DLRM_E_SHAPE;
     st = check_workspace(workspace, ws_bytes, round256(lookup_workspace_bytes(*c, batch, queries, at->n_heads)));

@@ -2,87 +2,431 @@
 //
 // The queries of history b stand at its last position len - 1 and see event j
 // iff j >= len - window or j < sinks.  Keys and values are e4m3 codes times the
-// power-of-two scale of their page and head.
+// power-of-two scale of their page and head: exact in bf16.
+//
+// What bounds it is reading the codes, 2 head_dim bytes per visible event and kv
+// head, so the work is split over waves that never wait for one another.  The
+// visible events of all histories make one row of 64-event tiles, and each wave
+// takes an equal, contiguous run of it, whatever the lengths are.  Only the first
+// and the last history of a run can be cut; their maximum, sum and weighted sum
+// go to the workspace and a second kernel joins them.
+//
+// One tile in one wave, products on the matrix cores (16x16x32, bf16), with the
+// query rows of the kv head (queries x heads per kv head, in chunks of 16) as the
+// columns of both products:
+//   S^T = K Q^T   four products of 16 events each.  Row m of product t is event
+//                 16 (m / 4) + 4 t + m % 4, so that lane group g = lane / 16 ends
+//                 up with the scores of events 16 g .. 16 g + 15, in order.
+//   O^T += V^T P^T  the sum runs over the events each lane group holds: P^T is the
+//                 lane's own scores, V^T sixteen consecutive bytes of the
+//                 event-minor value page.
+// K, V and P go from memory or registers straight into the products; nothing
+// passes through LDS.  Products of the query's 8-bit-mantissa parts (bf16: one
+// part, fp16: two, fp32: three, no bit lost) with the codes are exact; the sums
+// are fp32.  The weights are kept in two bf16 parts (fp32 queries: three), since
+// rounding them to one would add an error as large as the output's own rounding.
 #include "history.h"
 
 namespace dlrm {
 
-template <typename T>
-__global__ __launch_bounds__(64) void history_lookup_kernel(LookupArgs a) {
-    __shared__ float qs[128];
-    __shared__ float ps[64];
-    const int lane = threadIdx.x, h = blockIdx.y, hk = h / (a.n_heads / a.c.n_kv_heads);
-    const int64_t row = blockIdx.x;
-    const int b = (int)(row / a.queries), dim = a.c.head_dim, pe = a.c.page_events;
+constexpr int kTile = 64;                // events per tile
+constexpr int kLookupWaves = 2048;       // waves a launch aims at: two on each SIMD
+
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
+// The visible tiles of a history: `lead` tiles from its start, then the tiles
+// from `first` on, `count` in all.
+struct Span {
+    int len, low, lead_events, first, lead, count;
+};
+
+__device__ __forceinline__ Span span_of(const LookupArgs& a, int b) {
+    Span s;
     const int slot = a.slots ? a.slots[b] : b;
     const bool held = slot >= 0 && slot < a.c.n_slots;
-    const int64_t span = (int64_t)a.c.max_pages * pe;
-    int64_t len = held ? a.c.lens[slot] : 0;
-    len = len < 0 ? 0 : (len > span ? span : len);
-    const T* q = (const T*)a.q + row * a.ld_q + (int64_t)h * dim;
-    for (int d = lane; d < dim; d += 64) qs[d] = ld_f32(q + d);
-    __syncthreads();
-    float m = -INFINITY, l = 0.f, acc[2] = {0.f, 0.f};
-    const int64_t first = len - a.window > 0 ? len - a.window : 0;
-    const int64_t lead = a.sinks < first ? a.sinks : first;
-    const int64_t lead_tiles = (lead + 63) / 64;
-    const int64_t tiles = lead_tiles + (len - first + 63) / 64;
-    for (int64_t t = 0; t < tiles; ++t) {
-        const int64_t base = t < lead_tiles ? t * 64 : first + (t - lead_tiles) * 64;
-        const int64_t stop = t < lead_tiles ? lead : len;
-        const int64_t j = base + lane;
-        bool seen = j < stop;
-        int page = -1;
-        if (seen) {
-            page = a.c.table[(int64_t)slot * a.c.max_pages + j / pe];
-            seen = page >= 0 && page < a.c.n_pages;
+    const int most = a.c.max_pages * a.c.page_events;
+    int len = held ? a.c.lens[slot] : 0;
+    len = len < 0 ? 0 : (len > most ? most : len);
+    int low = len > a.window ? len - (int)a.window : 0;
+    int lead = (int)(a.sinks < low ? a.sinks : low);
+    if (lead == low) low = lead = 0;     // the sinks reach the window: everything is seen
+    s.len = len;
+    s.low = low;
+    s.lead_events = lead;
+    s.first = low / kTile;
+    s.lead = (lead + kTile - 1) / kTile;
+    s.lead = s.lead < s.first ? s.lead : s.first;
+    s.count = len ? s.lead + (len + kTile - 1) / kTile - s.first : 0;
+    return s;
+}
+
+// fp32 values as sums of bf16 parts cut off at 8 bits each: the high halves of
+// two words, packed.
+__device__ __forceinline__ unsigned pack_hi(float a, float b) {
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+
+template <int N>
+__device__ __forceinline__ void split8(const float* x, bf16x8* part) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack_hi(r[2 * i], r[2 * i + 1]);
+        part[n] = __builtin_bit_cast(bf16x8, w);
+        if (n + 1 < N) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] -= cut(r[i]);
         }
-        float s = -INFINITY;
-        if (seen) {
-            const int64_t ph = (int64_t)page * a.c.n_kv_heads + hk;
-            const uint8_t* k = a.c.k + (ph * pe + j % pe) * dim;
-            float dot = 0.f;
-            for (int d = 0; d < dim; ++d) dot = fmaf(qs[d], e4m3_f32(k[d]), dot);
-            s = dot * a.c.k_scale[ph] * a.scale;
-        }
-        const float mt = fmaxf(m, wave_max(s));
-        if (mt == -INFINITY) continue;
-        const float p = seen ? __expf(s - mt) : 0.f;
-        const float alpha = __expf(m - mt);
-        l = l * alpha + wave_sum(p);
-        m = mt;
-        __syncthreads();
-        ps[lane] = seen ? p : -1.f;
-        __syncthreads();
-        for (int c = 0; c < 2; ++c) {
-            const int d = lane + c * 64;
-            if (d >= dim) continue;
-            float o = acc[c] * alpha;
-            for (int x = 0; x < 64; ++x)
-                if (ps[x] >= 0.f || ps[x] != ps[x]) {
-                    const int64_t jj = base + x;
-                    const int pg = a.c.table[(int64_t)slot * a.c.max_pages + jj / pe];
-                    const int64_t ph = (int64_t)pg * a.c.n_kv_heads + hk;
-                    o = fmaf(ps[x], e4m3_f32(a.c.v[(ph * dim + d) * pe + jj % pe]) * a.c.v_scale[ph], o);
-                }
-            acc[c] = o;
-        }
-    }
-    T* out = (T*)a.out + row * a.ld_out + (int64_t)h * dim;
-    for (int c = 0; c < 2; ++c) {
-        const int d = lane + c * 64;
-        if (d < dim) out[d] = (T)(l == 0.f ? 0.f : acc[c] / l);
     }
 }
 
-size_t lookup_workspace_bytes(const dlrm_history_cache_t&, int64_t, int, int) { return 256; }
+// Eight codes times their scale as bf16.
+__device__ __forceinline__ bf16x8 decode8(unsigned lo, unsigned hi, float scale) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    const u32x4 w = {__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b),
+                     __builtin_bit_cast(unsigned, c), __builtin_bit_cast(unsigned, d)};
+    return __builtin_bit_cast(bf16x8, w);
+}
+
+template <typename T> struct Parts;
+template <> struct Parts<bf16> { static constexpr int q = 1, p = 2; };
+template <> struct Parts<f16> { static constexpr int q = 2, p = 2; };
+template <> struct Parts<float> { static constexpr int q = 3, p = 3; };
+
+// The codes of one tile as the products take them.
+template <int D>
+struct Tile {
+    static constexpr int KL = D >= 64 ? D / 64 : 1;     // 16-byte loads of a key row per lane (D 32: 8 bytes)
+    u32x4 k[4][KL];
+    u32x4 v[D / 16];
+    float ks, vs;
+    bool kin, vin;                                      // the pages are there
+};
+
+template <int D, int PE, typename T>
+__global__ __launch_bounds__(256, 2) void history_lookup_kernel(LookupArgs a, int n_waves, int* __restrict__ meta) {
+    constexpr int NQ = Parts<T>::q, NP = Parts<T>::p;
+    constexpr int KS = D / 32;                          // 32-element steps of the first product
+    constexpr int PT = kTile / PE;                      // pages per tile
+    __shared__ int before[256];
+    __shared__ int wsum[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int n = lane & 15, g = lane >> 4;
+    const int group = a.n_heads / a.c.n_kv_heads, rows = a.queries * group;
+    const int chunks = (rows + 15) / 16;
+    const int hk = blockIdx.y / chunks, r = (blockIdx.y % chunks) * 16 + n;
+    const int cols = rows < 16 ? rows : 16;             // columns of a partial result
+
+    // tiles before each thread's share of the histories
+    const int each = (a.batch + 255) / 256;
+    const int b_lo = tid * each, b_hi = b_lo + each < a.batch ? b_lo + each : a.batch;
+    int mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += span_of(a, b).count;
+    int inc = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(inc, d, 64);
+        if (lane >= d) inc += o;
+    }
+    if (lane == 63) wsum[wave] = inc;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i < wave) inc += wsum[i];
+        total += wsum[i];
+    }
+    before[tid] = inc - mine;
+    __syncthreads();
+    const int per = total > n_waves ? (total + n_waves - 1) / n_waves : 1;
+    const int w = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + wave);
+    if (w == 0 && blockIdx.y == 0 && lane == 0) meta[a.batch] = per;
+    int64_t at64 = (int64_t)w * per;
+    if (at64 >= total) return;
+    int at = (int)at64;
+    const int stop = at + per < total ? at + per : total;
+    int lo = 0, hi = 255;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] <= at) lo = mid;
+        else hi = mid - 1;
+    }
+    int start = __builtin_amdgcn_readfirstlane(before[lo]);       // tiles before history b
+    int b = __builtin_amdgcn_readfirstlane(lo * each);
+
+    while (at < stop) {
+        const Span sp = span_of(a, b);
+        if (start + sp.count <= at) {
+            start += sp.count;
+            ++b;
+            continue;
+        }
+        const int i0 = at - start, i1 = sp.count < stop - start ? sp.count : stop - start;
+        if (i0 == 0 && blockIdx.y == 0 && lane == 0) meta[b] = start;
+        const int slot = a.slots ? a.slots[b] : b;
+        const int32_t* table = a.c.table + (int64_t)slot * a.c.max_pages;
+
+        // the lane's query column: elements l 64 + g 16 + 8 u + i (D 32: g 8 + i) for step 2 l + u
+        bf16x8 q[KS][NQ];
+        const bool live = r < rows;
+        const int64_t qrow = (int64_t)b * a.queries + (live ? r / group : 0);
+        const int qhead = hk * group + (live ? r % group : 0);
+        {
+            const T* qp = (const T*)a.q + qrow * a.ld_q + (int64_t)qhead * D;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const int d0 = D == 32 ? g * 8 : (s >> 1) * 64 + g * 16 + (s & 1) * 8;
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = live ? (float)qp[d0 + i] : 0.f;
+                split8<NQ>(x, q[s]);
+            }
+        }
+        floatx4 o[D / 16];
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) o[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+        float m = -INFINITY, l = 0.f;
+
+        auto tile_of = [&](int i) { return i < sp.lead ? i : sp.first + (i - sp.lead); };
+        auto load = [&](int i, Tile<D>& t) {
+            const int p0 = tile_of(i) * PT;
+            int pk, pv;
+            if constexpr (PT == 1) {
+                pk = pv = table[p0];
+            } else {
+                const int ik = p0 + (n >> 2) * PT / 4, iv = p0 + g * PT / 4;
+                pk = ik < a.c.max_pages ? table[ik] : -1;
+                pv = iv < a.c.max_pages ? table[iv] : -1;
+            }
+            t.kin = pk >= 0 && pk < a.c.n_pages;
+            t.vin = pv >= 0 && pv < a.c.n_pages;
+            const int64_t hk_k = (int64_t)(t.kin ? pk : 0) * a.c.n_kv_heads + hk;
+            const int64_t hk_v = (int64_t)(t.vin ? pv : 0) * a.c.n_kv_heads + hk;
+            const uint8_t* kp = a.c.k + (hk_k * PE + (n >> 2) * 16 % PE + (n & 3)) * D + g * (D == 32 ? 8 : 16);
+            const uint8_t* vp = a.c.v + (hk_v * D + n) * PE + g * 16 % PE;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int c = 0; c < Tile<D>::KL; ++c) {
+                    if constexpr (D == 32) {
+                        const u32x2 x = *(const u32x2*)(kp + e * 4 * D);
+                        t.k[e][c] = u32x4{x[0], x[1], 0u, 0u};
+                    } else {
+                        t.k[e][c] = *(const u32x4*)(kp + e * 4 * D + c * 64);
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) t.v[j] = *(const u32x4*)(vp + j * 16 * PE);
+            t.ks = a.c.k_scale[hk_k];
+            t.vs = a.c.v_scale[hk_v];
+        };
+        const float to2 = a.scale * 1.44269504088896341f;
+        auto use = [&](int i, Tile<D>& t) {
+            floatx4 s[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[e] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < Tile<D>::KL; ++c)
+#pragma unroll
+                    for (int u = 0; u < (D == 32 ? 1 : 2); ++u) {
+                        const bf16x8 kk = decode8(t.k[e][c][2 * u], t.k[e][c][2 * u + 1], t.ks);
+#pragma unroll
+                        for (int x = 0; x < NQ; ++x)
+                            s[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[2 * c + u][x], s[e], 0, 0, 0);
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] *= to2;
+            // events of the tile's ends, and of pages that are not there, leave: score -inf, codes 0
+            const int e0 = tile_of(i) * kTile;
+            unsigned seen = 0xffffu;                     // of the lane group's 16 events
+            const bool whole = (e0 >= sp.low || e0 + kTile <= sp.lead_events) && e0 + kTile <= sp.len;
+            if (!whole || __any(!t.vin)) {
+                seen = 0;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const int j = e0 + g * 16 + x;
+                    seen |= (t.vin && j < sp.len && (j >= sp.low || j < sp.lead_events)) ? 1u << x : 0u;
+                }
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    if (!(seen >> x & 1)) s[x >> 2][x & 3] = -INFINITY;
+                u32x4 keep;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const unsigned f = seen >> (4 * x) & 15u;
+                    keep[x] = (f & 1 ? 0xffu : 0u) | (f & 2 ? 0xff00u : 0u) | (f & 4 ? 0xff0000u : 0u) |
+                              (f & 8 ? 0xff000000u : 0u);
+                }
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) t.v[j] &= keep;
+                t.vs = seen ? t.vs : 1.f;
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) top = fmaxf(top, s[x >> 2][x & 3]);
+            top = fmaxf(top, swizzle_xor16(top));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float mx = fmaxf(m, top);
+            const float ms = mx == -INFINITY ? 0.f : mx;
+            if (__any(mx > m)) {
+                const float alpha = __builtin_amdgcn_exp2f(m - ms);
+                l *= alpha;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) o[j] *= alpha;
+                m = mx;
+            }
+            float p[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                p[x] = __builtin_amdgcn_exp2f(s[x >> 2][x & 3] - ms);
+                l += p[x];
+            }
+            bf16x8 pp[2][NP];
+            split8<NP>(p, pp[0]);
+            split8<NP>(p + 8, pp[1]);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bf16x8 vv = decode8(t.v[j][2 * h], t.v[j][2 * h + 1], t.vs);
+#pragma unroll
+                    for (int x = 0; x < NP; ++x)
+                        o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pp[h][x], o[j], 0, 0, 0);
+                }
+        };
+
+        Tile<D> cur, nxt;
+        load(i0, cur);
+        for (int i = i0; i < i1; ++i) {
+            if (i + 1 < i1) load(i + 1, nxt);
+            use(i, cur);
+            cur = nxt;
+        }
+        l += swizzle_xor16(l);
+        l += __shfl_xor(l, 32, 64);
+
+        if (i0 == 0 && i1 == sp.count) {
+            if (live) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                T* op = (T*)a.out + qrow * a.ld_out + (int64_t)qhead * D;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) op[16 * j + 4 * g + i] = (T)(l == 0.f ? 0.f : o[j][i] * inv);
+            }
+        } else if (n < cols) {
+            // a run cuts at most the history it begins in and the one it ends in
+            float* part = a.partial +
+                          (((int64_t)2 * w + (i0 == 0 ? 1 : 0)) * gridDim.y + blockIdx.y) * cols * (D + 2) + n * (D + 2);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[16 * j + 4 * g + i] = o[j][i];
+            if (g == 0) {
+                part[D] = m;
+                part[D + 1] = l;
+            }
+        }
+        at = start + i1;
+        start += sp.count;
+        ++b;
+    }
+}
+
+// Joins the runs that share a history: one block per (history, chunk of rows).
+template <int D, typename T>
+__global__ __launch_bounds__(256) void history_join_kernel(LookupArgs a, const int* __restrict__ meta) {
+    const int b = blockIdx.x;
+    const int group = a.n_heads / a.c.n_kv_heads, rows = a.queries * group;
+    const int chunks = (rows + 15) / 16;
+    const int hk = blockIdx.y / chunks, r0 = (blockIdx.y % chunks) * 16;
+    const int cols = rows < 16 ? rows : 16;
+    const int count = span_of(a, b).count;
+    const int start = count ? meta[b] : 0, per = meta[a.batch];
+    const int w0 = start / per, w1 = count ? (start + count - 1) / per : 0;
+    if (count && w0 == w1) return;                      // one wave had it all
+    for (int x = threadIdx.x; x < cols * D; x += 256) {
+        const int n = x / D, d = x % D;
+        if (r0 + n >= rows) break;
+        float m = -INFINITY, l = 0.f, o = 0.f;
+        if (count) {
+            for (int w = w0; w <= w1; ++w) {
+                const float* part = a.partial +
+                                    (((int64_t)2 * w + (w == w0 ? 1 : 0)) * gridDim.y + blockIdx.y) * cols * (D + 2) + n * (D + 2);
+                const float pm = part[D], pl = part[D + 1], po = part[d];
+                const float mx = fmaxf(m, pm), ms = mx == -INFINITY ? 0.f : mx;
+                const float f = __builtin_amdgcn_exp2f(m - ms), h = __builtin_amdgcn_exp2f(pm - ms);
+                l = l * f + pl * h;
+                o = o * f + po * h;
+                m = mx;
+            }
+        }
+        T* out = (T*)a.out + ((int64_t)b * a.queries + (r0 + n) / group) * a.ld_out +
+                 (int64_t)(hk * group + (r0 + n) % group) * D;
+        out[d] = (T)(l == 0.f ? 0.f : o / l);
+    }
+}
+
+// Waves for each chunk of rows of each kv head.
+static int waves_of(const dlrm_history_cache_t& c, int64_t batch, int queries, int n_heads) {
+    const int64_t rows = (int64_t)queries * (n_heads / c.n_kv_heads);
+    const int64_t hc = (rows + 15) / 16 * c.n_kv_heads;
+    const int64_t tiles = batch * (((int64_t)c.max_pages * c.page_events + kTile - 1) / kTile);
+    int64_t w = (kLookupWaves + hc - 1) / hc;
+    w = w < tiles ? w : tiles;
+    return (int)((w + 3) / 4 * 4);
+}
+
+static size_t meta_bytes(int64_t batch) { return ((size_t)(batch + 1) * sizeof(int) + 255) / 256 * 256; }
+
+size_t lookup_workspace_bytes(const dlrm_history_cache_t& c, int64_t batch, int queries, int n_heads) {
+    const int64_t rows = (int64_t)queries * (n_heads / c.n_kv_heads);
+    const int64_t hc = (rows + 15) / 16 * c.n_kv_heads, cols = rows < 16 ? rows : 16;
+    return meta_bytes(batch) +
+           (size_t)2 * waves_of(c, batch, queries, n_heads) * hc * cols * (c.head_dim + 2) * sizeof(float);
+}
+
+template <int D, int PE, typename T>
+static hipError_t launch_t(LookupArgs a, hipStream_t s) {
+    const int rows = a.queries * (a.n_heads / a.c.n_kv_heads);
+    const int hc = (rows + 15) / 16 * a.c.n_kv_heads;
+    const int waves = waves_of(a.c, a.batch, a.queries, a.n_heads);
+    int* meta = (int*)a.partial;
+    a.partial = (float*)((char*)a.partial + meta_bytes(a.batch));
+    hipLaunchKernelGGL((history_lookup_kernel<D, PE, T>), dim3(waves / 4, hc), dim3(256), 0, s, a, waves, meta);
+    hipLaunchKernelGGL((history_join_kernel<D, T>), dim3(a.batch, hc), dim3(256), 0, s, a, meta);
+    return hipGetLastError();
+}
+template <int D, int PE>
+static hipError_t launch_d(const LookupArgs& a, int dtype, hipStream_t s) {
+    if (dtype == DLRM_DTYPE_F32) return launch_t<D, PE, float>(a, s);
+    if (dtype == DLRM_DTYPE_BF16) return launch_t<D, PE, bf16>(a, s);
+    return launch_t<D, PE, f16>(a, s);
+}
+template <int PE>
+static hipError_t launch_p(const LookupArgs& a, int dtype, hipStream_t s) {
+    if (a.c.head_dim == 32) return launch_d<32, PE>(a, dtype, s);
+    if (a.c.head_dim == 64) return launch_d<64, PE>(a, dtype, s);
+    return launch_d<128, PE>(a, dtype, s);
+}
 
 hipError_t launch_history_lookup(const LookupArgs& a, int dtype, hipStream_t s) {
-    const dim3 grid((unsigned)(a.batch * a.queries), (unsigned)a.n_heads);
-    if (dtype == DLRM_DTYPE_F32) hipLaunchKernelGGL(history_lookup_kernel<float>, grid, dim3(64), 0, s, a);
-    else if (dtype == DLRM_DTYPE_BF16) hipLaunchKernelGGL(history_lookup_kernel<bf16>, grid, dim3(64), 0, s, a);
-    else hipLaunchKernelGGL(history_lookup_kernel<f16>, grid, dim3(64), 0, s, a);
-    return hipGetLastError();
+    if (a.c.page_events == 16) return launch_p<16>(a, dtype, s);
+    if (a.c.page_events == 32) return launch_p<32>(a, dtype, s);
+    return launch_p<64>(a, dtype, s);
 }
 
 }  // namespace dlrm
