@@ -6,82 +6,360 @@
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale <q_i, k_j> - m_i)
 // in one pass over the keys with the running maximum m and sum.  A row that
 // sees nothing gives zeros.
+//
+// One block takes 32 W rows of one history and head, one wave 32 of them, and
+// walks the tiles of BN keys that any of its rows sees: first those of the
+// sinks, then those of the window.  Both products run on the matrix cores
+// (32x32x16) with the rows as columns:
+//   S^T = K Q^T, O^T += V^T P^T.
+// A lane then holds one row's scores of half the tile's keys: the row's maximum
+// and sum are the lane's own and its partner's (lane ^ 32), and the scores are
+// the second product's operand as they are, in registers.  K and V pass through
+// LDS, shared by the block's waves; V is turned by the transposing LDS read.  The
+// next tile is on its way from memory while this one is worked on.
+//
+// fp32 tensors are multiplied as three bf16 parts each (rounded, so that the
+// parts hold all 24 bits), in the six products of parts that are not below
+// 2^-24 of the whole: 6/16 of the fp32 matrix instructions' time.  16-bit
+// tensors round the weights to their own type once, an error of the size of the
+// output's own rounding; maxima, sums and outputs are held in fp32.
 #include "history.h"
 
 namespace dlrm {
 
-// One wave per (event, head): lanes over 64 keys for the products, over the
-// head's elements for the weighted sum.
-template <typename T>
-__global__ __launch_bounds__(64) void history_attention_kernel(EncodeArgs a, int dim) {
-    __shared__ float qs[128];
-    __shared__ float ps[64];
-    const int lane = threadIdx.x;
-    const int64_t row = blockIdx.x;
-    const int h = blockIdx.y, hk = h / (a.n_heads / a.n_kv);
-    // the last history that begins at or before the row
-    int lo = 0, hi = a.batch - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (history_begin(a.offsets, a.idx32, mid, a.n_events) <= row) lo = mid;
-        else hi = mid - 1;
-    }
-    const int64_t begin = history_begin(a.offsets, a.idx32, lo, a.n_events);
-    if (begin > row) return;
-    const T* q = (const T*)a.q + row * a.ld_q + (int64_t)h * dim;
-    for (int d = lane; d < dim; d += 64) qs[d] = ld_f32(q + d);
-    __syncthreads();
-    const int64_t i = row - begin;
-    float m = -INFINITY, l = 0.f, acc[2] = {0.f, 0.f};
-    const int64_t first = i - a.window + 1 > 0 ? i - a.window + 1 : 0;
-    const int64_t lead = (a.sinks < first ? a.sinks : first + 0);
-    const int64_t lead_tiles = (lead + 63) / 64;
-    const int64_t tiles = lead_tiles + (i - first) / 64 + 1;
-    for (int64_t t = 0; t < tiles; ++t) {
-        const int64_t base = t < lead_tiles ? t * 64 : first + (t - lead_tiles) * 64;
-        const int64_t stop = t < lead_tiles ? lead : i + 1;
-        const int64_t j = base + lane;
-        bool seen = j < stop;
-        if (seen && a.padding) seen = a.padding[begin + j] == 0;
-        float s = -INFINITY;
-        if (seen) {
-            const T* k = (const T*)a.k + (begin + j) * a.ld_k + (int64_t)hk * dim;
-            float dot = 0.f;
-            for (int d = 0; d < dim; ++d) dot = fmaf(qs[d], ld_f32(k + d), dot);
-            s = dot * a.scale;
-        }
-        const float mt = fmaxf(m, wave_max(s));
-        if (mt == -INFINITY) continue;
-        const float p = seen ? __expf(s - mt) : 0.f;
-        const float alpha = __expf(m - mt);
-        l = l * alpha + wave_sum(p);
-        m = mt;
-        __syncthreads();
-        ps[lane] = seen ? p : -1.f;
-        __syncthreads();
-        for (int c = 0; c < 2; ++c) {
-            const int d = lane + c * 64;
-            if (d >= dim) continue;
-            float o = acc[c] * alpha;
-            for (int x = 0; x < 64; ++x)
-                if (ps[x] >= 0.f || ps[x] != ps[x])
-                    o = fmaf(ps[x], ld_f32((const T*)a.v + (begin + base + x) * a.ld_v + (int64_t)hk * dim + d), o);
-            acc[c] = o;
-        }
-    }
-    T* out = (T*)a.out + row * a.ld_out + (int64_t)h * dim;
-    for (int c = 0; c < 2; ++c) {
-        const int d = lane + c * 64;
-        if (d < dim) out[d] = (T)(l == 0.f ? 0.f : acc[c] / l);
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+typedef short shortx8 __attribute__((ext_vector_type(8)));
+
+// How a type is multiplied: as `parts` values of `part` each.
+template <typename T> struct Mul;
+template <> struct Mul<bf16> { typedef bf16 part; static constexpr int parts = 1; };
+template <> struct Mul<f16> { typedef f16 part; static constexpr int parts = 1; };
+template <> struct Mul<float> { typedef bf16 part; static constexpr int parts = 3; };
+
+__device__ __forceinline__ floatx16 mfma(shortx8 a, shortx8 b, floatx16 c, bf16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+__device__ __forceinline__ floatx16 mfma(shortx8 a, shortx8 b, floatx16 c, f16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+
+// Sum of the products of parts: all pairs whose product can matter.
+template <typename E, int N>
+__device__ __forceinline__ floatx16 mul_parts(const shortx8* a, const shortx8* b, floatx16 c) {
+    if constexpr (N == 1) {
+        return mfma(a[0], b[0], c, E{});
+    } else {
+        c = mfma(a[0], b[2], c, E{});
+        c = mfma(a[1], b[1], c, E{});
+        c = mfma(a[2], b[0], c, E{});
+        c = mfma(a[0], b[1], c, E{});
+        c = mfma(a[1], b[0], c, E{});
+        return mfma(a[0], b[0], c, E{});
     }
 }
 
-hipError_t launch_history_attention(const EncodeArgs& a, int dtype, int dim, hipStream_t s) {
-    const dim3 grid((unsigned)a.n_events, (unsigned)a.n_heads);
-    if (dtype == DLRM_DTYPE_F32) hipLaunchKernelGGL(history_attention_kernel<float>, grid, dim3(64), 0, s, a, dim);
-    else if (dtype == DLRM_DTYPE_BF16) hipLaunchKernelGGL(history_attention_kernel<bf16>, grid, dim3(64), 0, s, a, dim);
-    else hipLaunchKernelGGL(history_attention_kernel<f16>, grid, dim3(64), 0, s, a, dim);
+// Eight fp32 values as N vectors of parts, the first the rounded values, each
+// next one the rounded rest.
+template <typename E, int N>
+__device__ __forceinline__ void split8(const float* x, shortx8* part) {
+    typedef E Ex8 __attribute__((ext_vector_type(8)));
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        Ex8 e;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            e[i] = (E)r[i];
+            if (n + 1 < N) r[i] -= (float)e[i];
+        }
+        part[n] = __builtin_bit_cast(shortx8, e);
+    }
+}
+
+// Eight consecutive elements of a row, as they are in memory.
+template <typename T>
+struct Raw {
+    T x[8];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p, bool wide) {
+    Raw<T> r;
+    if (wide) {
+        typedef T v __attribute__((ext_vector_type(16 / sizeof(T))));
+#pragma unroll
+        for (int c = 0; c < (int)sizeof(T) / 2; ++c) {
+            const v t = *(const v*)(p + c * (16 / sizeof(T)));
+#pragma unroll
+            for (int i = 0; i < 16 / (int)sizeof(T); ++i) r.x[c * (16 / sizeof(T)) + i] = t[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.x[i] = p[i];
+    }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void to_parts(const Raw<T>& r, shortx8* part) {
+    if constexpr (Mul<T>::parts == 1) {
+        part[0] = __builtin_bit_cast(shortx8, r);
+    } else {
+        split8<bf16, 3>(r.x, part);
+    }
+}
+template <typename T>
+__device__ __forceinline__ bool finite_bits(T x) {
+    if constexpr (sizeof(T) == 4) return (__builtin_bit_cast(unsigned, x) & 0x7f800000u) != 0x7f800000u;
+    const unsigned short all = sizeof(T) == 2 && __is_same(T, f16) ? 0x7c00 : 0x7f80;
+    if constexpr (sizeof(T) == 2) return (__builtin_bit_cast(unsigned short, x) & all) != all;
+    return true;
+}
+
+// Four keys of 16 columns, turned: lane j of a group of 16 points at key
+// j / 4, columns 4 (j % 4) .. + 3, and receives column j of the four keys.
+__device__ __forceinline__ shortx4 read_turned(const void* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) shortx4*)(__attribute__((address_space(3))) void*)p);
+}
+
+template <typename T, int D, int W, int BN>
+__global__ __launch_bounds__(64 * W) void history_attention_kernel(EncodeArgs a, int wide) {
+    typedef typename Mul<T>::part E;
+    constexpr int N = Mul<T>::parts;
+    constexpr int BM = 32 * W, THREADS = 64 * W;
+    constexpr int KP = D + 8;                       // row strides in LDS: 16-byte reads of 8 rows, and the turned
+    constexpr int VP = D == 32 ? D : D + 32;        // reads of 4 rows, touch every bank once
+    constexpr int VEC = (BN * D / 8 + THREADS - 1) / THREADS;
+    static_assert(BN * D / 8 % THREADS == 0, "whole vectors per thread");
+    __shared__ __attribute__((aligned(16))) E ks[N][BN][KP];
+    __shared__ __attribute__((aligned(16))) E vs[N][BN][VP];
+    __shared__ int odd[2];                          // the values of even / odd tiles hold an infinity or NaN
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 31, h = lane >> 5;
+    const int head = blockIdx.y, hk = head / (a.n_heads / a.n_kv);
+    int64_t nth;
+    // the longest rows first: a history's last tiles see the most keys
+    const int64_t unit = (int64_t)gridDim.x - 1 - blockIdx.x;
+    const int b = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, BM, 1, unit, &nth);
+    const int64_t begin = history_begin(a.offsets, a.idx32, b, a.n_events);
+    const int len = (int)(history_end(a.offsets, a.idx32, b, a.batch, begin, a.n_events) - begin);
+    if (nth < 0 || nth * BM >= len) return;
+    const int q0 = (int)nth * BM, r0 = q0 + wave * 32, row = r0 + n;
+    const int last = q0 + BM < len ? q0 + BM - 1 : len - 1;
+    const int window = (int)a.window, sinks = (int)a.sinks;
+    const T* kg = (const T*)a.k + begin * a.ld_k + (int64_t)hk * D;
+    const T* vg = (const T*)a.v + begin * a.ld_v + (int64_t)hk * D;
+    const uint8_t* pad = a.padding ? a.padding + begin : nullptr;
+
+    // tiles of keys: `lead` of the sinks, then from `first` on
+    int low = q0 >= window ? q0 - window + 1 : 0;
+    if (sinks >= low) low = 0;
+    const int first = low / BN;
+    int lead = low ? (sinks + BN - 1) / BN : 0;
+    lead = lead < first ? lead : first;
+    const int tiles = lead + last / BN + 1 - first;
+    auto key_of = [&](int t) { return (t < lead ? t : first + t - lead) * BN; };
+
+    // the row's elements 16 s + 8 h .. + 7; a negative scale turns their sign, so that scores only grow by it
+    shortx8 q[D / 16][N];
+    {
+        const T* qp = (const T*)a.q + (begin + row) * a.ld_q + (int64_t)head * D;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+            Raw<T> r = {};
+            if (row < len) r = load_raw(qp + 16 * s + 8 * h, wide);
+            if (a.scale < 0.f) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r.x[i] = -r.x[i];
+            }
+            to_parts(r, q[s]);
+        }
+    }
+    // exp(scale s) = 2^(c s); a scale of 0 is a c that leaves every finite score's weight at 1
+    const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-37f);
+
+    Raw<T> kr[VEC], vr[VEC];
+    unsigned long long hidden = 0;                  // padding events of the tile
+    auto fetch = [&](int t) {
+        const int k0 = key_of(t);
+        if (pad) hidden = __ballot(lane < BN && k0 + lane < len && pad[k0 + lane < len ? k0 + lane : 0] != 0);
+#pragma unroll
+        for (int x = 0; x < VEC; ++x) {
+            const int p = tid + x * THREADS, key = p / (D / 8), d = p % (D / 8) * 8;
+            kr[x] = vr[x] = Raw<T>{};
+            if (k0 + key < len) {
+                kr[x] = load_raw(kg + (int64_t)(k0 + key) * a.ld_k + d, wide);
+                vr[x] = load_raw(vg + (int64_t)(k0 + key) * a.ld_v + d, wide);
+            }
+        }
+    };
+
+    floatx16 o[D / 32];
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) o[j] = floatx16{};
+    float m = -INFINITY, l = 0.f;
+
+    fetch(0);
+    if (tid == 0) odd[0] = 0;
+    for (int t = 0; t < tiles; ++t) {
+        const int k0 = key_of(t);
+        const unsigned long long hide = hidden;
+        __syncthreads();                            // the tile before has been read
+        if (tid == 0) odd[(t + 1) & 1] = 0;
+        bool bad = false;
+#pragma unroll
+        for (int x = 0; x < VEC; ++x) {
+            const int p = tid + x * THREADS, key = p / (D / 8), d = p % (D / 8) * 8;
+            shortx8 kp[N], vp[N];
+            to_parts(kr[x], kp);
+            to_parts(vr[x], vp);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bad |= !finite_bits(vr[x].x[i]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                *(shortx8*)&ks[i][key][d] = kp[i];
+                *(shortx8*)&vs[i][key][d] = vp[i];
+            }
+        }
+        if (bad) odd[t & 1] = 1;
+        __syncthreads();
+        if (t + 1 < tiles) fetch(t + 1);
+        const bool fix = odd[t & 1] != 0;
+        if (fix) {
+            // such values are taken out of the products and added to the rows that see them
+            for (int p = tid; p < BN * D; p += THREADS)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (!finite_bits(vs[i][p / D][p % D])) vs[i][p / D][p % D] = (E)0.f;
+            __syncthreads();
+        }
+        if (k0 > r0 + 31 || (r0 - (k0 + BN - 1) >= window && k0 >= sinks)) continue;   // no row of the wave sees it
+        const bool whole = k0 + BN - 1 <= r0 && (r0 + 31 - k0 < window || k0 + BN <= sinks) && hide == 0;
+
+        floatx16 s[BN / 32];
+#pragma unroll
+        for (int u = 0; u < BN / 32; ++u) {
+            s[u] = floatx16{};
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+                shortx8 kk[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) kk[i] = *(const shortx8*)&ks[i][u * 32 + n][16 * x + 8 * h];
+                s[u] = mul_parts<E, N>(kk, q[x], s[u]);
+            }
+        }
+        auto sees = [&](int key) {
+            return key <= row && (row - key < window || key < sinks) && !(hide >> (key - k0) & 1);
+        };
+        if (!whole) {
+#pragma unroll
+            for (int u = 0; u < BN / 32; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!sees(k0 + u * 32 + 8 * (i >> 2) + 4 * h + (i & 3))) s[u][i] = -INFINITY;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < BN / 32; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        if (__any(top > m)) {
+            const float mx = fmaxf(m, top);
+            const float alpha = mx == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mx) * c);
+            l *= alpha;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) o[j] *= alpha;
+            m = mx;
+        }
+        const float mc = m == -INFINITY ? 0.f : m * c;
+#pragma unroll
+        for (int u = 0; u < BN / 32; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = __builtin_amdgcn_exp2f(fmaf(s[u][8 * e + i], c, -mc));
+                    l += p[i];
+                }
+                shortx8 pp[N];
+                split8<E, N>(p, pp);
+                // keys 16 e + 4 h + {0..3} and + 8 of this half: the lane's own scores
+                const int key = u * 32 + 16 * e + 4 * h + (n >> 2 & 3), col = 16 * (lane >> 4 & 1) + 4 * (n & 3);
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+                    shortx8 vv[N];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const shortx4 v0 = read_turned(&vs[i][key][32 * j + col]);
+                        const shortx4 v1 = read_turned(&vs[i][key + 8][32 * j + col]);
+                        vv[i] = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+                    }
+                    o[j] = mul_parts<E, N>(vv, pp, o[j]);
+                }
+            }
+        if (fix) {
+            for (int key = k0; key < k0 + BN && key < len; ++key)
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const T v = vg[(int64_t)key * a.ld_v + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3)];
+                        if (!finite_bits(v) && sees(key)) o[j][i] += (float)v;
+                    }
+        }
+    }
+    l += __shfl_xor(l, 32, 64);
+    if (row < len) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        T* op = (T*)a.out + (begin + row) * a.ld_out + (int64_t)head * D;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                op[32 * j + 8 * (i >> 2) + 4 * h + (i & 3)] = (T)(l == 0.f ? 0.f : o[j][i] * inv);
+    }
+}
+
+template <typename T, int D, int W>
+static hipError_t launch_w(const EncodeArgs& a, int wide, hipStream_t s) {
+    constexpr int BN = sizeof(T) == 4 && D == 128 ? 32 : 64;
+    const dim3 grid((unsigned)(a.n_events / (32 * W) + a.batch), (unsigned)a.n_heads);
+    hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN>), grid, dim3(64 * W), 0, s, a, wide);
     return hipGetLastError();
+}
+template <typename T, int D>
+static hipError_t launch_d(const EncodeArgs& a, int wide, hipStream_t s) {
+    const int64_t mean = a.n_events / a.batch;
+    if (mean <= 32) return launch_w<T, D, 1>(a, wide, s);
+    if (mean <= 96) return launch_w<T, D, 2>(a, wide, s);
+    return launch_w<T, D, 4>(a, wide, s);
+}
+template <typename T>
+static hipError_t launch_t(const EncodeArgs& a, int dim, hipStream_t s) {
+    const int64_t step = 16 / sizeof(T);
+    const int wide = a.ld_q % step == 0 && a.ld_k % step == 0 && a.ld_v % step == 0 &&
+                     (((uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v) & 15u) == 0;
+    if (dim == 32) return launch_d<T, 32>(a, wide, s);
+    if (dim == 64) return launch_d<T, 64>(a, wide, s);
+    return launch_d<T, 128>(a, wide, s);
+}
+
+hipError_t launch_history_attention(const EncodeArgs& args, int dtype, int dim, hipStream_t s) {
+    EncodeArgs a = args;
+    const int64_t most = (int64_t)1 << 30;      // no history is longer
+    a.window = a.window < most ? a.window : most;
+    a.sinks = a.sinks < most ? a.sinks : most;
+    if (dtype == DLRM_DTYPE_F32) return launch_t<float>(a, dim, s);
+    if (dtype == DLRM_DTYPE_BF16) return launch_t<bf16>(a, dim, s);
+    return launch_t<f16>(a, dim, s);
 }
 
 }  // namespace dlrm
