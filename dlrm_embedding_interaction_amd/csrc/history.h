@@ -89,16 +89,27 @@ __device__ __forceinline__ int64_t history_end(const void* off, int idx32, int64
 // has to be summed over the batch: with extra = 1 there is room for
 // ceil(len / width) units, with extra = 2 for the pages an append of len events
 // can touch.  Returns the history and u's number within it.
+// Called by whole waves: each step reads 64 offsets at once and narrows the
+// batch 64-fold, so that 4096 histories take two round trips.
 __device__ __forceinline__ int history_of_unit(const void* off, int idx32, int batch, int64_t n, int width,
                                                int extra, int64_t u, int64_t* nth) {
-    int lo = 0, hi = batch - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (history_begin(off, idx32, mid, n) / width + (int64_t)extra * mid <= u) lo = mid;
-        else hi = mid - 1;
+    const int lane = threadIdx.x & 63, sh = 31 - __builtin_clz(width);      // a power of two
+    int lo = 0, left = batch;
+    int64_t start = 0;
+    while (left > 0) {
+        const int step = (left + 63) / 64, at = lo + lane * step;
+        const bool in = lane * step < left;
+        const int64_t s = (history_begin(off, idx32, in ? at : lo, n) >> sh) + (int64_t)extra * at;
+        const int k = __popcll(__ballot(in && s <= u));                       // lanes 0 .. k - 1
+        const int last = k ? k - 1 : 0;
+        start = __shfl(s, last, 64);
+        const int rest = left - last * step;
+        lo += last * step;
+        if (step == 1) break;
+        left = rest < step ? rest : step;
     }
-    *nth = u - (history_begin(off, idx32, lo, n) / width + (int64_t)extra * lo);
-    return lo;
+    *nth = u - start;
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 __device__ __forceinline__ float wave_max(float v) {

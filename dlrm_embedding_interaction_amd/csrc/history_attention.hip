@@ -113,6 +113,32 @@ __device__ __forceinline__ void to_parts(const Raw<T>& r, shortx8* part) {
         split8<bf16, 3>(r.x, part);
     }
 }
+// The largest exponent field of eight elements, in place: infinities and NaN
+// have every bit of it set.
+template <typename T>
+__device__ __forceinline__ void top_exponent(const Raw<T>& r, unsigned& top) {
+    if constexpr (sizeof(T) == 2) {
+        typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+        typedef unsigned u4 __attribute__((ext_vector_type(4)));
+        const u4 w = __builtin_bit_cast(u4, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            top = __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(us2, top),
+                                                                         __builtin_bit_cast(us2, w[i] & 0x7fff7fffu)));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned w = __builtin_bit_cast(unsigned, r.x[i]) & 0x7fffffffu;
+            top = top > w ? top : w;
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ bool odd_exponent(unsigned top) {
+    if constexpr (sizeof(T) == 4) return top >= 0x7f800000u;
+    const unsigned all = __is_same(T, f16) ? 0x7c00u : 0x7f80u;
+    return (top & 0xffffu) >= all || top >> 16 >= all;
+}
 template <typename T>
 __device__ __forceinline__ bool finite_bits(T x) {
     if constexpr (sizeof(T) == 4) return (__builtin_bit_cast(unsigned, x) & 0x7f800000u) != 0x7f800000u;
@@ -129,20 +155,22 @@ __device__ __forceinline__ shortx4 read_turned(const void* p) {
 }
 
 template <typename T, int D, int W, int BN>
-__global__ __launch_bounds__(64 * W) void history_attention_kernel(EncodeArgs a, int wide) {
+__global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs a, int wide, int heads) {
     typedef typename Mul<T>::part E;
     constexpr int N = Mul<T>::parts;
-    constexpr int BM = 32 * W, THREADS = 64 * W;
+    constexpr int THREADS = 64 * W;
     constexpr int KP = D + 8;                       // row strides in LDS: 16-byte reads of 8 rows, and the turned
     constexpr int VP = D == 32 ? D : D + 32;        // reads of 4 rows, touch every bank once
     constexpr int VEC = (BN * D / 8 + THREADS - 1) / THREADS;
     static_assert(BN * D / 8 % THREADS == 0, "whole vectors per thread");
     __shared__ __attribute__((aligned(16))) E ks[N][BN][KP];
     __shared__ __attribute__((aligned(16))) E vs[N][BN][VP];
+    __shared__ __attribute__((aligned(16))) float hides[BN];   // 0, or -inf for a padding event
     __shared__ int odd[2];                          // the values of even / odd tiles hold an infinity or NaN
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 31, h = lane >> 5;
-    const int head = blockIdx.y, hk = head / (a.n_heads / a.n_kv);
+    const int BM = 32 * W / heads;
+    const int head = blockIdx.y * heads + wave % heads, hk = head / (a.n_heads / a.n_kv);
     int64_t nth;
     // the longest rows first: a history's last tiles see the most keys
     const int64_t unit = (int64_t)gridDim.x - 1 - blockIdx.x;
@@ -150,7 +178,7 @@ __global__ __launch_bounds__(64 * W) void history_attention_kernel(EncodeArgs a,
     const int64_t begin = history_begin(a.offsets, a.idx32, b, a.n_events);
     const int len = (int)(history_end(a.offsets, a.idx32, b, a.batch, begin, a.n_events) - begin);
     if (nth < 0 || nth * BM >= len) return;
-    const int q0 = (int)nth * BM, r0 = q0 + wave * 32, row = r0 + n;
+    const int q0 = (int)nth * BM, r0 = q0 + wave / heads * 32, row = r0 + n;
     const int last = q0 + BM < len ? q0 + BM - 1 : len - 1;
     const int window = (int)a.window, sinks = (int)a.sinks;
     const T* kg = (const T*)a.k + begin * a.ld_k + (int64_t)hk * D;
@@ -185,15 +213,15 @@ __global__ __launch_bounds__(64 * W) void history_attention_kernel(EncodeArgs a,
     const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-37f);
 
     Raw<T> kr[VEC], vr[VEC];
-    unsigned long long hidden = 0;                  // padding events of the tile
+    float hide = 0.f;                               // of the tile's key `tid`
     auto fetch = [&](int t) {
         const int k0 = key_of(t);
-        if (pad) hidden = __ballot(lane < BN && k0 + lane < len && pad[k0 + lane < len ? k0 + lane : 0] != 0);
+        if (pad && tid < BN) hide = k0 + tid < len && pad[k0 + tid] != 0 ? -INFINITY : 0.f;
 #pragma unroll
         for (int x = 0; x < VEC; ++x) {
             const int p = tid + x * THREADS, key = p / (D / 8), d = p % (D / 8) * 8;
             kr[x] = vr[x] = Raw<T>{};
-            if (k0 + key < len) {
+            if (k0 + key < len && !(pad && pad[k0 + key])) {
                 kr[x] = load_raw(kg + (int64_t)(k0 + key) * a.ld_k + d, wide);
                 vr[x] = load_raw(vg + (int64_t)(k0 + key) * a.ld_v + d, wide);
             }
@@ -209,25 +237,24 @@ __global__ __launch_bounds__(64 * W) void history_attention_kernel(EncodeArgs a,
     if (tid == 0) odd[0] = 0;
     for (int t = 0; t < tiles; ++t) {
         const int k0 = key_of(t);
-        const unsigned long long hide = hidden;
         __syncthreads();                            // the tile before has been read
         if (tid == 0) odd[(t + 1) & 1] = 0;
-        bool bad = false;
+        unsigned big = 0;
 #pragma unroll
         for (int x = 0; x < VEC; ++x) {
             const int p = tid + x * THREADS, key = p / (D / 8), d = p % (D / 8) * 8;
             shortx8 kp[N], vp[N];
             to_parts(kr[x], kp);
             to_parts(vr[x], vp);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) bad |= !finite_bits(vr[x].x[i]);
+            top_exponent(vr[x], big);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 *(shortx8*)&ks[i][key][d] = kp[i];
                 *(shortx8*)&vs[i][key][d] = vp[i];
             }
         }
-        if (bad) odd[t & 1] = 1;
+        if (pad && tid < BN) hides[tid] = hide;
+        if (odd_exponent<T>(big)) odd[t & 1] = 1;
         __syncthreads();
         if (t + 1 < tiles) fetch(t + 1);
         const bool fix = odd[t & 1] != 0;
@@ -240,12 +267,20 @@ __global__ __launch_bounds__(64 * W) void history_attention_kernel(EncodeArgs a,
             __syncthreads();
         }
         if (k0 > r0 + 31 || (r0 - (k0 + BN - 1) >= window && k0 >= sinks)) continue;   // no row of the wave sees it
-        const bool whole = k0 + BN - 1 <= r0 && (r0 + 31 - k0 < window || k0 + BN <= sinks) && hide == 0;
+        const bool whole = k0 + BN - 1 <= r0 && (r0 + 31 - k0 < window || k0 + BN <= sinks);
 
         floatx16 s[BN / 32];
 #pragma unroll
         for (int u = 0; u < BN / 32; ++u) {
             s[u] = floatx16{};
+            if (pad) {                              // the sums start at -inf for padding events, whose keys are zeros
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const floatx4 z = *(const floatx4*)&hides[u * 32 + 8 * i + 4 * h];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) s[u][4 * i + y] = z[y];
+                }
+            }
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
                 shortx8 kk[N];
@@ -254,15 +289,17 @@ __global__ __launch_bounds__(64 * W) void history_attention_kernel(EncodeArgs a,
                 s[u] = mul_parts<E, N>(kk, q[x], s[u]);
             }
         }
-        auto sees = [&](int key) {
-            return key <= row && (row - key < window || key < sinks) && !(hide >> (key - k0) & 1);
-        };
+        // bit y of a row's mask: it sees key k0 + 32 u + 4 h + y
+        auto up_to = [](int y) { return y < 0 ? 0u : y > 30 ? ~0u : (2u << y) - 1u; };      // bits 0 .. y
         if (!whole) {
 #pragma unroll
-            for (int u = 0; u < BN / 32; ++u)
+            for (int u = 0; u < BN / 32; ++u) {
+                const int k1 = k0 + 32 * u + 4 * h;
+                const unsigned see = up_to(row - k1) & (~up_to(row - window - k1) | up_to(sinks - 1 - k1));
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (!sees(k0 + u * 32 + 8 * (i >> 2) + 4 * h + (i & 3))) s[u][i] = -INFINITY;
+                    s[u][i] = see >> (8 * (i >> 2) + (i & 3)) & 1 ? s[u][i] : -INFINITY;
+            }
         }
         float top = -INFINITY;
 #pragma unroll
@@ -312,7 +349,8 @@ __global__ __launch_bounds__(64 * W) void history_attention_kernel(EncodeArgs a,
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const T v = vg[(int64_t)key * a.ld_v + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3)];
-                        if (!finite_bits(v) && sees(key)) o[j][i] += (float)v;
+                        const bool sees = key <= row && (row - key < window || key < sinks) && !(pad && pad[key]);
+                        if (!finite_bits(v) && sees) o[j][i] += (float)v;
                     }
         }
     }
@@ -329,18 +367,24 @@ __global__ __launch_bounds__(64 * W) void history_attention_kernel(EncodeArgs a,
 }
 
 template <typename T, int D, int W>
-static hipError_t launch_w(const EncodeArgs& a, int wide, hipStream_t s) {
+static hipError_t launch_w(const EncodeArgs& a, int wide, int heads, hipStream_t s) {
     constexpr int BN = sizeof(T) == 4 && D == 128 ? 32 : 64;
-    const dim3 grid((unsigned)(a.n_events / (32 * W) + a.batch), (unsigned)a.n_heads);
-    hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN>), grid, dim3(64 * W), 0, s, a, wide);
+    const dim3 grid((unsigned)(a.n_events / (32 * W / heads) + a.batch), (unsigned)(a.n_heads / heads));
+    hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN>), grid, dim3(64 * W), 0, s, a, wide, heads);
     return hipGetLastError();
 }
 template <typename T, int D>
 static hipError_t launch_d(const EncodeArgs& a, int wide, hipStream_t s) {
     const int64_t mean = a.n_events / a.batch;
-    if (mean <= 32) return launch_w<T, D, 1>(a, wide, s);
-    if (mean <= 96) return launch_w<T, D, 2>(a, wide, s);
-    return launch_w<T, D, 4>(a, wide, s);
+    const int group = a.n_heads / a.n_kv;
+    const int heads = group % 4 == 0 ? 4 : (group % 2 == 0 ? 2 : 1);
+    const int rows = mean <= 32 ? 1 : (mean <= 96 ? 2 : 4);     // in 32s
+#if 1
+    if constexpr (D > 32) if (heads * rows >= 8) return launch_w<T, D, 8>(a, wide, heads, s);
+#endif
+    if (heads * rows >= 4) return launch_w<T, D, 4>(a, wide, heads, s);
+    if (heads * rows == 2) return launch_w<T, D, 2>(a, wide, heads, s);
+    return launch_w<T, D, 1>(a, wide, heads, s);
 }
 template <typename T>
 static hipError_t launch_t(const EncodeArgs& a, int dim, hipStream_t s) {
