@@ -88,10 +88,10 @@ template <typename T>
 struct Raw {
     T x[8];
 };
-template <typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T* p, bool wide) {
+template <bool WIDE, typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p) {
     Raw<T> r;
-    if (wide) {
+    if constexpr (WIDE) {
         typedef T v __attribute__((ext_vector_type(16 / sizeof(T))));
 #pragma unroll
         for (int c = 0; c < (int)sizeof(T) / 2; ++c) {
@@ -154,8 +154,19 @@ __device__ __forceinline__ shortx4 read_turned(const void* p) {
         (__attribute__((address_space(3))) shortx4*)(__attribute__((address_space(3))) void*)p);
 }
 
-template <typename T, int D, int W, int BN>
-__global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs a, int wide, int heads) {
+// The larger of a value and its partner's in lane ^ 32, and their sum.
+__device__ __forceinline__ float halves_max(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float halves_sum(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// WIDE: 16-byte loads.  PAD: padding bytes may be given.
+template <typename T, int D, int W, int BN, bool WIDE, bool PAD>
+__global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs a, int heads) {
     typedef typename Mul<T>::part E;
     constexpr int N = Mul<T>::parts;
     constexpr int THREADS = 64 * W;
@@ -183,7 +194,7 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
     const int window = (int)a.window, sinks = (int)a.sinks;
     const T* kg = (const T*)a.k + begin * a.ld_k + (int64_t)hk * D;
     const T* vg = (const T*)a.v + begin * a.ld_v + (int64_t)hk * D;
-    const uint8_t* pad = a.padding ? a.padding + begin : nullptr;
+    const uint8_t* pad = PAD && a.padding ? a.padding + begin : nullptr;
 
     // tiles of keys: `lead` of the sinks, then from `first` on
     int low = q0 >= window ? q0 - window + 1 : 0;
@@ -197,11 +208,10 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
     // the row's elements 16 s + 8 h .. + 7; a negative scale turns their sign, so that scores only grow by it
     shortx8 q[D / 16][N];
     {
-        const T* qp = (const T*)a.q + (begin + row) * a.ld_q + (int64_t)head * D;
+        const T* qp = (const T*)a.q + (begin + (row < len ? row : len - 1)) * a.ld_q + (int64_t)head * D;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-            Raw<T> r = {};
-            if (row < len) r = load_raw(qp + 16 * s + 8 * h, wide);
+            Raw<T> r = load_raw<WIDE>(qp + 16 * s + 8 * h);
             if (a.scale < 0.f) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) r.x[i] = -r.x[i];
@@ -214,17 +224,17 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
 
     Raw<T> kr[VEC], vr[VEC];
     float hide = 0.f;                               // of the tile's key `tid`
+    // Rows behind the history's end stand in as its last one: no row sees them.
     auto fetch = [&](int t) {
         const int k0 = key_of(t);
-        if (pad && tid < BN) hide = k0 + tid < len && pad[k0 + tid] != 0 ? -INFINITY : 0.f;
+        if (PAD && pad && tid < BN) hide = k0 + tid < len && pad[k0 + tid] != 0 ? -INFINITY : 0.f;
 #pragma unroll
         for (int x = 0; x < VEC; ++x) {
-            const int p = tid + x * THREADS, key = p / (D / 8), d = p % (D / 8) * 8;
-            kr[x] = vr[x] = Raw<T>{};
-            if (k0 + key < len && !(pad && pad[k0 + key])) {
-                kr[x] = load_raw(kg + (int64_t)(k0 + key) * a.ld_k + d, wide);
-                vr[x] = load_raw(vg + (int64_t)(k0 + key) * a.ld_v + d, wide);
-            }
+            const int p = tid + x * THREADS, d = p % (D / 8) * 8;
+            const int key = min(k0 + p / (D / 8), len - 1);
+            kr[x] = load_raw<WIDE>(kg + (int64_t)key * a.ld_k + d);
+            vr[x] = load_raw<WIDE>(vg + (int64_t)key * a.ld_v + d);
+            if (PAD && pad && pad[key] != 0) kr[x] = vr[x] = Raw<T>{};
         }
     };
 
@@ -253,7 +263,7 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
                 *(shortx8*)&vs[i][key][d] = vp[i];
             }
         }
-        if (pad && tid < BN) hides[tid] = hide;
+        if (PAD && pad && tid < BN) hides[tid] = hide;
         if (odd_exponent<T>(big)) odd[t & 1] = 1;
         __syncthreads();
         if (t + 1 < tiles) fetch(t + 1);
@@ -273,7 +283,7 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
 #pragma unroll
         for (int u = 0; u < BN / 32; ++u) {
             s[u] = floatx16{};
-            if (pad) {                              // the sums start at -inf for padding events, whose keys are zeros
+            if (PAD && pad) {                       // the sums start at -inf for padding events, whose keys are zeros
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const floatx4 z = *(const floatx4*)&hides[u * 32 + 8 * i + 4 * h];
@@ -306,8 +316,10 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
         for (int u = 0; u < BN / 32; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        if (__any(top > m)) {
+        top = halves_max(top);
+        // the maximum a row's weights are taken against may lag the true one by 2^8: weights then stay below
+        // that, far from the end of every type, and most tiles leave the sums as they are
+        if (__any((top - m) * c > 8.f)) {
             const float mx = fmaxf(m, top);
             const float alpha = mx == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mx) * c);
             l *= alpha;
@@ -354,7 +366,7 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
                     }
         }
     }
-    l += __shfl_xor(l, 32, 64);
+    l = halves_sum(l);
     if (row < len) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         T* op = (T*)a.out + (begin + row) * a.ld_out + (int64_t)head * D;
@@ -367,21 +379,24 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
 }
 
 template <typename T, int D, int W>
-static hipError_t launch_w(const EncodeArgs& a, int wide, int heads, hipStream_t s) {
+static hipError_t launch_w(const EncodeArgs& a, bool wide, int heads, hipStream_t s) {
     constexpr int BN = sizeof(T) == 4 && D == 128 ? 32 : 64;
     const dim3 grid((unsigned)(a.n_events / (32 * W / heads) + a.batch), (unsigned)(a.n_heads / heads));
-    hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN>), grid, dim3(64 * W), 0, s, a, wide, heads);
+    const dim3 block(64 * W);
+    if (!wide) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, false, true>), grid, block, 0, s, a, heads);
+    else if (a.padding) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, true>), grid, block, 0, s, a, heads);
+    else hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, false>), grid, block, 0, s, a, heads);
     return hipGetLastError();
 }
 template <typename T, int D>
-static hipError_t launch_d(const EncodeArgs& a, int wide, hipStream_t s) {
+static hipError_t launch_d(const EncodeArgs& a, bool wide, hipStream_t s) {
     const int64_t mean = a.n_events / a.batch;
     const int group = a.n_heads / a.n_kv;
     const int heads = group % 4 == 0 ? 4 : (group % 2 == 0 ? 2 : 1);
     const int rows = mean <= 32 ? 1 : (mean <= 96 ? 2 : 4);     // in 32s
-#if 1
-    if constexpr (D > 32) if (heads * rows >= 8) return launch_w<T, D, 8>(a, wide, heads, s);
-#endif
+    if constexpr (D > 32) {
+        if (heads * rows >= 8) return launch_w<T, D, 8>(a, wide, heads, s);
+    }
     if (heads * rows >= 4) return launch_w<T, D, 4>(a, wide, heads, s);
     if (heads * rows == 2) return launch_w<T, D, 2>(a, wide, heads, s);
     return launch_w<T, D, 1>(a, wide, heads, s);
@@ -389,8 +404,8 @@ static hipError_t launch_d(const EncodeArgs& a, int wide, hipStream_t s) {
 template <typename T>
 static hipError_t launch_t(const EncodeArgs& a, int dim, hipStream_t s) {
     const int64_t step = 16 / sizeof(T);
-    const int wide = a.ld_q % step == 0 && a.ld_k % step == 0 && a.ld_v % step == 0 &&
-                     (((uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v) & 15u) == 0;
+    const bool wide = a.ld_q % step == 0 && a.ld_k % step == 0 && a.ld_v % step == 0 &&
+                      (((uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v) & 15u) == 0;
     if (dim == 32) return launch_d<T, 32>(a, wide, s);
     if (dim == 64) return launch_d<T, 64>(a, wide, s);
     return launch_d<T, 128>(a, wide, s);
