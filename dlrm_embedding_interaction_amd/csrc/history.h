@@ -90,26 +90,38 @@ __device__ __forceinline__ int64_t history_end(const void* off, int idx32, int64
 // ceil(len / width) units, with extra = 2 for the pages an append of len events
 // can touch.  Returns the history and u's number within it.
 // Called by whole waves: each step reads 64 offsets at once and narrows the
-// batch 64-fold, so that 4096 histories take two round trips.
-__device__ __forceinline__ int history_of_unit(const void* off, int idx32, int batch, int64_t n, int width,
-                                               int extra, int64_t u, int64_t* nth) {
+// batch 64-fold, so that 4096 histories take two round trips; the last one
+// holds the bounds of the history, too.
+struct Unit {
+    int b;                  // history
+    int64_t nth;            // number of the unit within it; below 0: no one's
+    int64_t begin, end;     // the history's rows
+};
+__device__ __forceinline__ Unit history_of_unit(const void* off, int idx32, int batch, int64_t n, int width,
+                                                int extra, int64_t u) {
     const int lane = threadIdx.x & 63, sh = 31 - __builtin_clz(width);      // a power of two
     int lo = 0, left = batch;
-    int64_t start = 0;
-    while (left > 0) {
+    Unit r;
+    while (true) {
         const int step = (left + 63) / 64, at = lo + lane * step;
         const bool in = lane * step < left;
-        const int64_t s = (history_begin(off, idx32, in ? at : lo, n) >> sh) + (int64_t)extra * at;
+        const int64_t o = history_begin(off, idx32, in ? at : lo, n);
+        const int64_t s = (o >> sh) + (int64_t)extra * at;
         const int k = __popcll(__ballot(in && s <= u));                       // lanes 0 .. k - 1
-        const int last = k ? k - 1 : 0;
-        start = __shfl(s, last, 64);
-        const int rest = left - last * step;
+        const int last = __builtin_amdgcn_readfirstlane(k ? k - 1 : 0);
         lo += last * step;
-        if (step == 1) break;
+        if (step == 1) {
+            r.b = lo;
+            r.nth = u - __shfl(s, last, 64);
+            r.begin = __shfl(o, last, 64);
+            const int64_t next = __shfl(o, last < 63 ? last + 1 : 63, 64);
+            r.end = last < 63 && last + 1 < left ? (next < r.begin ? r.begin : next)
+                                                 : history_end(off, idx32, lo, batch, r.begin, n);
+            return r;
+        }
+        const int rest = left - last * step;
         left = rest < step ? rest : step;
     }
-    *nth = u - start;
-    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 __device__ __forceinline__ float wave_max(float v) {

@@ -164,9 +164,12 @@ __device__ __forceinline__ float halves_sum(float v) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+#ifndef MINW
+#define MINW (sizeof(T) == 4 ? 2 : D == 128 ? 2 : D == 64 ? 3 : 4)
+#endif
 // WIDE: 16-byte loads.  PAD: padding bytes may be given.
 template <typename T, int D, int W, int BN, bool WIDE, bool PAD>
-__global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs a, int heads) {
+__global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeArgs a, int heads) {
     typedef typename Mul<T>::part E;
     constexpr int N = Mul<T>::parts;
     constexpr int THREADS = 64 * W;
@@ -182,12 +185,11 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 31, h = lane >> 5;
     const int BM = 32 * W / heads;
     const int head = blockIdx.y * heads + wave % heads, hk = head / (a.n_heads / a.n_kv);
-    int64_t nth;
     // the longest rows first: a history's last tiles see the most keys
-    const int64_t unit = (int64_t)gridDim.x - 1 - blockIdx.x;
-    const int b = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, BM, 1, unit, &nth);
-    const int64_t begin = history_begin(a.offsets, a.idx32, b, a.n_events);
-    const int len = (int)(history_end(a.offsets, a.idx32, b, a.batch, begin, a.n_events) - begin);
+    const Unit un = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, BM, 1,
+                                    (int64_t)gridDim.x - 1 - blockIdx.x);
+    const int64_t nth = un.nth, begin = un.begin;
+    const int len = (int)(un.end - begin);
     if (nth < 0 || nth * BM >= len) return;
     const int q0 = (int)nth * BM, r0 = q0 + wave / heads * 32, row = r0 + n;
     const int last = q0 + BM < len ? q0 + BM - 1 : len - 1;
@@ -223,18 +225,19 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
     const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-37f);
 
     Raw<T> kr[VEC], vr[VEC];
-    float hide = 0.f;                               // of the tile's key `tid`
+    // padding bytes, as loaded (a comparison here would wait for the loads): of the tile's key `tid`, of the vectors
+    uint8_t hide = 0, gone[VEC] = {};
     // Rows behind the history's end stand in as its last one: no row sees them.
     auto fetch = [&](int t) {
         const int k0 = key_of(t);
-        if (PAD && pad && tid < BN) hide = k0 + tid < len && pad[k0 + tid] != 0 ? -INFINITY : 0.f;
+        if (PAD && pad && tid < BN) hide = pad[min(k0 + tid, len - 1)];
 #pragma unroll
         for (int x = 0; x < VEC; ++x) {
             const int p = tid + x * THREADS, d = p % (D / 8) * 8;
             const int key = min(k0 + p / (D / 8), len - 1);
             kr[x] = load_raw<WIDE>(kg + (int64_t)key * a.ld_k + d);
             vr[x] = load_raw<WIDE>(vg + (int64_t)key * a.ld_v + d);
-            if (PAD && pad && pad[key] != 0) kr[x] = vr[x] = Raw<T>{};
+            if (PAD && pad) gone[x] = pad[key];
         }
     };
 
@@ -254,6 +257,7 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
         for (int x = 0; x < VEC; ++x) {
             const int p = tid + x * THREADS, key = p / (D / 8), d = p % (D / 8) * 8;
             shortx8 kp[N], vp[N];
+            if (PAD && gone[x] != 0) kr[x] = vr[x] = Raw<T>{};
             to_parts(kr[x], kp);
             to_parts(vr[x], vp);
             top_exponent(vr[x], big);
@@ -263,7 +267,7 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
                 *(shortx8*)&vs[i][key][d] = vp[i];
             }
         }
-        if (PAD && pad && tid < BN) hides[tid] = hide;
+        if (PAD && pad && tid < BN) hides[tid] = hide != 0 ? -INFINITY : 0.f;
         if (odd_exponent<T>(big)) odd[t & 1] = 1;
         __syncthreads();
         if (t + 1 < tiles) fetch(t + 1);
@@ -276,19 +280,18 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
                     if (!finite_bits(vs[i][p / D][p % D])) vs[i][p / D][p % D] = (E)0.f;
             __syncthreads();
         }
-        if (k0 > r0 + 31 || (r0 - (k0 + BN - 1) >= window && k0 >= sinks)) continue;   // no row of the wave sees it
-        const bool whole = k0 + BN - 1 <= r0 && (r0 + 31 - k0 < window || k0 + BN <= sinks);
-
-        floatx16 s[BN / 32];
+        // 32 keys at a time, those that no row of the wave sees left out
 #pragma unroll
         for (int u = 0; u < BN / 32; ++u) {
-            s[u] = floatx16{};
+            const int k1 = k0 + 32 * u;
+            if (k1 > r0 + 31 || (r0 - (k1 + 31) >= window && k1 >= sinks)) continue;
+            floatx16 s = floatx16{};
             if (PAD && pad) {                       // the sums start at -inf for padding events, whose keys are zeros
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const floatx4 z = *(const floatx4*)&hides[u * 32 + 8 * i + 4 * h];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) s[u][4 * i + y] = z[y];
+                    for (int y = 0; y < 4; ++y) s[4 * i + y] = z[y];
                 }
             }
 #pragma unroll
@@ -296,46 +299,37 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
                 shortx8 kk[N];
 #pragma unroll
                 for (int i = 0; i < N; ++i) kk[i] = *(const shortx8*)&ks[i][u * 32 + n][16 * x + 8 * h];
-                s[u] = mul_parts<E, N>(kk, q[x], s[u]);
+                s = mul_parts<E, N>(kk, q[x], s);
             }
-        }
-        // bit y of a row's mask: it sees key k0 + 32 u + 4 h + y
-        auto up_to = [](int y) { return y < 0 ? 0u : y > 30 ? ~0u : (2u << y) - 1u; };      // bits 0 .. y
-        if (!whole) {
+            if (k1 + 31 > r0 || (r0 + 31 - k1 >= window && k1 + 32 > sinks)) {
+                // bit y: the row sees key k1 + 4 h + y
+                auto up_to = [](int y) { return y < 0 ? 0u : y > 30 ? ~0u : (2u << y) - 1u; };      // bits 0 .. y
+                const int k2 = k1 + 4 * h;
+                const unsigned see = up_to(row - k2) & (~up_to(row - window - k2) | up_to(sinks - 1 - k2));
 #pragma unroll
-            for (int u = 0; u < BN / 32; ++u) {
-                const int k1 = k0 + 32 * u + 4 * h;
-                const unsigned see = up_to(row - k1) & (~up_to(row - window - k1) | up_to(sinks - 1 - k1));
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[u][i] = see >> (8 * (i >> 2) + (i & 3)) & 1 ? s[u][i] : -INFINITY;
+                for (int i = 0; i < 16; ++i) s[i] = see >> (8 * (i >> 2) + (i & 3)) & 1 ? s[i] : -INFINITY;
             }
-        }
-        float top = -INFINITY;
+            float top = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < BN / 32; ++u)
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i]);
+            top = halves_max(top);
+            // the maximum a row's weights are taken against may lag the true one by 2^8: weights then stay below
+            // that, far from the end of every type, and most tiles leave the sums as they are
+            if (__any((top - m) * c > 8.f)) {
+                const float mx = fmaxf(m, top);
+                const float alpha = mx == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mx) * c);
+                l *= alpha;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-        top = halves_max(top);
-        // the maximum a row's weights are taken against may lag the true one by 2^8: weights then stay below
-        // that, far from the end of every type, and most tiles leave the sums as they are
-        if (__any((top - m) * c > 8.f)) {
-            const float mx = fmaxf(m, top);
-            const float alpha = mx == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mx) * c);
-            l *= alpha;
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) o[j] *= alpha;
-            m = mx;
-        }
-        const float mc = m == -INFINITY ? 0.f : m * c;
-#pragma unroll
-        for (int u = 0; u < BN / 32; ++u)
+                for (int j = 0; j < D / 32; ++j) o[j] *= alpha;
+                m = mx;
+            }
+            const float mc = m == -INFINITY ? 0.f : m * c;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float p[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    p[i] = __builtin_amdgcn_exp2f(fmaf(s[u][8 * e + i], c, -mc));
+                    p[i] = __builtin_amdgcn_exp2f(fmaf(s[8 * e + i], c, -mc));
                     l += p[i];
                 }
                 shortx8 pp[N];
@@ -354,6 +348,7 @@ __global__ __launch_bounds__(64 * W, 2) void history_attention_kernel(EncodeArgs
                     o[j] = mul_parts<E, N>(vv, pp, o[j]);
                 }
             }
+        }
         if (fix) {
             for (int key = k0; key < k0 + BN && key < len; ++key)
 #pragma unroll

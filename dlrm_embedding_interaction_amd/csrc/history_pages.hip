@@ -145,11 +145,10 @@ __global__ __launch_bounds__(256) void history_append_kernel(AppendArgs a, int w
     __shared__ float wmax[4];
     const int pe = c.page_events, dim = c.head_dim, hk = blockIdx.y, tid = threadIdx.x;
     const bool minor = blockIdx.z != 0;
-    int64_t nth;
-    const int b = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, pe, 2, blockIdx.x, &nth);
+    const Unit un = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, pe, 2, blockIdx.x);
+    const int b = un.b;
+    const int64_t nth = un.nth, begin = un.begin, count = un.end - un.begin;
     const Grant g = a.grants[b];
-    const int64_t begin = history_begin(a.offsets, a.idx32, b, a.n_events);
-    const int64_t count = history_end(a.offsets, a.idx32, b, a.batch, begin, a.n_events) - begin;
     if (g.old_len < 0 || count == 0) return;
     const int slot = a.slots ? a.slots[b] : b;
     const int64_t first = g.old_len / pe, page_no = first + nth, stop = g.old_len + count;
