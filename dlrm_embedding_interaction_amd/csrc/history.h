@@ -12,7 +12,7 @@
 namespace dlrm {
 
 constexpr int kScaleFloor = -100;    // smallest exponent of a page's power-of-two scale
-constexpr int kRebuildChunk = 4096;  // pages per block of the free-list rebuild
+constexpr int kRebuildChunk = 4096;  // pages per block of the free-list work on large pools
 
 typedef __bf16 bf16;
 typedef _Float16 f16;
@@ -131,12 +131,28 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 __device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
 
-// One element of T as fp32 and back (round to nearest even).
+// Eight consecutive elements of a row, as they are in memory.
 template <typename T>
-__device__ __forceinline__ float ld_f32(const T* p) {
-    return (float)*p;
+struct Raw {
+    T x[8];
+};
+template <bool WIDE, typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p) {
+    Raw<T> r;
+    if constexpr (WIDE) {
+        typedef T v __attribute__((ext_vector_type(16 / sizeof(T))));
+#pragma unroll
+        for (int c = 0; c < (int)sizeof(T) / 2; ++c) {
+            const v t = *(const v*)(p + c * (16 / sizeof(T)));
+#pragma unroll
+            for (int i = 0; i < 16 / (int)sizeof(T); ++i) r.x[c * (16 / sizeof(T)) + i] = t[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.x[i] = p[i];
+    }
+    return r;
 }
-
 // e4m3 codes: two floats to two codes in the low half, and one code to fp32.
 __device__ __forceinline__ unsigned pk_e4m3(float a, float b) {
     return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xffffu;

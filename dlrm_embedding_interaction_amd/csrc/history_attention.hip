@@ -83,28 +83,6 @@ __device__ __forceinline__ void split8(const float* x, shortx8* part) {
     }
 }
 
-// Eight consecutive elements of a row, as they are in memory.
-template <typename T>
-struct Raw {
-    T x[8];
-};
-template <bool WIDE, typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T* p) {
-    Raw<T> r;
-    if constexpr (WIDE) {
-        typedef T v __attribute__((ext_vector_type(16 / sizeof(T))));
-#pragma unroll
-        for (int c = 0; c < (int)sizeof(T) / 2; ++c) {
-            const v t = *(const v*)(p + c * (16 / sizeof(T)));
-#pragma unroll
-            for (int i = 0; i < 16 / (int)sizeof(T); ++i) r.x[c * (16 / sizeof(T)) + i] = t[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r.x[i] = p[i];
-    }
-    return r;
-}
 template <typename T>
 __device__ __forceinline__ void to_parts(const Raw<T>& r, shortx8* part) {
     if constexpr (Mul<T>::parts == 1) {

@@ -11,7 +11,7 @@
 
 namespace dlrm {
 
-constexpr int kOneBlockPages = 16384;  // free-list work of one block: 1024 threads x 16 pages
+constexpr int kOneBlockPages = 65536;  // pools up to here have their free list written by one block
 
 // Exclusive sum of v over the block's threads in order; *total over all.
 template <int THREADS>
@@ -55,49 +55,68 @@ __global__ __launch_bounds__(256) void history_init_kernel(dlrm_history_cache_t 
 // its events open, and one more where its last page is part filled and shared.
 // Needs are summed in batch order; a history whose sum passes the free count is
 // refused whole.  Nothing here changes refs or the table, so that every history
-// of the call sees them as they were before it.
+// of the call sees them as they were before it.  What it takes is the chain
+// slot -> length -> page -> holders of dependent reads: four histories per thread
+// go through it together.
 __global__ __launch_bounds__(1024) void history_reserve_kernel(AppendArgs a) {
+    constexpr int PER = 4;
     const dlrm_history_cache_t& c = a.c;
     __shared__ int refused, taken;
     if (threadIdx.x == 0) refused = taken = 0;
     __syncthreads();
     const int n_free = c.counters[0], pe = c.page_events;
     int carry = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 1024) {
-        const int b = b0 + threadIdx.x;
-        int need = 0, src = -1, copy = 0, slot = -1;
-        int64_t old = 0, count = 0;
-        bool ok = false;
-        if (b < a.batch) {
-            slot = a.slots ? a.slots[b] : b;
-            const int64_t begin = history_begin(a.offsets, a.idx32, b, a.n_events);
-            count = history_end(a.offsets, a.idx32, b, a.batch, begin, a.n_events) - begin;
-            if (slot >= 0 && slot < c.n_slots) {
-                old = c.lens[slot];
-                ok = old >= 0 && old + count <= (int64_t)c.max_pages * pe;
-            }
-            if (ok && count > 0) {
-                const int part = (int)(old % pe);
-                if (part) {
-                    src = c.table[(int64_t)slot * c.max_pages + old / pe];
-                    ok = src >= 0 && src < c.n_pages;
-                    copy = ok && c.refs[src] > 1;
-                }
-                if (ok) need = (int)((old + count + pe - 1) / pe - (old + pe - 1) / pe) + copy;
-            }
+    for (int b0 = 0; b0 < a.batch; b0 += 1024 * PER) {
+        int need[PER], src[PER], copy[PER], slot[PER], sum = 0;
+        int64_t old[PER], count[PER], begin[PER], end[PER];
+        bool ok[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int b = b0 + threadIdx.x * PER + i;
+            slot[i] = b < a.batch ? (a.slots ? a.slots[b] : b) : -1;
+            begin[i] = b < a.batch ? history_begin(a.offsets, a.idx32, b, a.n_events) : 0;
+            end[i] = b + 1 < a.batch ? ld_index(a.offsets, b + 1, a.idx32) : a.n_events;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            end[i] = end[i] < begin[i] ? begin[i] : (end[i] > a.n_events ? a.n_events : end[i]);
+            count[i] = end[i] - begin[i];
+            ok[i] = slot[i] >= 0 && slot[i] < c.n_slots;
+            old[i] = ok[i] ? c.lens[slot[i]] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            ok[i] = ok[i] && old[i] >= 0 && old[i] + count[i] <= (int64_t)c.max_pages * pe;
+            src[i] = -1;
+            if (ok[i] && count[i] > 0 && old[i] % pe) src[i] = c.table[(int64_t)slot[i] * c.max_pages + old[i] / pe];
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (ok[i] && count[i] > 0 && old[i] % pe) ok[i] = src[i] >= 0 && src[i] < c.n_pages;
+            copy[i] = ok[i] && src[i] >= 0 && c.refs[src[i]] > 1;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            need[i] = ok[i] && count[i] > 0 ? (int)((old[i] + count[i] + pe - 1) / pe - (old[i] + pe - 1) / pe) + copy[i] : 0;
+            sum += need[i];
         }
         int total;
-        const int before = carry + block_exclusive<1024>(need, &total);
+        int before = carry + block_exclusive<1024>(sum, &total);
         carry += total;
-        if (b < a.batch) {
-            ok = ok && (need == 0 || before + need <= n_free);
-            a.grants[b] = Grant{ok ? (int)old : -1, n_free - 1 - before, src, copy};
-            if (ok) {
-                c.lens[slot] = (int)(old + count);
-                if (need) atomicMax(&taken, before + need);
-            } else {
-                atomicAdd(&refused, 1);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int b = b0 + threadIdx.x * PER + i;
+            if (b < a.batch) {
+                const bool granted = ok[i] && (need[i] == 0 || before + need[i] <= n_free);
+                a.grants[b] = Grant{granted ? (int)old[i] : -1, n_free - 1 - before, src[i], copy[i]};
+                if (granted) {
+                    if (count[i] > 0) c.lens[slot[i]] = (int)(old[i] + count[i]);
+                    if (need[i]) atomicMax(&taken, before + need[i]);
+                } else {
+                    atomicAdd(&refused, 1);
+                }
             }
+            before += need[i];
         }
     }
     __syncthreads();
@@ -107,22 +126,24 @@ __global__ __launch_bounds__(1024) void history_reserve_kernel(AppendArgs a) {
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool wide, float* x) {
-    if (wide) {
-        if constexpr (sizeof(T) == 2) {
-            typedef T v8 __attribute__((ext_vector_type(8)));
-            const v8 r = *(const v8*)p;
+// Four values as four codes.
+__device__ __forceinline__ unsigned pk_e4m3x4(float a, float b, float c, float d) {
+    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
+}
+
+// Word k of 16-lane row q goes to word q of row k.
+__device__ __forceinline__ void exchange4(unsigned* w) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = (float)r[i];
-        } else {
-            const floatx4 r0 = *(const floatx4*)p, r1 = *(const floatx4*)(p + 4);
+    for (int k = 0; k < 2; ++k) {
+        const auto r = __builtin_amdgcn_permlane32_swap(w[k], w[k + 2], false, false);
+        w[k] = r[0];
+        w[k + 2] = r[1];
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = r0[i], x[4 + i] = r1[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (float)p[i];
+    for (int k = 0; k < 4; k += 2) {
+        const auto r = __builtin_amdgcn_permlane16_swap(w[k], w[k + 1], false, false);
+        w[k] = r[0];
+        w[k + 1] = r[1];
     }
 }
 
@@ -130,138 +151,139 @@ __device__ __forceinline__ void load8(const T* p, bool wide, float* x) {
 __device__ __forceinline__ unsigned rescale4(unsigned w, float f) {
     const float x0 = __builtin_amdgcn_cvt_f32_fp8((int)w, 0) * f, x1 = __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * f;
     const float x2 = __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * f, x3 = __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * f;
-    return pk_e4m3(x0, x1) | pk_e4m3(x2, x3) << 16;
+    return pk_e4m3x4(x0, x1, x2, x3);
 }
 
-// One block per (page an append touches, kv head, keys or values): the largest
+// Bytes of word w of a 16-event group that lie below event `to` of the group.
+__device__ __forceinline__ unsigned bytes_below(int to, int w) {
+    const int k = to - 4 * w;
+    return k >= 4 ? ~0u : (k <= 0 ? 0u : (1u << (8 * k)) - 1u);
+}
+
+// One wave per (page an append touches, kv head, keys or values).  The largest
 // finite value of the new events sets the block's scale, never below the one it
-// has; codes are written from registers, the values' turned through LDS into
-// their event-minor order.  Events the page already holds are read only where
-// the page is copied or its scale grows.
-template <typename T>
-__global__ __launch_bounds__(256) void history_append_kernel(AppendArgs a, int wide) {
+// has; the events stay in registers from the load to the codes.  A lane takes
+// four consecutive events of eight elements: the codes of the four events of one
+// element make a word of the event-minor value page, and exchanging words
+// between the four 16-lane rows makes whole 16-byte pieces of it, without LDS.
+// Events the page already holds are read only where the page is copied, its
+// scale grows, or they share a 16-byte piece with new values.
+template <typename T, int D, int PE, bool WIDE>
+__global__ __launch_bounds__(256, 2) void history_append_kernel(AppendArgs a) {
     const dlrm_history_cache_t& c = a.c;
-    __shared__ __attribute__((aligned(16))) uint8_t turned[64 * 128];
-    __shared__ float wmax[4];
-    const int pe = c.page_events, dim = c.head_dim, hk = blockIdx.y, tid = threadIdx.x;
-    const bool minor = blockIdx.z != 0;
-    const Unit un = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, pe, 2, blockIdx.x);
-    const int b = un.b;
-    const int64_t nth = un.nth, begin = un.begin, count = un.end - un.begin;
-    const Grant g = a.grants[b];
-    if (g.old_len < 0 || count == 0) return;
-    const int slot = a.slots ? a.slots[b] : b;
-    const int64_t first = g.old_len / pe, page_no = first + nth, stop = g.old_len + count;
-    if (nth < 0 || page_no * pe >= stop) return;
-    const int lo = nth == 0 ? g.old_len % pe : 0;                                  // events already in the page
-    const int hi = (int)(stop - page_no * pe < pe ? stop - page_no * pe : pe);     // events after the call
+    constexpr int C8 = D / 8;                            // 8-element pieces of a head
+    constexpr int EV = 2048 / D;                         // events of one round of the wave
+    constexpr int ROUNDS = PE > EV ? PE / EV : 1;
+    const int lane = threadIdx.x & 63;
+    const int item = __builtin_amdgcn_readfirstlane((int)blockIdx.y * 4 + (threadIdx.x >> 6));
+    if (item >= 2 * c.n_kv_heads) return;
+    const int hk = item >> 1;
+    const bool minor = item & 1;
+    const Unit un = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, PE, 2, blockIdx.x);
+    const int64_t count = un.end - un.begin;
+    const Grant g = a.grants[un.b];
+    const int slot = a.slots ? a.slots[un.b] : un.b;
+    if (un.nth < 0 || g.old_len < 0 || count == 0) return;
+    const int64_t page_no = g.old_len / PE + un.nth, stop = g.old_len + count;
+    if (page_no * PE >= stop) return;
+    const int lo = un.nth == 0 ? g.old_len % PE : 0;                               // events already in the page
+    const int hi = (int)(stop - page_no * PE < PE ? stop - page_no * PE : PE);     // events after the call
     const bool kept = lo > 0 && !g.copy;
-    const int opened = (int)nth - (g.src >= 0 && !g.copy ? 1 : 0);                 // of the pages taken from the list
+    const int opened = (int)un.nth - (g.src >= 0 && !g.copy ? 1 : 0);              // of the pages taken from the list
+    const int64_t ld = minor ? a.ld_v : a.ld_k;
+    // the page's first event stands lo events before the call's first one
+    const T* x = (const T*)(minor ? a.v : a.k) + (un.begin + page_no * PE - g.old_len) * ld + (int64_t)hk * D;
+    const int ch = lane % C8, quad = (lane >> 4) + 4 * ((lane & 15) / C8);
+
+    // events outside [lo, hi) stand in as the nearest one inside
+    Raw<T> raw[ROUNDS][4];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r)
+        if (r * EV < hi && (r + 1) * EV > lo)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int ev = min(max(r * EV + 4 * quad + j, lo), hi - 1);
+                raw[r][j] = load_raw<WIDE>(x + (int64_t)ev * ld + ch * 8);
+            }
     const int dst = kept ? g.src : c.free_pages[g.pos - opened];
     if (dst < 0 || dst >= c.n_pages) return;
     const int src = lo > 0 ? g.src : dst;
-
     const int64_t dst_h = (int64_t)dst * c.n_kv_heads + hk, src_h = (int64_t)src * c.n_kv_heads + hk;
-    const int64_t page_bytes = (int64_t)pe * dim;
-    uint8_t* codes = (minor ? c.v : c.k) + dst_h * page_bytes;
-    const uint8_t* held = (minor ? c.v : c.k) + src_h * page_bytes;
+    uint8_t* codes = (minor ? c.v : c.k) + dst_h * (PE * D);
+    const uint8_t* held = (minor ? c.v : c.k) + src_h * (PE * D);
     float* scales = minor ? c.v_scale : c.k_scale;
-    const int64_t ld = minor ? a.ld_v : a.ld_k;
-    // the page's first event stands lo events before the call's first one
-    const T* x = (const T*)(minor ? a.v : a.k) + (begin + page_no * pe - g.old_len) * ld + (int64_t)hk * dim;
+    const float was = lo > 0 ? scales[src_h] : 0.f;
 
-    const int d8 = dim / 8;               // 8-element pieces of a head: 4, 8 or 16
-    const int sh = 31 - __builtin_clz(d8);
-    const int lo8 = lo << sh, hi8 = hi << sh;
-    float val[4][8];
     float top = 0.f;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int p = lo8 + tid + r * 256;
-        if (p < hi8) {
-            load8(x + (int64_t)(p >> sh) * ld + (p & (d8 - 1)) * 8, wide, val[r]);
+    for (int r = 0; r < ROUNDS; ++r)
+        if (r * EV < hi && (r + 1) * EV > lo)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float m = fabsf(val[r][i]);
-                top = m < INFINITY ? fmaxf(top, m) : top;
-            }
-        }
-    }
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float m = fabsf((float)raw[r][j].x[i]);
+                    top = m < INFINITY ? fmaxf(top, m) : top;
+                }
     top = wave_max(top);
-    if ((tid & 63) == 0) wmax[tid >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
-    const float was = lo > 0 ? scales[src_h] : 0.f;
     float s = page_scale(top);
     s = was > s ? was : s;
-    const float inv = 1.f / s;            // a power of two: exact
+    const float inv = 1.f / s;                           // a power of two: exact
     const bool rewrite = lo > 0 && (g.copy || s > was);
     const float grown = rewrite ? was * inv : 1.f;
+    const int from = rewrite ? 0 : lo;
 
-    uint2 code[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int p = lo8 + tid + r * 256;
-        if (p < hi8) {
-            code[r].x = pk_e4m3(val[r][0] * inv, val[r][1] * inv) | pk_e4m3(val[r][2] * inv, val[r][3] * inv) << 16;
-            code[r].y = pk_e4m3(val[r][4] * inv, val[r][5] * inv) | pk_e4m3(val[r][6] * inv, val[r][7] * inv) << 16;
-        }
-    }
-    if (!minor) {
+    for (int r = 0; r < ROUNDS; ++r) {
+        if (r * EV >= hi || (r + 1) * EV <= from) continue;
+        if (!minor) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int p = lo8 + tid + r * 256;
-            if (p < hi8) *(uint2*)(codes + p * 8) = code[r];
-        }
-        if (rewrite)
-            for (int p = tid; p < lo8; p += 256) {
-                const uint2 w = *(const uint2*)(held + p * 8);
-                *(uint2*)(codes + p * 8) = make_uint2(rescale4(w.x, grown), rescale4(w.y, grown));
-            }
-    } else {
+            for (int j = 0; j < 4; ++j) {
+                const int ev = r * EV + 4 * quad + j;
+                if (ev < from || ev >= hi) continue;
+                uint2 w;
+                if (ev >= lo) {
+                    float f[8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int p = lo8 + tid + r * 256;
-            if (p < hi8) {
-                const int ev = p >> sh, d = (p & (d8 - 1)) * 8;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    turned[(d + i) * pe + ev] = (uint8_t)((i < 4 ? code[r].x : code[r].y) >> (8 * (i & 3)));
-            }
-        }
-        __syncthreads();
-        const int from = rewrite ? 0 : lo;
-        const int pieces = dim * pe / 16;
-        for (int p = tid; p < pieces; p += 256) {
-            const int e0 = (p * 16) % pe;                    // the piece's first event
-            if (e0 >= hi || e0 + 16 <= from) continue;
-            uint4 w = *(const uint4*)(turned + p * 16);
-            if (rewrite && e0 < lo) {
-                const uint4 o = *(const uint4*)(held + p * 16);
-                const unsigned old[4] = {rescale4(o.x, grown), rescale4(o.y, grown), rescale4(o.z, grown),
-                                         rescale4(o.w, grown)};
-                unsigned n[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = lo - (e0 + 4 * i);         // old events of this word
-                    const unsigned m = k >= 4 ? ~0u : (k <= 0 ? 0u : (1u << (8 * k)) - 1u);
-                    n[i] = (old[i] & m) | (n[i] & ~m);
+                    for (int i = 0; i < 8; ++i) f[i] = (float)raw[r][j].x[i] * inv;
+                    w.x = pk_e4m3x4(f[0], f[1], f[2], f[3]);
+                    w.y = pk_e4m3x4(f[4], f[5], f[6], f[7]);
+                } else {
+                    const uint2 o = *(const uint2*)(held + ev * D + ch * 8);
+                    w = make_uint2(rescale4(o.x, grown), rescale4(o.y, grown));
                 }
-                w = make_uint4(n[0], n[1], n[2], n[3]);
+                *(uint2*)(codes + ev * D + ch * 8) = w;
             }
-            if (e0 >= from && e0 + 16 <= hi) {
-                *(uint4*)(codes + p * 16) = w;
-            } else {
-                const unsigned n[4] = {w.x, w.y, w.z, w.w};
+        } else {
+            unsigned w[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (e0 + i >= from && e0 + i < hi) codes[p * 16 + i] = (uint8_t)(n[i / 4] >> (8 * (i & 3)));
+            for (int i = 0; i < 8; ++i)
+                w[i] = pk_e4m3x4((float)raw[r][0].x[i] * inv, (float)raw[r][1].x[i] * inv,
+                                 (float)raw[r][2].x[i] * inv, (float)raw[r][3].x[i] * inv);
+            const int e0 = r * EV + 16 * ((lane & 15) / C8);             // the lane's 16 events after the exchange
+            exchange4(w);
+            exchange4(w + 4);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (e0 >= hi || e0 + 16 <= from) continue;
+                const int at = (ch * 8 + 4 * k + (lane >> 4)) * PE + e0;
+                if (lo > e0 || hi < e0 + 16) {
+                    const uint4 o = *(const uint4*)(held + at), d = *(const uint4*)(codes + at);
+                    const unsigned old[4] = {o.x, o.y, o.z, o.w}, stale[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const unsigned below = bytes_below(lo - e0, y), in = bytes_below(hi - e0, y);
+                        w[4 * k + y] = ((rewrite ? rescale4(old[y], grown) : old[y]) & below) | (w[4 * k + y] & in & ~below) |
+                                       (stale[y] & ~in);
+                    }
+                }
+                *(uint4*)(codes + at) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
             }
         }
     }
-    if (tid == 0) {
+    if (lane == 0) {
         if (!kept || s != was) scales[dst_h] = s;
-        if (hk == 0 && !minor && !kept) {
+        if (item == 0 && !kept) {
             c.table[(int64_t)slot * c.max_pages + page_no] = dst;
             c.refs[dst] = 1;
             if (lo > 0) atomicSub(&c.refs[src], 1);
@@ -327,48 +349,93 @@ __global__ __launch_bounds__(256) void history_trim_kernel(dlrm_history_cache_t 
     for (int64_t i = lo + threadIdx.x; i < hi; i += 256) release_entry(c, row + i);
 }
 
-// Free pages of each chunk.
-__global__ __launch_bounds__(256) void history_count_kernel(dlrm_history_cache_t c, int32_t* counts) {
-    const int base = blockIdx.x * kRebuildChunk;
+// The block's free pages as words of 64 bits: the wave reads WORDS x 64
+// consecutive pages at a time and keeps one word for each 64 in LDS.  Returns the
+// free pages of the wave's share; `refs` may have changed in this kernel, so they
+// are read past the vector cache.
+template <int WAVES>
+__device__ __forceinline__ int mark_free(const dlrm_history_cache_t& c, int base, int words_per_wave,
+                                         unsigned long long* words) {
+    constexpr int AT_ONCE = 8;
+    const int lane = threadIdx.x & 63, w0 = (threadIdx.x >> 6) * words_per_wave;
     int n = 0;
-    for (int i = threadIdx.x; i < kRebuildChunk; i += 256)
-        n += base + i < c.n_pages && c.refs[base + i] == 0 ? 1 : 0;
-    int total;
-    block_exclusive<256>(n, &total);
-    if (threadIdx.x == 0) counts[blockIdx.x] = total;
+    for (int k = 0; k < words_per_wave; k += AT_ONCE) {
+        int r[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int p = base + (w0 + k + i) * 64 + lane;
+            r[i] = k + i < words_per_wave && p < c.n_pages
+                       ? __hip_atomic_load(&c.refs[p], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 1;
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const unsigned long long m = __ballot(r[i] == 0);
+            if (k + i < words_per_wave) {
+                if (lane == 0) words[w0 + k + i] = m;
+                n += __popcll(m);
+            }
+        }
+    }
+    return n;
 }
 
-// Writes the chunk's free pages: page p goes to the place that counts the free
-// pages above it.
-template <int THREADS, int PER>
-__device__ __forceinline__ void list_free(const dlrm_history_cache_t& c, int base, int above) {
-    const int p0 = base + (int)threadIdx.x * PER;
-    int n = 0;
-    bool free[PER];
+// Sums of one number per wave: over the waves after mine, and over all.
+template <int WAVES>
+__device__ __forceinline__ int after_mine(int n, int* total) {
+    __shared__ int part[WAVES];
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = n;
+    __syncthreads();
+    int after = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        free[i] = p0 + i < c.n_pages && c.refs[p0 + i] == 0;
-        n += free[i] ? 1 : 0;
+    for (int i = 0; i < WAVES; ++i) {
+        after += i > (int)(threadIdx.x >> 6) ? part[i] : 0;
+        all += part[i];
     }
+    *total = all;
+    return after;
+}
+
+// Free page p goes to the place that counts the free pages above it.
+template <int WAVES>
+__device__ __forceinline__ void list_free(const dlrm_history_cache_t& c, int base, int words_per_wave, int above,
+                                          unsigned long long* words) {
+    const int n = mark_free<WAVES>(c, base, words_per_wave, words);
     int total;
-    const int before = block_exclusive<THREADS>(n, &total);
-    int at = above + total - before - 1;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (free[i]) c.free_pages[at--] = p0 + i;
+    int at = above + after_mine<WAVES>(n, &total);      // also the barrier behind the words
+    const int lane = threadIdx.x & 63, w0 = (threadIdx.x >> 6) * words_per_wave;
+    for (int k = words_per_wave - 1; k >= 0; --k) {
+        const unsigned long long m = words[w0 + k];
+        if (m >> lane & 1) c.free_pages[at + __popcll(lane == 63 ? 0ull : m >> (lane + 1))] = base + (w0 + k) * 64 + lane;
+        at += __popcll(m);
+    }
     if (base == 0 && threadIdx.x == 0) c.counters[0] = above + total;
 }
 
+static __host__ __device__ inline int words_each(int n_pages, int waves) {
+    return ((n_pages + 63) / 64 + waves - 1) / waves;
+}
+
 __global__ __launch_bounds__(1024) void history_rebuild_one_kernel(dlrm_history_cache_t c) {
-    list_free<1024, kOneBlockPages / 1024>(c, 0, 0);
+    __shared__ unsigned long long words[kOneBlockPages / 64 + 16];
+    list_free<16>(c, 0, words_each(c.n_pages, 16), 0, words);
+}
+
+// Free pages of each chunk.
+__global__ __launch_bounds__(256) void history_count_kernel(dlrm_history_cache_t c, int32_t* counts) {
+    __shared__ unsigned long long words[kRebuildChunk / 64];
+    const int n = mark_free<4>(c, blockIdx.x * kRebuildChunk, kRebuildChunk / 256, words);
+    int total;
+    after_mine<4>(n, &total);
+    if (threadIdx.x == 0) counts[blockIdx.x] = total;
 }
 
 __global__ __launch_bounds__(256) void history_rebuild_kernel(dlrm_history_cache_t c, const int32_t* counts) {
+    __shared__ unsigned long long words[kRebuildChunk / 64];
     int n = 0;
     for (int i = blockIdx.x + 1 + threadIdx.x; i < (int)gridDim.x; i += 256) n += counts[i];
     int above;
     block_exclusive<256>(n, &above);
-    list_free<256, kRebuildChunk / 256>(c, blockIdx.x * kRebuildChunk, above);
+    list_free<4>(c, blockIdx.x * kRebuildChunk, kRebuildChunk / 256, above, words);
 }
 
 static hipError_t rebuild(const dlrm_history_cache_t& c, int32_t* counts, hipStream_t s) {
@@ -400,9 +467,60 @@ static MoveWs move_ws(const dlrm_history_cache_t& c, int32_t* ws) {
     return w;
 }
 
+// Enters the marked pages into the lists: `before` free pages lie before the
+// wave's first one, `holes` below m.
+__device__ __forceinline__ void list_moves(const dlrm_history_cache_t& c, const MoveWs& w, int base, int words_per_wave,
+                                           int before, int m, int holes, const unsigned long long* words) {
+    const int lane = threadIdx.x & 63, w0 = (threadIdx.x >> 6) * words_per_wave;
+    for (int k = 0; k < words_per_wave; ++k) {
+        const unsigned long long f = words[w0 + k];
+        const int p = base + (w0 + k) * 64 + lane;
+        const int fb = before + __popcll(f & ((1ull << lane) - 1));
+        if (p < c.n_pages) {
+            // used pages before p and at or above m: (p - fb) - (m - holes)
+            if (f >> lane & 1) {
+                if (p < m) w.to[fb] = p;
+            } else if (p >= m) {
+                w.from[p - fb - (m - holes)] = p;
+            }
+        }
+        before += __popcll(f);
+    }
+}
+
+// The new place and the holders of a page that moves.
+__device__ __forceinline__ void pair_move(const dlrm_history_cache_t& c, const MoveWs& w, int i) {
+    const int from = w.from[i], to = w.to[i];
+    w.place[from] = to;
+    c.refs[to] = c.refs[from];
+    c.refs[from] = 0;
+}
+
+__global__ __launch_bounds__(1024) void history_plan_one_kernel(dlrm_history_cache_t c, MoveWs w) {
+    __shared__ unsigned long long words[kOneBlockPages / 64 + 16];
+    const int each = words_each(c.n_pages, 16);
+    const int n = mark_free<16>(c, 0, each, words);
+    int total, holes;
+    const int after = after_mine<16>(n, &total);
+    const int m = c.n_pages - total;
+    int below = 0;
+    for (int k = threadIdx.x; k * 64 < m; k += 1024)
+        below += __popcll(m - k * 64 >= 64 ? words[k] : words[k] & ((1ull << (m - k * 64)) - 1));
+    block_exclusive<1024>(below, &holes);
+    list_moves(c, w, 0, each, total - after - n, m, holes, words);
+    __threadfence();
+    __syncthreads();
+    for (int i = threadIdx.x; i < holes; i += 1024) pair_move(c, w, i);
+    if (threadIdx.x == 0) {
+        *w.n = holes;
+        c.counters[0] = total;
+    }
+}
+
 __global__ __launch_bounds__(256) void history_plan_kernel(dlrm_history_cache_t c, MoveWs w, int chunks) {
-    // free pages in all, before this chunk, and before page m
-    int n = 0, nb = 0, total, before;
+    __shared__ unsigned long long words[kRebuildChunk / 64];
+    // free pages in all, before this chunk, and below page m
+    int n = 0, nb = 0, total, before, sum;
     for (int i = threadIdx.x; i < chunks; i += 256) {
         const int k = w.counts[i];
         n += k;
@@ -415,31 +533,22 @@ __global__ __launch_bounds__(256) void history_plan_kernel(dlrm_history_cache_t 
     for (int i = threadIdx.x; i < m_chunk && i < chunks; i += 256) nm += w.counts[i];
     for (int p = m_chunk * kRebuildChunk + threadIdx.x; p < m; p += 256) nm += c.refs[p] == 0 ? 1 : 0;
     block_exclusive<256>(nm, &holes);
-    constexpr int PER = kRebuildChunk / 256;
-    const int p0 = (int)blockIdx.x * kRebuildChunk + (int)threadIdx.x * PER;
-    int k = 0, sum;
-    bool free[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        free[i] = p0 + i < c.n_pages && c.refs[p0 + i] == 0;
-        k += free[i] ? 1 : 0;
-    }
-    int fb = before + block_exclusive<256>(k, &sum);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int p = p0 + i;
-        if (p >= c.n_pages) break;
-        // used pages before p and at or above m: (p - fb) - (m - holes)
-        if (free[i] && p < m) w.to[fb] = p;
-        if (!free[i] && p >= m) w.from[p - fb - (m - holes)] = p;
-        fb += free[i] ? 1 : 0;
-    }
+    const int mine = mark_free<4>(c, blockIdx.x * kRebuildChunk, kRebuildChunk / 256, words);
+    const int after = after_mine<4>(mine, &sum);
+    list_moves(c, w, blockIdx.x * kRebuildChunk, kRebuildChunk / 256, before + sum - after - mine, m, holes, words);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *w.n = holes;
         c.counters[0] = total;
     }
 }
 
+__global__ __launch_bounds__(256) void history_pair_kernel(dlrm_history_cache_t c, MoveWs w) {
+    const int n = *w.n;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        pair_move(c, w, (int)i);
+}
+
+// Moves the pages and gives them their new numbers in the table and the list.
 __global__ __launch_bounds__(256) void history_move_kernel(dlrm_history_cache_t c, MoveWs w) {
     const int n = *w.n;
     const int64_t vecs = (int64_t)c.n_kv_heads * c.page_events * c.head_dim / 16;
@@ -448,22 +557,15 @@ __global__ __launch_bounds__(256) void history_move_kernel(dlrm_history_cache_t 
         const uint4 *k0 = (const uint4*)c.k + from * vecs, *v0 = (const uint4*)c.v + from * vecs;
         uint4 *k1 = (uint4*)c.k + to * vecs, *v1 = (uint4*)c.v + to * vecs;
         for (int64_t i = threadIdx.x; i < vecs; i += 256) {
-            k1[i] = k0[i];
-            v1[i] = v0[i];
+            const uint4 k = k0[i], v = v0[i];
+            k1[i] = k;
+            v1[i] = v;
         }
         for (int h = threadIdx.x; h < c.n_kv_heads; h += 256) {
             c.k_scale[(int64_t)to * c.n_kv_heads + h] = c.k_scale[(int64_t)from * c.n_kv_heads + h];
             c.v_scale[(int64_t)to * c.n_kv_heads + h] = c.v_scale[(int64_t)from * c.n_kv_heads + h];
         }
-        if (threadIdx.x == 0) {
-            w.place[from] = to;
-            c.refs[to] = c.refs[from];
-            c.refs[from] = 0;
-        }
     }
-}
-
-__global__ __launch_bounds__(256) void history_relabel_kernel(dlrm_history_cache_t c, MoveWs w) {
     const int n_free = c.counters[0], m = c.n_pages - n_free;
     const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
     for (int64_t i = i0; i < n_free; i += step) c.free_pages[i] = c.n_pages - 1 - (int)i;
@@ -486,16 +588,34 @@ hipError_t launch_history_init(const dlrm_history_cache_t& c, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <typename T, int D, int PE>
+static void launch_append(const AppendArgs& a, bool wide, dim3 grid, hipStream_t s) {
+    if (wide) hipLaunchKernelGGL((history_append_kernel<T, D, PE, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((history_append_kernel<T, D, PE, false>), grid, dim3(256), 0, s, a);
+}
+template <typename T, int D>
+static void launch_append(const AppendArgs& a, bool wide, dim3 grid, hipStream_t s) {
+    if (a.c.page_events == 16) launch_append<T, D, 16>(a, wide, grid, s);
+    else if (a.c.page_events == 32) launch_append<T, D, 32>(a, wide, grid, s);
+    else launch_append<T, D, 64>(a, wide, grid, s);
+}
+template <typename T>
+static void launch_append(const AppendArgs& a, dim3 grid, hipStream_t s) {
+    const int step = 16 / sizeof(T);
+    const bool wide = a.ld_k % step == 0 && a.ld_v % step == 0 && (((uintptr_t)a.k | (uintptr_t)a.v) & 15u) == 0;
+    if (a.c.head_dim == 32) launch_append<T, 32>(a, wide, grid, s);
+    else if (a.c.head_dim == 64) launch_append<T, 64>(a, wide, grid, s);
+    else launch_append<T, 128>(a, wide, grid, s);
+}
+
 hipError_t launch_history_append(const AppendArgs& a, int dtype, hipStream_t s) {
     hipLaunchKernelGGL(history_reserve_kernel, dim3(1), dim3(1024), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_events == 0) return e;
-    const dim3 grid((unsigned)(a.n_events / a.c.page_events + 2 * (int64_t)a.batch), (unsigned)a.c.n_kv_heads, 2);
-    const int step = dtype == DLRM_DTYPE_F32 ? 4 : 8;
-    const int wide = a.ld_k % step == 0 && a.ld_v % step == 0 && (((uintptr_t)a.k | (uintptr_t)a.v) & 15u) == 0;
-    if (dtype == DLRM_DTYPE_F32) hipLaunchKernelGGL(history_append_kernel<float>, grid, dim3(256), 0, s, a, wide);
-    else if (dtype == DLRM_DTYPE_BF16) hipLaunchKernelGGL(history_append_kernel<bf16>, grid, dim3(256), 0, s, a, wide);
-    else hipLaunchKernelGGL(history_append_kernel<f16>, grid, dim3(256), 0, s, a, wide);
+    const dim3 grid((unsigned)(a.n_events / a.c.page_events + 2 * (int64_t)a.batch), (unsigned)((2 * a.c.n_kv_heads + 3) / 4));
+    if (dtype == DLRM_DTYPE_F32) launch_append<float>(a, grid, s);
+    else if (dtype == DLRM_DTYPE_BF16) launch_append<bf16>(a, grid, s);
+    else launch_append<f16>(a, grid, s);
     return hipGetLastError();
 }
 
@@ -522,12 +642,17 @@ hipError_t launch_history_trim(const dlrm_history_cache_t& c, int n, const int32
 
 hipError_t launch_history_compact(const dlrm_history_cache_t& c, int32_t* ws, hipStream_t s) {
     const MoveWs w = move_ws(c, ws);
-    const int chunks = rebuild_chunks(c.n_pages);
-    hipLaunchKernelGGL(history_count_kernel, dim3(chunks), dim3(256), 0, s, c, w.counts);
-    hipLaunchKernelGGL(history_plan_kernel, dim3(chunks), dim3(256), 0, s, c, w, chunks);
-    hipLaunchKernelGGL(history_move_kernel, dim3(c.n_pages < 2048 ? c.n_pages : 2048), dim3(256), 0, s, c, w);
-    hipLaunchKernelGGL(history_relabel_kernel,
-                       dim3(grid_for((int64_t)c.n_slots * c.max_pages + c.n_pages, 2048)), dim3(256), 0, s, c, w);
+    if (c.n_pages <= kOneBlockPages) {
+        hipLaunchKernelGGL(history_plan_one_kernel, dim3(1), dim3(1024), 0, s, c, w);
+    } else {
+        const int chunks = rebuild_chunks(c.n_pages);
+        hipLaunchKernelGGL(history_count_kernel, dim3(chunks), dim3(256), 0, s, c, w.counts);
+        hipLaunchKernelGGL(history_plan_kernel, dim3(chunks), dim3(256), 0, s, c, w, chunks);
+        hipLaunchKernelGGL(history_pair_kernel, dim3(grid_for(c.n_pages, 1024)), dim3(256), 0, s, c, w);
+    }
+    const int64_t cells = (int64_t)c.n_slots * c.max_pages + c.n_pages;
+    const unsigned movers = (unsigned)(c.n_pages < 2048 ? c.n_pages : 2048), rows = grid_for(cells, 2048);
+    hipLaunchKernelGGL(history_move_kernel, dim3(movers > rows ? movers : rows), dim3(256), 0, s, c, w);
     return hipGetLastError();
 }
 
