@@ -43,7 +43,7 @@ dlrm_status_t check_cache_pointers(const dlrm_history_cache_t* c) {
     if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->table || !c->lens || !c->refs || !c->free_pages ||
         !c->counters)
         return DLRM_E_NULL;
-    if ((((uintptr_t)c->k | (uintptr_t)c->v) & 15u) != 0) return DLRM_E_SHAPE;
+    if ((((uintptr_t)c->k | (uintptr_t)c->v | (uintptr_t)c->refs) & 15u) != 0) return DLRM_E_SHAPE;
     return DLRM_OK;
 }
 

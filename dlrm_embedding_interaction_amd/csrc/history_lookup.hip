@@ -31,6 +31,7 @@ namespace dlrm {
 
 constexpr int kTile = 64;                // events per tile
 constexpr int kLookupWaves = 2048;       // waves a launch aims at: two on each SIMD
+constexpr int kDirectTiles = 32;         // histories of at most this many tiles have a block of their own
 
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -114,13 +115,18 @@ struct Tile {
     bool kin, vin;                                      // the pages are there
 };
 
-template <int D, int PE, typename T>
+// DIRECT: one block per (history, chunk of rows), its waves taking every fourth
+// tile and joining their results through LDS.
+template <int D, int PE, typename T, bool DIRECT>
 __global__ __launch_bounds__(256, 2) void history_lookup_kernel(LookupArgs a, int n_waves, int* __restrict__ meta) {
     constexpr int NQ = Parts<T>::q, NP = Parts<T>::p;
     constexpr int KS = D / 32;                          // 32-element steps of the first product
     constexpr int PT = kTile / PE;                      // pages per tile
-    __shared__ int before[256];
+    constexpr int OP = D + 4;                           // row stride of the joined results
+    __shared__ int before[DIRECT ? 1 : 256];
     __shared__ int wsum[4];
+    __shared__ __attribute__((aligned(16))) float part_o[DIRECT ? 4 * 16 * OP : 4];
+    __shared__ float part_m[64], part_l[64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = lane & 15, g = lane >> 4;
     const int group = a.n_heads / a.c.n_kv_heads, rows = a.queries * group;
@@ -128,52 +134,58 @@ __global__ __launch_bounds__(256, 2) void history_lookup_kernel(LookupArgs a, in
     const int hk = blockIdx.y / chunks, r = (blockIdx.y % chunks) * 16 + n;
     const int cols = rows < 16 ? rows : 16;             // columns of a partial result
 
-    // tiles before each thread's share of the histories
-    const int each = (a.batch + 255) / 256;
-    const int b_lo = tid * each, b_hi = b_lo + each < a.batch ? b_lo + each : a.batch;
-    int mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += span_of(a, b).count;
-    int inc = mine;
+    int w = 0, at = 0, stop = 1, start = 0, b = blockIdx.x, per = 1;
+    if constexpr (!DIRECT) {
+        // tiles before each thread's share of the histories
+        const int each = (a.batch + 255) / 256;
+        const int b_lo = tid * each, b_hi = b_lo + each < a.batch ? b_lo + each : a.batch;
+        int mine = 0;
+        for (int b = b_lo; b < b_hi; ++b) mine += span_of(a, b).count;
+        int inc = mine;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(inc, d, 64);
-        if (lane >= d) inc += o;
-    }
-    if (lane == 63) wsum[wave] = inc;
-    __syncthreads();
-    int total = 0;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(inc, d, 64);
+            if (lane >= d) inc += o;
+        }
+        if (lane == 63) wsum[wave] = inc;
+        __syncthreads();
+        int total = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (i < wave) inc += wsum[i];
-        total += wsum[i];
+        for (int i = 0; i < 4; ++i) {
+            if (i < wave) inc += wsum[i];
+            total += wsum[i];
+        }
+        before[tid] = inc - mine;
+        __syncthreads();
+        per = total > n_waves ? (total + n_waves - 1) / n_waves : 1;
+        w = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + wave);
+        if (w == 0 && blockIdx.y == 0 && lane == 0) meta[a.batch] = per;
+        int64_t at64 = (int64_t)w * per;
+        if (at64 >= total) return;
+        at = (int)at64;
+        stop = at + per < total ? at + per : total;
+        int lo = 0, hi = 255;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (before[mid] <= at) lo = mid;
+            else hi = mid - 1;
+        }
+        start = __builtin_amdgcn_readfirstlane(before[lo]);       // tiles before history b
+        b = __builtin_amdgcn_readfirstlane(lo * each);
     }
-    before[tid] = inc - mine;
-    __syncthreads();
-    const int per = total > n_waves ? (total + n_waves - 1) / n_waves : 1;
-    const int w = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + wave);
-    if (w == 0 && blockIdx.y == 0 && lane == 0) meta[a.batch] = per;
-    int64_t at64 = (int64_t)w * per;
-    if (at64 >= total) return;
-    int at = (int)at64;
-    const int stop = at + per < total ? at + per : total;
-    int lo = 0, hi = 255;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (before[mid] <= at) lo = mid;
-        else hi = mid - 1;
-    }
-    int start = __builtin_amdgcn_readfirstlane(before[lo]);       // tiles before history b
-    int b = __builtin_amdgcn_readfirstlane(lo * each);
 
     while (at < stop) {
         const Span sp = span_of(a, b);
-        if (start + sp.count <= at) {
+        if (!DIRECT && start + sp.count <= at) {
             start += sp.count;
             ++b;
             continue;
         }
-        const int i0 = at - start, i1 = sp.count < stop - start ? sp.count : stop - start;
-        if (i0 == 0 && blockIdx.y == 0 && lane == 0) meta[b] = start;
+        // the wave's tiles of the history: a run, or every fourth
+        const int i0 = DIRECT ? wave : at - start;
+        const int i1 = DIRECT || sp.count < stop - start ? sp.count : stop - start;
+        constexpr int STEP = DIRECT ? 4 : 1;
+        if (!DIRECT && i0 == 0 && blockIdx.y == 0 && lane == 0) meta[b] = start;
         const int slot = a.slots ? a.slots[b] : b;
         const int32_t* table = a.c.table + (int64_t)slot * a.c.max_pages;
 
@@ -309,16 +321,38 @@ __global__ __launch_bounds__(256, 2) void history_lookup_kernel(LookupArgs a, in
         };
 
         Tile<D> cur, nxt;
-        load(i0, cur);
-        for (int i = i0; i < i1; ++i) {
-            if (i + 1 < i1) load(i + 1, nxt);
+        if (i0 < i1) load(i0, cur);
+        for (int i = i0; i < i1; i += STEP) {
+            if (i + STEP < i1) load(i + STEP, nxt);
             use(i, cur);
             cur = nxt;
         }
         l += swizzle_xor16(l);
         l += __shfl_xor(l, 32, 64);
 
-        if (i0 == 0 && i1 == sp.count) {
+        if constexpr (DIRECT) {
+            if (g == 0) part_m[wave * 16 + n] = m;
+            __syncthreads();
+            const float mx = fmaxf(fmaxf(part_m[n], part_m[16 + n]), fmaxf(part_m[32 + n], part_m[48 + n]));
+            const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mx);
+            if (g == 0) part_l[wave * 16 + n] = l * f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) *(floatx4*)&part_o[(wave * 16 + n) * OP + 16 * j + 4 * g] = o[j] * f;
+            __syncthreads();
+            for (int x = tid; x < 4 * D; x += 256) {
+                const int y = x / (D / 4), d = x % (D / 4) * 4, row = r - n + y;
+                if (row >= rows) break;
+                const float sum = part_l[y] + part_l[16 + y] + part_l[32 + y] + part_l[48 + y];
+                floatx4 v = *(const floatx4*)&part_o[y * OP + d];
+#pragma unroll
+                for (int i = 1; i < 4; ++i) v += *(const floatx4*)&part_o[(16 * i + y) * OP + d];
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                T* op = (T*)a.out + ((int64_t)b * a.queries + row / group) * a.ld_out +
+                        (int64_t)(hk * group + row % group) * D + d;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) op[i] = (T)(sum == 0.f ? 0.f : v[i] * inv);
+            }
+        } else if (i0 == 0 && i1 == sp.count) {
             if (live) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 T* op = (T*)a.out + qrow * a.ld_out + (int64_t)qhead * D;
@@ -340,6 +374,7 @@ __global__ __launch_bounds__(256, 2) void history_lookup_kernel(LookupArgs a, in
                 part[D + 1] = l;
             }
         }
+        if constexpr (DIRECT) break;
         at = start + i1;
         start += sp.count;
         ++b;
@@ -399,14 +434,26 @@ size_t lookup_workspace_bytes(const dlrm_history_cache_t& c, int64_t batch, int 
            (size_t)2 * waves_of(c, batch, queries, n_heads) * hc * cols * (c.head_dim + 2) * sizeof(float);
 }
 
+// A history's visible tiles at most, as the host can tell.
+static int64_t most_tiles(const LookupArgs& a) {
+    const int64_t span = ((int64_t)a.c.max_pages * a.c.page_events + kTile - 1) / kTile;
+    if (a.window >= span * kTile || a.sinks >= span * kTile) return span;
+    const int64_t seen = (a.window + kTile - 1) / kTile + 1 + (a.sinks + kTile - 1) / kTile;
+    return seen < span ? seen : span;
+}
+
 template <int D, int PE, typename T>
 static hipError_t launch_t(LookupArgs a, hipStream_t s) {
     const int rows = a.queries * (a.n_heads / a.c.n_kv_heads);
     const int hc = (rows + 15) / 16 * a.c.n_kv_heads;
-    const int waves = waves_of(a.c, a.batch, a.queries, a.n_heads);
     int* meta = (int*)a.partial;
     a.partial = (float*)((char*)a.partial + meta_bytes(a.batch));
-    hipLaunchKernelGGL((history_lookup_kernel<D, PE, T>), dim3(waves / 4, hc), dim3(256), 0, s, a, waves, meta);
+    if (most_tiles(a) <= kDirectTiles) {
+        hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, true>), dim3(a.batch, hc), dim3(256), 0, s, a, 0, meta);
+        return hipGetLastError();
+    }
+    const int waves = waves_of(a.c, a.batch, a.queries, a.n_heads);
+    hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, false>), dim3(waves / 4, hc), dim3(256), 0, s, a, waves, meta);
     hipLaunchKernelGGL((history_join_kernel<D, T>), dim3(a.batch, hc), dim3(256), 0, s, a, meta);
     return hipGetLastError();
 }

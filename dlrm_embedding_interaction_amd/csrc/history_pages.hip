@@ -64,40 +64,49 @@ __global__ __launch_bounds__(1024) void history_reserve_kernel(AppendArgs a) {
     __shared__ int refused, taken;
     if (threadIdx.x == 0) refused = taken = 0;
     __syncthreads();
-    const int n_free = c.counters[0], pe = c.page_events;
+    const int n_free = c.counters[0], sh = 31 - __builtin_clz(c.page_events), mask = c.page_events - 1;
+    const int most = c.max_pages << sh;
     int carry = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 1024 * PER) {
-        int need[PER], src[PER], copy[PER], slot[PER], sum = 0;
-        int64_t old[PER], count[PER], begin[PER], end[PER];
+        int need[PER], src[PER], copy[PER], slot[PER], old[PER], sum = 0;
+        int64_t begin[PER], end[PER];
         bool ok[PER];
+        // every read is of something that is there, whether it is used or not: reads under conditions would wait
+        // for one another
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int b = b0 + threadIdx.x * PER + i;
-            slot[i] = b < a.batch ? (a.slots ? a.slots[b] : b) : -1;
-            begin[i] = b < a.batch ? history_begin(a.offsets, a.idx32, b, a.n_events) : 0;
-            end[i] = b + 1 < a.batch ? ld_index(a.offsets, b + 1, a.idx32) : a.n_events;
+            const int b = min(b0 + (int)threadIdx.x * PER + i, a.batch - 1);
+            slot[i] = a.slots ? a.slots[b] : b;
+            begin[i] = ld_index(a.offsets, b, a.idx32);
+            end[i] = ld_index(a.offsets, min(b + 1, a.batch - 1), a.idx32);
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
+            const int b = b0 + (int)threadIdx.x * PER + i;
+            if (b + 1 >= a.batch) end[i] = a.n_events;
+            begin[i] = begin[i] < 0 ? 0 : (begin[i] > a.n_events ? a.n_events : begin[i]);
             end[i] = end[i] < begin[i] ? begin[i] : (end[i] > a.n_events ? a.n_events : end[i]);
-            count[i] = end[i] - begin[i];
-            ok[i] = slot[i] >= 0 && slot[i] < c.n_slots;
-            old[i] = ok[i] ? c.lens[slot[i]] : 0;
+            ok[i] = b < a.batch && slot[i] >= 0 && slot[i] < c.n_slots;
+            slot[i] = ok[i] ? slot[i] : 0;
+            old[i] = c.lens[slot[i]];
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            ok[i] = ok[i] && old[i] >= 0 && old[i] + count[i] <= (int64_t)c.max_pages * pe;
-            src[i] = -1;
-            if (ok[i] && count[i] > 0 && old[i] % pe) src[i] = c.table[(int64_t)slot[i] * c.max_pages + old[i] / pe];
+            ok[i] = ok[i] && old[i] >= 0 && old[i] + (end[i] - begin[i]) <= most;
+            old[i] = ok[i] ? old[i] : 0;
+            src[i] = c.table[(int64_t)slot[i] * c.max_pages + min(old[i] >> sh, c.max_pages - 1)];
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            if (ok[i] && count[i] > 0 && old[i] % pe) ok[i] = src[i] >= 0 && src[i] < c.n_pages;
-            copy[i] = ok[i] && src[i] >= 0 && c.refs[src[i]] > 1;
+            const bool part = end[i] > begin[i] && (old[i] & mask) != 0, in = src[i] >= 0 && src[i] < c.n_pages;
+            copy[i] = c.refs[in ? src[i] : 0] > 1 && part && in;
+            if (part) ok[i] = ok[i] && in;
+            else src[i] = -1;
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            need[i] = ok[i] && count[i] > 0 ? (int)((old[i] + count[i] + pe - 1) / pe - (old[i] + pe - 1) / pe) + copy[i] : 0;
+            const int count = (int)(end[i] - begin[i]);
+            need[i] = ok[i] && count > 0 ? ((old[i] + count + mask) >> sh) - ((old[i] + mask) >> sh) + copy[i] : 0;
             sum += need[i];
         }
         int total;
@@ -108,9 +117,9 @@ __global__ __launch_bounds__(1024) void history_reserve_kernel(AppendArgs a) {
             const int b = b0 + threadIdx.x * PER + i;
             if (b < a.batch) {
                 const bool granted = ok[i] && (need[i] == 0 || before + need[i] <= n_free);
-                a.grants[b] = Grant{granted ? (int)old[i] : -1, n_free - 1 - before, src[i], copy[i]};
+                a.grants[b] = Grant{granted ? old[i] : -1, n_free - 1 - before, src[i], copy[i]};
                 if (granted) {
-                    if (count[i] > 0) c.lens[slot[i]] = (int)(old[i] + count[i]);
+                    if (end[i] > begin[i]) c.lens[slot[i]] = old[i] + (int)(end[i] - begin[i]);
                     if (need[i]) atomicMax(&taken, before + need[i]);
                 } else {
                     atomicAdd(&refused, 1);
@@ -320,17 +329,19 @@ __global__ __launch_bounds__(256) void history_fork_kernel(dlrm_history_cache_t 
 __global__ __launch_bounds__(256) void history_truncate_kernel(dlrm_history_cache_t c, const int32_t* slots,
                                                                const int32_t* new_lens) {
     const int slot = slots[blockIdx.x], want = new_lens ? new_lens[blockIdx.x] : 0, pe = c.page_events;
+    const int sh = 31 - __builtin_clz(pe);
     bool ok = slot >= 0 && slot < c.n_slots && want >= 0;
     if (ok) ok = want <= c.lens[slot] && want <= (int64_t)c.max_pages * pe;
     const int64_t row = (int64_t)slot * c.max_pages;
     // the page that would be filled further may have been trimmed away
-    if (ok && want % pe) ok = c.table[row + want / pe] >= 0;
+    if (ok && (want & (pe - 1))) ok = c.table[row + (want >> sh)] >= 0;
     __syncthreads();  // every thread has read the length
     if (!ok) {
         if (threadIdx.x == 0) atomicAdd(&c.counters[1], 1);
         return;
     }
-    for (int64_t i = ((int64_t)want + pe - 1) / pe + threadIdx.x; i < c.max_pages; i += 256) release_entry(c, row + i);
+    for (int i = (want >> sh) + (want & (pe - 1) ? 1 : 0) + (int)threadIdx.x; i < c.max_pages; i += 256)
+        release_entry(c, row + i);
     if (threadIdx.x == 0) c.lens[slot] = want;
 }
 
@@ -349,40 +360,61 @@ __global__ __launch_bounds__(256) void history_trim_kernel(dlrm_history_cache_t 
     for (int64_t i = lo + threadIdx.x; i < hi; i += 256) release_entry(c, row + i);
 }
 
-// The block's free pages as words of 64 bits: the wave reads WORDS x 64
-// consecutive pages at a time and keeps one word for each 64 in LDS.  Returns the
-// free pages of the wave's share; `refs` may have changed in this kernel, so they
-// are read past the vector cache.
-template <int WAVES>
-__device__ __forceinline__ int mark_free(const dlrm_history_cache_t& c, int base, int words_per_wave,
-                                         unsigned long long* words) {
-    constexpr int AT_ONCE = 8;
-    const int lane = threadIdx.x & 63, w0 = (threadIdx.x >> 6) * words_per_wave;
-    int n = 0;
-    for (int k = 0; k < words_per_wave; k += AT_ONCE) {
-        int r[AT_ONCE];
+// The free pages of a wave's share of a block, loads of 256 consecutive pages
+// at a time: four bits for each load, of the lane's four pages.
+template <int LOADS>
+struct FreeBits {
+    unsigned bits[(LOADS + 7) / 8];
+    int n;              // in the wave's share
+    int p0, loads;      // the share's first page, its loads
+    __device__ __forceinline__ unsigned of(int l) const {
+        unsigned b = bits[0];
 #pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-            const int p = base + (w0 + k + i) * 64 + lane;
-            r[i] = k + i < words_per_wave && p < c.n_pages
-                       ? __hip_atomic_load(&c.refs[p], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 1;
-        }
-#pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-            const unsigned long long m = __ballot(r[i] == 0);
-            if (k + i < words_per_wave) {
-                if (lane == 0) words[w0 + k + i] = m;
-                n += __popcll(m);
-            }
-        }
+        for (int i = 1; i < (LOADS + 7) / 8; ++i) b = l >> 3 == i ? bits[i] : b;
+        return b >> (4 * (l & 7)) & 15u;
     }
-    return n;
+};
+
+template <int LOADS>
+__device__ __forceinline__ FreeBits<LOADS> mark_free(const dlrm_history_cache_t& c, int base, int loads) {
+    FreeBits<LOADS> f;
+    const int lane = threadIdx.x & 63;
+    f.p0 = base + (int)(threadIdx.x >> 6) * loads * 256;
+    f.loads = loads;
+    f.n = 0;
+#pragma unroll
+    for (int l0 = 0; l0 < LOADS; l0 += 8) {
+        int4 r[8];
+        unsigned b = 0;
+#pragma unroll
+        for (int l = 0; l < 8; ++l) {
+            const int p = f.p0 + (l0 + l) * 256 + lane * 4;
+            r[l] = l0 + l < loads && p + 3 < c.n_pages ? *(const int4*)(c.refs + p) : make_int4(1, 1, 1, 1);
+        }
+#pragma unroll
+        for (int l = 0; l < 8; ++l) {
+            const int p = f.p0 + (l0 + l) * 256 + lane * 4;
+            if (l0 + l < loads && p < c.n_pages && p + 3 >= c.n_pages) {
+                r[l].x = c.refs[p];
+                if (p + 1 < c.n_pages) r[l].y = c.refs[p + 1];
+                if (p + 2 < c.n_pages) r[l].z = c.refs[p + 2];
+            }
+            b |= ((r[l].x == 0 ? 1u : 0u) | (r[l].y == 0 ? 2u : 0u) | (r[l].z == 0 ? 4u : 0u) |
+                  (r[l].w == 0 ? 8u : 0u)) << (4 * l);
+        }
+        f.bits[l0 / 8] = b;
+        f.n += __popc(b);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) f.n += __shfl_xor(f.n, d, 64);
+    return f;
 }
 
 // Sums of one number per wave: over the waves after mine, and over all.
 template <int WAVES>
 __device__ __forceinline__ int after_mine(int n, int* total) {
     __shared__ int part[WAVES];
+    __syncthreads();  // part may still be read from a call before
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = n;
     __syncthreads();
     int after = 0, all = 0;
@@ -395,47 +427,62 @@ __device__ __forceinline__ int after_mine(int n, int* total) {
     return after;
 }
 
+// Free pages of one load: of the lanes below mine, and of all.
+__device__ __forceinline__ int lanes_below(unsigned b, int* total) {
+    const unsigned long long lt = (1ull << (threadIdx.x & 63)) - 1;
+    int below = 0, all = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const unsigned long long m = __ballot(b >> j & 1);
+        below += __popcll(m & lt);
+        all += __popcll(m);
+    }
+    *total = all;
+    return below;
+}
+
 // Free page p goes to the place that counts the free pages above it.
-template <int WAVES>
-__device__ __forceinline__ void list_free(const dlrm_history_cache_t& c, int base, int words_per_wave, int above,
-                                          unsigned long long* words) {
-    const int n = mark_free<WAVES>(c, base, words_per_wave, words);
+template <int WAVES, int LOADS>
+__device__ __forceinline__ void list_free(const dlrm_history_cache_t& c, int base, int loads, int above) {
+    const FreeBits<LOADS> f = mark_free<LOADS>(c, base, loads);
     int total;
-    int at = above + after_mine<WAVES>(n, &total);      // also the barrier behind the words
-    const int lane = threadIdx.x & 63, w0 = (threadIdx.x >> 6) * words_per_wave;
-    for (int k = words_per_wave - 1; k >= 0; --k) {
-        const unsigned long long m = words[w0 + k];
-        if (m >> lane & 1) c.free_pages[at + __popcll(lane == 63 ? 0ull : m >> (lane + 1))] = base + (w0 + k) * 64 + lane;
-        at += __popcll(m);
+    int at = above + after_mine<WAVES>(f.n, &total);
+    for (int l = loads - 1; l >= 0; --l) {
+        const unsigned b = f.of(l);
+        int all;
+        const int below = lanes_below(b, &all);
+        int to = at + all - below - __popc(b);          // free pages above the lane's last
+        const int p = f.p0 + l * 256 + (int)(threadIdx.x & 63) * 4;
+#pragma unroll
+        for (int j = 3; j >= 0; --j)
+            if (b >> j & 1) c.free_pages[to++] = p + j;
+        at += all;
     }
     if (base == 0 && threadIdx.x == 0) c.counters[0] = above + total;
 }
 
-static __host__ __device__ inline int words_each(int n_pages, int waves) {
-    return ((n_pages + 63) / 64 + waves - 1) / waves;
-}
+constexpr int kChunkLoads = kRebuildChunk / 1024;        // of each of four waves
+constexpr int kOneLoads = kOneBlockPages / 4096;         // of each of sixteen waves
+__device__ __forceinline__ int one_loads(int n_pages) { return (n_pages + 4095) / 4096; }
 
 __global__ __launch_bounds__(1024) void history_rebuild_one_kernel(dlrm_history_cache_t c) {
-    __shared__ unsigned long long words[kOneBlockPages / 64 + 16];
-    list_free<16>(c, 0, words_each(c.n_pages, 16), 0, words);
+    list_free<16, kOneLoads>(c, 0, one_loads(c.n_pages), 0);
 }
 
 // Free pages of each chunk.
 __global__ __launch_bounds__(256) void history_count_kernel(dlrm_history_cache_t c, int32_t* counts) {
-    __shared__ unsigned long long words[kRebuildChunk / 64];
-    const int n = mark_free<4>(c, blockIdx.x * kRebuildChunk, kRebuildChunk / 256, words);
+    const FreeBits<kChunkLoads> f = mark_free<kChunkLoads>(c, blockIdx.x * kRebuildChunk, kChunkLoads);
     int total;
-    after_mine<4>(n, &total);
+    after_mine<4>(f.n, &total);
     if (threadIdx.x == 0) counts[blockIdx.x] = total;
 }
 
 __global__ __launch_bounds__(256) void history_rebuild_kernel(dlrm_history_cache_t c, const int32_t* counts) {
-    __shared__ unsigned long long words[kRebuildChunk / 64];
     int n = 0;
     for (int i = blockIdx.x + 1 + threadIdx.x; i < (int)gridDim.x; i += 256) n += counts[i];
     int above;
     block_exclusive<256>(n, &above);
-    list_free<4>(c, blockIdx.x * kRebuildChunk, kRebuildChunk / 256, above, words);
+    list_free<4, kChunkLoads>(c, blockIdx.x * kRebuildChunk, kChunkLoads, above);
 }
 
 static hipError_t rebuild(const dlrm_history_cache_t& c, int32_t* counts, hipStream_t s) {
@@ -469,22 +516,26 @@ static MoveWs move_ws(const dlrm_history_cache_t& c, int32_t* ws) {
 
 // Enters the marked pages into the lists: `before` free pages lie before the
 // wave's first one, `holes` below m.
-__device__ __forceinline__ void list_moves(const dlrm_history_cache_t& c, const MoveWs& w, int base, int words_per_wave,
-                                           int before, int m, int holes, const unsigned long long* words) {
-    const int lane = threadIdx.x & 63, w0 = (threadIdx.x >> 6) * words_per_wave;
-    for (int k = 0; k < words_per_wave; ++k) {
-        const unsigned long long f = words[w0 + k];
-        const int p = base + (w0 + k) * 64 + lane;
-        const int fb = before + __popcll(f & ((1ull << lane) - 1));
-        if (p < c.n_pages) {
+template <int LOADS>
+__device__ __forceinline__ void list_moves(const dlrm_history_cache_t& c, const MoveWs& w, const FreeBits<LOADS>& f,
+                                           int before, int m, int holes) {
+    for (int l = 0; l < f.loads; ++l) {
+        const unsigned b = f.of(l);
+        int all;
+        int fb = before + lanes_below(b, &all);
+        const int p0 = f.p0 + l * 256 + (int)(threadIdx.x & 63) * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int p = p0 + j;
             // used pages before p and at or above m: (p - fb) - (m - holes)
-            if (f >> lane & 1) {
+            if (b >> j & 1) {
                 if (p < m) w.to[fb] = p;
-            } else if (p >= m) {
+                ++fb;
+            } else if (p >= m && p < c.n_pages) {
                 w.from[p - fb - (m - holes)] = p;
             }
         }
-        before += __popcll(f);
+        before += all;
     }
 }
 
@@ -497,17 +548,18 @@ __device__ __forceinline__ void pair_move(const dlrm_history_cache_t& c, const M
 }
 
 __global__ __launch_bounds__(1024) void history_plan_one_kernel(dlrm_history_cache_t c, MoveWs w) {
-    __shared__ unsigned long long words[kOneBlockPages / 64 + 16];
-    const int each = words_each(c.n_pages, 16);
-    const int n = mark_free<16>(c, 0, each, words);
+    const int loads = one_loads(c.n_pages);
+    const FreeBits<kOneLoads> f = mark_free<kOneLoads>(c, 0, loads);
     int total, holes;
-    const int after = after_mine<16>(n, &total);
+    const int after = after_mine<16>(f.n, &total);
     const int m = c.n_pages - total;
     int below = 0;
-    for (int k = threadIdx.x; k * 64 < m; k += 1024)
-        below += __popcll(m - k * 64 >= 64 ? words[k] : words[k] & ((1ull << (m - k * 64)) - 1));
+    for (int l = 0; l < loads; ++l) {
+        const int k = m - (f.p0 + l * 256 + (int)(threadIdx.x & 63) * 4);        // of the lane's pages below m
+        below += __popc(f.of(l) & (k >= 4 ? 15u : (k <= 0 ? 0u : (1u << k) - 1u)));
+    }
     block_exclusive<1024>(below, &holes);
-    list_moves(c, w, 0, each, total - after - n, m, holes, words);
+    list_moves(c, w, f, total - after - f.n, m, holes);
     __threadfence();
     __syncthreads();
     for (int i = threadIdx.x; i < holes; i += 1024) pair_move(c, w, i);
@@ -518,7 +570,6 @@ __global__ __launch_bounds__(1024) void history_plan_one_kernel(dlrm_history_cac
 }
 
 __global__ __launch_bounds__(256) void history_plan_kernel(dlrm_history_cache_t c, MoveWs w, int chunks) {
-    __shared__ unsigned long long words[kRebuildChunk / 64];
     // free pages in all, before this chunk, and below page m
     int n = 0, nb = 0, total, before, sum;
     for (int i = threadIdx.x; i < chunks; i += 256) {
@@ -533,9 +584,9 @@ __global__ __launch_bounds__(256) void history_plan_kernel(dlrm_history_cache_t 
     for (int i = threadIdx.x; i < m_chunk && i < chunks; i += 256) nm += w.counts[i];
     for (int p = m_chunk * kRebuildChunk + threadIdx.x; p < m; p += 256) nm += c.refs[p] == 0 ? 1 : 0;
     block_exclusive<256>(nm, &holes);
-    const int mine = mark_free<4>(c, blockIdx.x * kRebuildChunk, kRebuildChunk / 256, words);
-    const int after = after_mine<4>(mine, &sum);
-    list_moves(c, w, blockIdx.x * kRebuildChunk, kRebuildChunk / 256, before + sum - after - mine, m, holes, words);
+    const FreeBits<kChunkLoads> f = mark_free<kChunkLoads>(c, blockIdx.x * kRebuildChunk, kChunkLoads);
+    const int after = after_mine<4>(f.n, &sum);
+    list_moves(c, w, f, before + sum - after - f.n, m, holes);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *w.n = holes;
         c.counters[0] = total;

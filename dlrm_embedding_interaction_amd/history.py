@@ -10,7 +10,7 @@ from typing import Optional
 
 import torch
 
-from . import _check, _dev, _index_bytes, _stream, _vp, load
+from . import DLRM_OK, _check, _dev, _vp, load
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ALL_EVENTS = 1 << 30    # a window that no history reaches
@@ -47,22 +47,51 @@ def declare(L: ctypes.CDLL) -> None:
 
 def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, dims: int, device: torch.device) -> int:
     """Row stride of (..., heads, head_dim) rows whose heads lie side by side."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if t.dim() != dims:
+    shape = t.shape
+    if len(shape) != dims:
         raise ValueError(f"{name} must have {dims} dimensions")
-    heads, dim = t.shape[-2:]
-    if (dim > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != dim):
+    heads, dim = shape[-2], shape[-1]
+    if t.is_contiguous():
+        return max(heads * dim, 1)
+    stride = t.stride()
+    if (dim > 1 and stride[-1] != 1) or (heads > 1 and stride[-2] != dim):
         raise ValueError(f"the heads of one row of {name} must lie side by side")
-    if dims == 4 and t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
+    if dims == 4 and shape[0] > 1 and shape[1] > 1 and stride[0] != shape[1] * stride[1]:
         raise ValueError(f"{name} must have evenly spaced rows")
     n = t.numel() // max(1, heads * dim)
-    stride = t.stride(0) if dims == 3 or t.shape[1] == 1 else t.stride(1)
-    return stride if n > 1 else max(heads * dim, 1)
+    return (stride[0] if dims == 3 or shape[1] == 1 else stride[1]) if n > 1 else max(heads * dim, 1)
+
+
+def _offsets(t: torch.Tensor, device: torch.device) -> int:
+    """Width of the offsets in bytes."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("offsets must be a CUDA (HIP) tensor")
+    if t.dtype is not torch.int64 and t.dtype is not torch.int32:
+        raise TypeError("offsets must be int32 or int64")
+    if t.dim() != 1 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"offsets must be 1-D and contiguous on {device}")
+    return 8 if t.dtype is torch.int64 else 4
+
+
+_ATTENTION = {}     # descriptors by their values
+
+
+def _attention(dtype, heads, kv, dim, window, sinks, scale):
+    key = (dtype, heads, kv, dim, window, sinks, scale)
+    ref = _ATTENTION.get(key)
+    if ref is None:
+        if len(_ATTENTION) > 1024:
+            _ATTENTION.clear()
+        a = _Attention(DTYPES[dtype], heads, kv, dim, int(window), int(sinks),
+                       dim ** -0.5 if scale is None else float(scale), 0)
+        ref = _ATTENTION[key] = ctypes.byref(a)
+    return ref
 
 
 def _i32(t: torch.Tensor, name: str, device: torch.device) -> torch.Tensor:
@@ -70,6 +99,11 @@ def _i32(t: torch.Tensor, name: str, device: torch.device) -> torch.Tensor:
     if t.dim() != 1 or t.device != device:
         raise ValueError(f"{name} must be 1-D on {device}")
     return t
+
+
+def _stream(device: torch.device) -> int:
+    """The current stream's handle, without the stream object that a call this short would notice."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def history_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
@@ -88,9 +122,7 @@ def history_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets
     n, heads, dim = q.shape
     if k.shape != v.shape or k.shape[0] != n or k.shape[2] != dim:
         raise ValueError("k and v must be (N, n_kv_heads, head_dim) beside q's (N, n_heads, head_dim)")
-    ib = _index_bytes([offsets], [offsets])
-    if offsets.dim() != 1 or offsets.device != dev:
-        raise ValueError(f"offsets must be 1-D on {dev}")
+    ib = _offsets(offsets, dev)
     if padding is not None:
         if padding.dtype == torch.bool:
             padding = padding.view(torch.uint8)
@@ -99,16 +131,17 @@ def history_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets
             raise ValueError("padding must hold one byte for each event")
     if out is None:
         out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
-    ld.append(_rows(out, "out", q.dtype, 3, dev))
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    a = _Attention(DTYPES[q.dtype], heads, k.shape[1], dim, int(window), int(sinks),
-                   dim ** -0.5 if scale is None else float(scale), 0)
-    rc = L.dlrm_history_attention(ctypes.byref(a), offsets.shape[0], n, offsets.data_ptr(), ib, q.data_ptr(), ld[0],
+        ld.append(max(heads * dim, 1))
+    else:
+        ld.append(_rows(out, "out", q.dtype, 3, dev))
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    rc = L.dlrm_history_attention(_attention(q.dtype, heads, k.shape[1], dim, window, sinks, scale), offsets.shape[0], n, offsets.data_ptr(), ib, q.data_ptr(), ld[0],
                                   k.data_ptr(), ld[1], v.data_ptr(), ld[2],
                                   padding.data_ptr() if padding is not None else None, out.data_ptr(), ld[3],
                                   _stream(dev))
-    _check(rc, "dlrm_history_attention")
+    if rc != DLRM_OK:
+        _check(rc, "dlrm_history_attention")
     return out
 
 
@@ -198,9 +231,7 @@ class HistoryCache:
         ld_k, ld_v = (_rows(t, n, k.dtype, 3, self.device) for t, n in ((k, "k"), (v, "v")))
         if k.shape != v.shape or tuple(k.shape[1:]) != (self.n_kv_heads, self.head_dim):
             raise ValueError("k and v must be (N, n_kv_heads, head_dim)")
-        ib = _index_bytes([offsets], [offsets])
-        if offsets.dim() != 1 or offsets.device != self.device:
-            raise ValueError(f"offsets must be 1-D on {self.device}")
+        ib = _offsets(offsets, self.device)
         batch = offsets.shape[0]
         s = _stream(self.device)
         ws = self._workspace(s, batch)
@@ -220,16 +251,17 @@ class HistoryCache:
         ld_q = _rows(q, "q", q.dtype, q.dim(), self.device)
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        ld_out = _rows(out, "out", q.dtype, q.dim(), self.device)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
+            ld_out = max(q.shape[-2] * q.shape[-1], 1)
+        else:
+            ld_out = _rows(out, "out", q.dtype, q.dim(), self.device)
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
         batch, heads, dim = q.shape[0], q.shape[-2], q.shape[-1]
         queries = q.shape[1] if q.dim() == 4 else 1
-        a = _Attention(DTYPES[q.dtype], heads, self.n_kv_heads, dim, int(window), int(sinks),
-                       dim ** -0.5 if scale is None else float(scale), 0)
+        a = _attention(q.dtype, heads, self.n_kv_heads, dim, window, sinks, scale)
         s = _stream(self.device)
         ws = self._workspace(s, batch, queries, heads)
-        rc = load().dlrm_history_lookup(self._ref, ctypes.byref(a), batch, self._slots(slots, batch), queries,
+        rc = load().dlrm_history_lookup(self._ref, a, batch, self._slots(slots, batch), queries,
                                         q.data_ptr(), ld_q, out.data_ptr(), ld_out, ws.data_ptr(), ws.numel(), s)
         _check(rc, "dlrm_history_lookup")
         return out

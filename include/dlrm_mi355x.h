@@ -498,7 +498,7 @@ dlrm_status_t dlrm_history_attention(const dlrm_attention_t* a, int64_t batch, i
  *               holder, in descending order; the last one is taken first
  *   counters    (4): pages in free_pages; histories refused so far (below); two
  *               reserved
- * k and v are 16-byte aligned (DLRM_E_SHAPE otherwise).  In every call, slots
+ * k, v and refs are 16-byte aligned (DLRM_E_SHAPE otherwise).  In every call, slots
  * outside [0, n_slots) are refused: nothing happens for them and counters[1]
  * grows by one; table entries outside [0, n_pages) are events that nothing
  * sees.  No slot may appear twice in one call, nor as source and destination
