@@ -153,12 +153,33 @@ __device__ __forceinline__ Raw<T> load_raw(const T* p) {
     }
     return r;
 }
-// e4m3 codes: two floats to two codes in the low half, and one code to fp32.
-__device__ __forceinline__ unsigned pk_e4m3(float a, float b) {
-    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xffffu;
+// The largest magnitude among elements as bits, without their sign (16-bit
+// types: of the even and of the odd elements).  Infinities and NaN come out above
+// every finite value.
+template <typename T>
+__device__ __forceinline__ void top_magnitude(const Raw<T>& r, unsigned& top) {
+    if constexpr (sizeof(T) == 2) {
+        typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+        typedef unsigned u4 __attribute__((ext_vector_type(4)));
+        const u4 w = __builtin_bit_cast(u4, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            top = __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(us2, top),
+                                                                         __builtin_bit_cast(us2, w[i] & 0x7fff7fffu)));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned w = __builtin_bit_cast(unsigned, r.x[i]) & 0x7fffffffu;
+            top = top > w ? top : w;
+        }
+    }
 }
-__device__ __forceinline__ float e4m3_f32(unsigned code) { return __builtin_amdgcn_cvt_f32_fp8((int)code, 0); }
-
+template <typename T>
+__device__ __forceinline__ bool odd_magnitude(unsigned top) {
+    if constexpr (sizeof(T) == 4) return top >= 0x7f800000u;
+    const unsigned all = __is_same(T, f16) ? 0x7c00u : 0x7f80u;
+    return (top & 0xffffu) >= all || top >> 16 >= all;
+}
 // The smallest power of two s >= 2^kScaleFloor with amax / s <= 448 (the
 // largest e4m3 value, 0.875 x 2^9).  Read off the bits, so exact: amax =
 // m 2^x with m in [1, 2) gives 2^(x - 8) for m <= 1.75 and 2^(x - 7) above.

@@ -91,32 +91,6 @@ __device__ __forceinline__ void to_parts(const Raw<T>& r, shortx8* part) {
         split8<bf16, 3>(r.x, part);
     }
 }
-// The largest exponent field of eight elements, in place: infinities and NaN
-// have every bit of it set.
-template <typename T>
-__device__ __forceinline__ void top_exponent(const Raw<T>& r, unsigned& top) {
-    if constexpr (sizeof(T) == 2) {
-        typedef unsigned short us2 __attribute__((ext_vector_type(2)));
-        typedef unsigned u4 __attribute__((ext_vector_type(4)));
-        const u4 w = __builtin_bit_cast(u4, r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            top = __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(us2, top),
-                                                                         __builtin_bit_cast(us2, w[i] & 0x7fff7fffu)));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const unsigned w = __builtin_bit_cast(unsigned, r.x[i]) & 0x7fffffffu;
-            top = top > w ? top : w;
-        }
-    }
-}
-template <typename T>
-__device__ __forceinline__ bool odd_exponent(unsigned top) {
-    if constexpr (sizeof(T) == 4) return top >= 0x7f800000u;
-    const unsigned all = __is_same(T, f16) ? 0x7c00u : 0x7f80u;
-    return (top & 0xffffu) >= all || top >> 16 >= all;
-}
 template <typename T>
 __device__ __forceinline__ bool finite_bits(T x) {
     if constexpr (sizeof(T) == 4) return (__builtin_bit_cast(unsigned, x) & 0x7f800000u) != 0x7f800000u;
@@ -238,7 +212,7 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
             if (PAD && gone[x] != 0) kr[x] = vr[x] = Raw<T>{};
             to_parts(kr[x], kp);
             to_parts(vr[x], vp);
-            top_exponent(vr[x], big);
+            top_magnitude(vr[x], big);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 *(shortx8*)&ks[i][key][d] = kp[i];
@@ -246,7 +220,7 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
             }
         }
         if (PAD && pad && tid < BN) hides[tid] = hide != 0 ? -INFINITY : 0.f;
-        if (odd_exponent<T>(big)) odd[t & 1] = 1;
+        if (odd_magnitude<T>(big)) odd[t & 1] = 1;
         __syncthreads();
         if (t + 1 < tiles) fetch(t + 1);
         const bool fix = odd[t & 1] != 0;

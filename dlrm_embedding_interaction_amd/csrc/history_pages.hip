@@ -135,9 +135,25 @@ __global__ __launch_bounds__(1024) void history_reserve_kernel(AppendArgs a) {
     }
 }
 
-// Four values as four codes.
-__device__ __forceinline__ unsigned pk_e4m3x4(float a, float b, float c, float d) {
-    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
+// Two values over a power-of-two scale as two codes, into the low or high half.
+typedef short short2v __attribute__((ext_vector_type(2)));
+template <bool HIGH>
+__device__ __forceinline__ short2v code2(short2v w, bf16 a, bf16 b, float s) {
+    typedef bf16 v __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, v{a, b}, s, HIGH);
+}
+template <bool HIGH>
+__device__ __forceinline__ short2v code2(short2v w, f16 a, f16 b, float s) {
+    typedef f16 v __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, v{a, b}, s, HIGH);
+}
+template <bool HIGH>
+__device__ __forceinline__ short2v code2(short2v w, float a, float b, float s) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, s, HIGH);
+}
+template <typename T>
+__device__ __forceinline__ unsigned code4(T a, T b, T c, T d, float s) {
+    return __builtin_bit_cast(unsigned, code2<true>(code2<false>(short2v{}, a, b, s), c, d, s));
 }
 
 // Word k of 16-lane row q goes to word q of row k.
@@ -156,11 +172,39 @@ __device__ __forceinline__ void exchange4(unsigned* w) {
     }
 }
 
-// Four codes of a word times a power of two, rounded to e4m3 again.
-__device__ __forceinline__ unsigned rescale4(unsigned w, float f) {
-    const float x0 = __builtin_amdgcn_cvt_f32_fp8((int)w, 0) * f, x1 = __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * f;
-    const float x2 = __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * f, x3 = __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * f;
-    return pk_e4m3x4(x0, x1, x2, x3);
+// Four codes of a word over a power of two, rounded to e4m3 again.
+__device__ __forceinline__ unsigned rescale4(unsigned w, float s) {
+    return code4(__builtin_amdgcn_cvt_f32_fp8((int)w, 0), __builtin_amdgcn_cvt_f32_fp8((int)w, 1),
+                 __builtin_amdgcn_cvt_f32_fp8((int)w, 2), __builtin_amdgcn_cvt_f32_fp8((int)w, 3), s);
+}
+
+// The element with the largest finite magnitude over the wave: bits decide, and
+// only where they show an infinity or NaN are the elements looked at one by one.
+template <typename T, int N>
+__device__ __forceinline__ float wave_magnitude(const Raw<T>* raw, const bool* in) {
+    unsigned bits = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (in[i]) top_magnitude(raw[i], bits);
+    float top;
+    if constexpr (sizeof(T) == 2) {
+        const unsigned m = (bits & 0xffffu) > bits >> 16 ? bits & 0xffffu : bits >> 16;
+        top = (float)__builtin_bit_cast(T, (unsigned short)m);
+    } else {
+        top = __uint_as_float(bits);
+    }
+    if (__any(odd_magnitude<T>(bits))) {
+        top = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (in[i])
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const float m = fabsf((float)raw[i].x[x]);
+                    top = m < INFINITY ? fmaxf(top, m) : top;
+                }
+    }
+    return wave_max(top);
 }
 
 // Bytes of word w of a 16-event group that lie below event `to` of the group.
@@ -223,23 +267,14 @@ __global__ __launch_bounds__(256, 2) void history_append_kernel(AppendArgs a) {
     float* scales = minor ? c.v_scale : c.k_scale;
     const float was = lo > 0 ? scales[src_h] : 0.f;
 
-    float top = 0.f;
+    bool in[ROUNDS * 4];
 #pragma unroll
-    for (int r = 0; r < ROUNDS; ++r)
-        if (r * EV < hi && (r + 1) * EV > lo)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float m = fabsf((float)raw[r][j].x[i]);
-                    top = m < INFINITY ? fmaxf(top, m) : top;
-                }
-    top = wave_max(top);
+    for (int r = 0; r < ROUNDS * 4; ++r) in[r] = r / 4 * EV < hi && (r / 4 + 1) * EV > lo;
+    const float top = wave_magnitude<T, ROUNDS * 4>(&raw[0][0], in);
     float s = page_scale(top);
     s = was > s ? was : s;
-    const float inv = 1.f / s;                           // a power of two: exact
     const bool rewrite = lo > 0 && (g.copy || s > was);
-    const float grown = rewrite ? was * inv : 1.f;
+    const float grown = rewrite ? s / was : 1.f;         // a power of two: exact
     const int from = rewrite ? 0 : lo;
 
 #pragma unroll
@@ -252,11 +287,9 @@ __global__ __launch_bounds__(256, 2) void history_append_kernel(AppendArgs a) {
                 if (ev < from || ev >= hi) continue;
                 uint2 w;
                 if (ev >= lo) {
-                    float f[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = (float)raw[r][j].x[i] * inv;
-                    w.x = pk_e4m3x4(f[0], f[1], f[2], f[3]);
-                    w.y = pk_e4m3x4(f[4], f[5], f[6], f[7]);
+                    const T* f = raw[r][j].x;
+                    w.x = code4(f[0], f[1], f[2], f[3], s);
+                    w.y = code4(f[4], f[5], f[6], f[7], s);
                 } else {
                     const uint2 o = *(const uint2*)(held + ev * D + ch * 8);
                     w = make_uint2(rescale4(o.x, grown), rescale4(o.y, grown));
@@ -267,8 +300,7 @@ __global__ __launch_bounds__(256, 2) void history_append_kernel(AppendArgs a) {
             unsigned w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                w[i] = pk_e4m3x4((float)raw[r][0].x[i] * inv, (float)raw[r][1].x[i] * inv,
-                                 (float)raw[r][2].x[i] * inv, (float)raw[r][3].x[i] * inv);
+                w[i] = code4(raw[r][0].x[i], raw[r][1].x[i], raw[r][2].x[i], raw[r][3].x[i], s);
             const int e0 = r * EV + 16 * ((lane & 15) / C8);             // the lane's 16 events after the exchange
             exchange4(w);
             exchange4(w + 4);
@@ -295,6 +327,7 @@ __global__ __launch_bounds__(256, 2) void history_append_kernel(AppendArgs a) {
         if (item == 0 && !kept) {
             c.table[(int64_t)slot * c.max_pages + page_no] = dst;
             c.refs[dst] = 1;
+            // the last two holders may both take a copy: the page is then listed as free by the next release
             if (lo > 0) atomicSub(&c.refs[src], 1);
         }
     }
@@ -302,111 +335,113 @@ __global__ __launch_bounds__(256, 2) void history_append_kernel(AppendArgs a) {
 
 // ---- sharing and releasing -----------------------------------------------------
 
-__device__ __forceinline__ void release_entry(const dlrm_history_cache_t& c, int64_t at) {
-    const int p = atomicExch(&c.table[at], -1);
-    if (p >= 0 && p < c.n_pages) atomicSub(&c.refs[p], 1);
+__device__ __forceinline__ void drop_page(const dlrm_history_cache_t& c, int p) {
+    if (p >= 0 && p < c.n_pages) atomicSub(&c.refs[p], 1);      // its result is not waited for
 }
 
-__global__ __launch_bounds__(256) void history_fork_kernel(dlrm_history_cache_t c, const int32_t* src,
-                                                           const int32_t* dst) {
-    const int from = src[blockIdx.x], to = dst[blockIdx.x];
-    if (from < 0 || from >= c.n_slots || to < 0 || to >= c.n_slots) {
-        if (threadIdx.x == 0) atomicAdd(&c.counters[1], 1);
-        return;
-    }
-    if (from == to) return;
-    const int64_t f = (int64_t)from * c.max_pages, t = (int64_t)to * c.max_pages;
-    for (int i = threadIdx.x; i < c.max_pages; i += 256) {
-        const int p = c.table[f + i], o = c.table[t + i];
-        if (p == o) continue;
-        c.table[t + i] = p;
-        if (p >= 0 && p < c.n_pages) atomicAdd(&c.refs[p], 1);
-        if (o >= 0 && o < c.n_pages) atomicSub(&c.refs[o], 1);
-    }
-    if (threadIdx.x == 0) c.lens[to] = c.lens[from];
-}
-
-__global__ __launch_bounds__(256) void history_truncate_kernel(dlrm_history_cache_t c, const int32_t* slots,
-                                                               const int32_t* new_lens) {
-    const int slot = slots[blockIdx.x], want = new_lens ? new_lens[blockIdx.x] : 0, pe = c.page_events;
-    const int sh = 31 - __builtin_clz(pe);
-    bool ok = slot >= 0 && slot < c.n_slots && want >= 0;
-    if (ok) ok = want <= c.lens[slot] && want <= (int64_t)c.max_pages * pe;
-    const int64_t row = (int64_t)slot * c.max_pages;
-    // the page that would be filled further may have been trimmed away
-    if (ok && (want & (pe - 1))) ok = c.table[row + (want >> sh)] >= 0;
-    __syncthreads();  // every thread has read the length
-    if (!ok) {
-        if (threadIdx.x == 0) atomicAdd(&c.counters[1], 1);
-        return;
-    }
-    for (int i = (want >> sh) + (want & (pe - 1) ? 1 : 0) + (int)threadIdx.x; i < c.max_pages; i += 256)
-        release_entry(c, row + i);
-    if (threadIdx.x == 0) c.lens[slot] = want;
-}
-
-__global__ __launch_bounds__(256) void history_trim_kernel(dlrm_history_cache_t c, const int32_t* slots,
-                                                           int64_t window, int64_t sinks) {
-    const int slot = slots[blockIdx.x], pe = c.page_events;
-    if (slot < 0 || slot >= c.n_slots) {
-        if (threadIdx.x == 0) atomicAdd(&c.counters[1], 1);
-        return;
-    }
-    const int64_t row = (int64_t)slot * c.max_pages;
-    // pages whose events all lie behind the sinks and before the window
-    const int64_t lo = sinks < (int64_t)c.max_pages * pe ? (sinks + pe - 1) / pe : c.max_pages;
-    int64_t hi = c.lens[slot] > window ? (c.lens[slot] - window) / pe : 0;
-    hi = hi < c.max_pages ? hi : c.max_pages;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += 256) release_entry(c, row + i);
-}
-
-// The free pages of a wave's share of a block, loads of 256 consecutive pages
-// at a time: four bits for each load, of the lane's four pages.
-template <int LOADS>
-struct FreeBits {
-    unsigned bits[(LOADS + 7) / 8];
-    int n;              // in the wave's share
-    int p0, loads;      // the share's first page, its loads
-    __device__ __forceinline__ unsigned of(int l) const {
-        unsigned b = bits[0];
-#pragma unroll
-        for (int i = 1; i < (LOADS + 7) / 8; ++i) b = l >> 3 == i ? bits[i] : b;
-        return b >> (4 * (l & 7)) & 15u;
-    }
+// One block per history.  The list is written by a kernel of its own: a last
+// block that wrote it here would need every block to write its caches back first,
+// which took 10 to 40 us more than the second launch.
+enum Release { kFork, kTruncate, kTrim };
+struct ReleaseArgs {
+    dlrm_history_cache_t c;
+    const int32_t *slots, *other;       // fork: sources, destinations; truncate: slots, new lengths
+    int64_t window, sinks;
+    int n;
 };
 
-template <int LOADS>
-__device__ __forceinline__ FreeBits<LOADS> mark_free(const dlrm_history_cache_t& c, int base, int loads) {
-    FreeBits<LOADS> f;
-    const int lane = threadIdx.x & 63;
-    f.p0 = base + (int)(threadIdx.x >> 6) * loads * 256;
-    f.loads = loads;
-    f.n = 0;
-#pragma unroll
-    for (int l0 = 0; l0 < LOADS; l0 += 8) {
-        int4 r[8];
-        unsigned b = 0;
-#pragma unroll
-        for (int l = 0; l < 8; ++l) {
-            const int p = f.p0 + (l0 + l) * 256 + lane * 4;
-            r[l] = l0 + l < loads && p + 3 < c.n_pages ? *(const int4*)(c.refs + p) : make_int4(1, 1, 1, 1);
-        }
-#pragma unroll
-        for (int l = 0; l < 8; ++l) {
-            const int p = f.p0 + (l0 + l) * 256 + lane * 4;
-            if (l0 + l < loads && p < c.n_pages && p + 3 >= c.n_pages) {
-                r[l].x = c.refs[p];
-                if (p + 1 < c.n_pages) r[l].y = c.refs[p + 1];
-                if (p + 2 < c.n_pages) r[l].z = c.refs[p + 2];
+template <Release OP>
+__global__ __launch_bounds__(256) void history_release_kernel(ReleaseArgs a) {
+    const int i = blockIdx.x, tid = threadIdx.x;
+    const dlrm_history_cache_t& c = a.c;
+    const int sh = 31 - __builtin_clz(c.page_events);
+    const int slot = a.slots[i];
+    bool ok = slot >= 0 && slot < c.n_slots;
+    if constexpr (OP == kFork) {
+        const int to = a.other[i];
+        ok = ok && to >= 0 && to < c.n_slots;
+        if (ok && slot != to) {
+            const int64_t f = (int64_t)slot * c.max_pages, t = (int64_t)to * c.max_pages;
+            const int len = c.lens[slot];
+            for (int x = tid; x < c.max_pages; x += 256) {
+                const int p = c.table[f + x], o = c.table[t + x];
+                if (p == o) continue;
+                c.table[t + x] = p;
+                if (p >= 0 && p < c.n_pages) atomicAdd(&c.refs[p], 1);
+                drop_page(c, o);
             }
-            b |= ((r[l].x == 0 ? 1u : 0u) | (r[l].y == 0 ? 2u : 0u) | (r[l].z == 0 ? 4u : 0u) |
-                  (r[l].w == 0 ? 8u : 0u)) << (4 * l);
+            if (tid == 0) c.lens[to] = len;
         }
-        f.bits[l0 / 8] = b;
-        f.n += __popc(b);
+    } else {
+        const int len = ok ? c.lens[slot] : 0;
+        const int64_t row = (int64_t)slot * c.max_pages;
+        int lo, hi = c.max_pages;
+        if constexpr (OP == kTruncate) {
+            const int want = a.other ? a.other[i] : 0, mask = c.page_events - 1;
+            ok = ok && want >= 0 && want <= len && want <= c.max_pages << sh;
+            // the page that would be filled further may have been trimmed away
+            if (ok && (want & mask)) ok = c.table[row + (want >> sh)] >= 0;
+            lo = ok ? (want + mask) >> sh : hi;
+            __syncthreads();            // every thread has read the length
+            if (ok && tid == 0) c.lens[slot] = want;
+        } else {
+            // pages whose events all lie behind the sinks and before the window
+            lo = a.sinks < (int64_t)c.max_pages << sh ? (int)((a.sinks + c.page_events - 1) >> sh) : hi;
+            const int64_t end = len > a.window ? (len - a.window) >> sh : 0;
+            hi = ok && end < hi ? (int)end : (ok ? hi : 0);
+        }
+        for (int x = lo + tid; x < hi; x += 256) {
+            const int p = c.table[row + x];
+            if (p == -1) continue;
+            c.table[row + x] = -1;
+            drop_page(c, p);
+        }
     }
+    if (!ok && tid == 0) atomicAdd(&c.counters[1], 1);
+}
+
+// The free pages of a wave's share of a block, at most 64 words of 64 pages: lane
+// k keeps word k, and the free pages of the words above it.
+struct FreeWords {
+    unsigned long long word;
+    int above, n;           // free pages in the words above mine, in all
+    int p0, words;          // the share's first page, its words
+    __device__ __forceinline__ unsigned long long of(int k) const {
+        const unsigned lo = __builtin_amdgcn_readlane((unsigned)word, k);
+        const unsigned hi = __builtin_amdgcn_readlane((unsigned)(word >> 32), k);
+        return (unsigned long long)hi << 32 | lo;
+    }
+    __device__ __forceinline__ int above_of(int k) const { return __builtin_amdgcn_readlane(above, k); }
+};
+
+__device__ __forceinline__ FreeWords mark_free(const dlrm_history_cache_t& c, int base, int words) {
+    constexpr int AT_ONCE = 16;
+    FreeWords f;
+    const int lane = threadIdx.x & 63;
+    f.p0 = base + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * words * 64;
+    f.words = words;
+    f.word = 0;
+    for (int k0 = 0; k0 < words; k0 += AT_ONCE) {
+        int r[AT_ONCE];
 #pragma unroll
-    for (int d = 32; d; d >>= 1) f.n += __shfl_xor(f.n, d, 64);
+        for (int i = 0; i < AT_ONCE; ++i)
+            r[i] = c.refs[min(f.p0 + (k0 + i) * 64 + lane, c.n_pages - 1)];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const unsigned long long m =
+                __ballot(r[i] == 0 && k0 + i < words && f.p0 + (k0 + i) * 64 + lane < c.n_pages);
+            f.word = lane == k0 + i ? m : f.word;
+        }
+    }
+    const int mine = __popcll(f.word);
+    int sum = mine;                     // of the words from mine up
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_down(sum, d, 64);
+        if (lane + d < 64) sum += o;
+    }
+    f.above = sum - mine;
+    f.n = __builtin_amdgcn_readlane(sum, 0);
     return f;
 }
 
@@ -427,51 +462,30 @@ __device__ __forceinline__ int after_mine(int n, int* total) {
     return after;
 }
 
-// Free pages of one load: of the lanes below mine, and of all.
-__device__ __forceinline__ int lanes_below(unsigned b, int* total) {
-    const unsigned long long lt = (1ull << (threadIdx.x & 63)) - 1;
-    int below = 0, all = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const unsigned long long m = __ballot(b >> j & 1);
-        below += __popcll(m & lt);
-        all += __popcll(m);
-    }
-    *total = all;
-    return below;
-}
-
 // Free page p goes to the place that counts the free pages above it.
-template <int WAVES, int LOADS>
-__device__ __forceinline__ void list_free(const dlrm_history_cache_t& c, int base, int loads, int above) {
-    const FreeBits<LOADS> f = mark_free<LOADS>(c, base, loads);
+template <int WAVES>
+__device__ __forceinline__ void list_free(const dlrm_history_cache_t& c, int base, int words, int above) {
+    const FreeWords f = mark_free(c, base, words);
     int total;
-    int at = above + after_mine<WAVES>(f.n, &total);
-    for (int l = loads - 1; l >= 0; --l) {
-        const unsigned b = f.of(l);
-        int all;
-        const int below = lanes_below(b, &all);
-        int to = at + all - below - __popc(b);          // free pages above the lane's last
-        const int p = f.p0 + l * 256 + (int)(threadIdx.x & 63) * 4;
-#pragma unroll
-        for (int j = 3; j >= 0; --j)
-            if (b >> j & 1) c.free_pages[to++] = p + j;
-        at += all;
+    const int at = above + after_mine<WAVES>(f.n, &total), lane = threadIdx.x & 63;
+    for (int k = 0; k < words; ++k) {
+        const unsigned long long m = f.of(k);
+        if (m >> lane & 1) c.free_pages[at + f.above_of(k) + __popcll(m >> lane >> 1)] = f.p0 + k * 64 + lane;
     }
     if (base == 0 && threadIdx.x == 0) c.counters[0] = above + total;
 }
 
-constexpr int kChunkLoads = kRebuildChunk / 1024;        // of each of four waves
-constexpr int kOneLoads = kOneBlockPages / 4096;         // of each of sixteen waves
-__device__ __forceinline__ int one_loads(int n_pages) { return (n_pages + 4095) / 4096; }
+constexpr int kChunkWords = kRebuildChunk / 256;         // of each of four waves
+// Words of each of sixteen waves; a pool that one block lists has at most 64.
+__device__ __forceinline__ int one_words(int n_pages) { return (n_pages + 1023) / 1024; }
 
 __global__ __launch_bounds__(1024) void history_rebuild_one_kernel(dlrm_history_cache_t c) {
-    list_free<16, kOneLoads>(c, 0, one_loads(c.n_pages), 0);
+    list_free<16>(c, 0, one_words(c.n_pages), 0);
 }
 
 // Free pages of each chunk.
 __global__ __launch_bounds__(256) void history_count_kernel(dlrm_history_cache_t c, int32_t* counts) {
-    const FreeBits<kChunkLoads> f = mark_free<kChunkLoads>(c, blockIdx.x * kRebuildChunk, kChunkLoads);
+    const FreeWords f = mark_free(c, blockIdx.x * kRebuildChunk, kChunkWords);
     int total;
     after_mine<4>(f.n, &total);
     if (threadIdx.x == 0) counts[blockIdx.x] = total;
@@ -482,16 +496,18 @@ __global__ __launch_bounds__(256) void history_rebuild_kernel(dlrm_history_cache
     for (int i = blockIdx.x + 1 + threadIdx.x; i < (int)gridDim.x; i += 256) n += counts[i];
     int above;
     block_exclusive<256>(n, &above);
-    list_free<4, kChunkLoads>(c, blockIdx.x * kRebuildChunk, kChunkLoads, above);
+    list_free<4>(c, blockIdx.x * kRebuildChunk, kChunkWords, above);
 }
 
-static hipError_t rebuild(const dlrm_history_cache_t& c, int32_t* counts, hipStream_t s) {
-    if (c.n_pages <= kOneBlockPages) {
-        hipLaunchKernelGGL(history_rebuild_one_kernel, dim3(1), dim3(1024), 0, s, c);
+template <Release OP>
+static hipError_t release(const ReleaseArgs& a, int32_t* counts, hipStream_t s) {
+    hipLaunchKernelGGL(history_release_kernel<OP>, dim3(a.n), dim3(256), 0, s, a);
+    if (a.c.n_pages <= kOneBlockPages) {
+        hipLaunchKernelGGL(history_rebuild_one_kernel, dim3(1), dim3(1024), 0, s, a.c);
     } else {
-        const int n = rebuild_chunks(c.n_pages);
-        hipLaunchKernelGGL(history_count_kernel, dim3(n), dim3(256), 0, s, c, counts);
-        hipLaunchKernelGGL(history_rebuild_kernel, dim3(n), dim3(256), 0, s, c, counts);
+        const int n = rebuild_chunks(a.c.n_pages);
+        hipLaunchKernelGGL(history_count_kernel, dim3(n), dim3(256), 0, s, a.c, counts);
+        hipLaunchKernelGGL(history_rebuild_kernel, dim3(n), dim3(256), 0, s, a.c, counts);
     }
     return hipGetLastError();
 }
@@ -516,26 +532,19 @@ static MoveWs move_ws(const dlrm_history_cache_t& c, int32_t* ws) {
 
 // Enters the marked pages into the lists: `before` free pages lie before the
 // wave's first one, `holes` below m.
-template <int LOADS>
-__device__ __forceinline__ void list_moves(const dlrm_history_cache_t& c, const MoveWs& w, const FreeBits<LOADS>& f,
+__device__ __forceinline__ void list_moves(const dlrm_history_cache_t& c, const MoveWs& w, const FreeWords& f,
                                            int before, int m, int holes) {
-    for (int l = 0; l < f.loads; ++l) {
-        const unsigned b = f.of(l);
-        int all;
-        int fb = before + lanes_below(b, &all);
-        const int p0 = f.p0 + l * 256 + (int)(threadIdx.x & 63) * 4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int p = p0 + j;
-            // used pages before p and at or above m: (p - fb) - (m - holes)
-            if (b >> j & 1) {
-                if (p < m) w.to[fb] = p;
-                ++fb;
-            } else if (p >= m && p < c.n_pages) {
-                w.from[p - fb - (m - holes)] = p;
-            }
+    const int lane = threadIdx.x & 63;
+    for (int k = 0; k < f.words; ++k) {
+        const unsigned long long b = f.of(k);
+        const int p = f.p0 + k * 64 + lane;
+        const int fb = before + f.n - f.above_of(k) - __popcll(b >> lane);      // free pages before p
+        // used pages before p and at or above m: (p - fb) - (m - holes)
+        if (b >> lane & 1) {
+            if (p < m) w.to[fb] = p;
+        } else if (p >= m && p < c.n_pages) {
+            w.from[p - fb - (m - holes)] = p;
         }
-        before += all;
     }
 }
 
@@ -548,19 +557,15 @@ __device__ __forceinline__ void pair_move(const dlrm_history_cache_t& c, const M
 }
 
 __global__ __launch_bounds__(1024) void history_plan_one_kernel(dlrm_history_cache_t c, MoveWs w) {
-    const int loads = one_loads(c.n_pages);
-    const FreeBits<kOneLoads> f = mark_free<kOneLoads>(c, 0, loads);
+    const FreeWords f = mark_free(c, 0, one_words(c.n_pages));
     int total, holes;
     const int after = after_mine<16>(f.n, &total);
     const int m = c.n_pages - total;
-    int below = 0;
-    for (int l = 0; l < loads; ++l) {
-        const int k = m - (f.p0 + l * 256 + (int)(threadIdx.x & 63) * 4);        // of the lane's pages below m
-        below += __popc(f.of(l) & (k >= 4 ? 15u : (k <= 0 ? 0u : (1u << k) - 1u)));
-    }
+    const int k = m - (f.p0 + (int)(threadIdx.x & 63) * 64);     // of the lane's word: pages below m
+    const int below = __popcll(f.word & (k >= 64 ? ~0ull : (k <= 0 ? 0ull : (1ull << k) - 1)));
     block_exclusive<1024>(below, &holes);
     list_moves(c, w, f, total - after - f.n, m, holes);
-    __threadfence();
+    __threadfence_block();      // the lists are read by other threads of the block
     __syncthreads();
     for (int i = threadIdx.x; i < holes; i += 1024) pair_move(c, w, i);
     if (threadIdx.x == 0) {
@@ -584,7 +589,7 @@ __global__ __launch_bounds__(256) void history_plan_kernel(dlrm_history_cache_t 
     for (int i = threadIdx.x; i < m_chunk && i < chunks; i += 256) nm += w.counts[i];
     for (int p = m_chunk * kRebuildChunk + threadIdx.x; p < m; p += 256) nm += c.refs[p] == 0 ? 1 : 0;
     block_exclusive<256>(nm, &holes);
-    const FreeBits<kChunkLoads> f = mark_free<kChunkLoads>(c, blockIdx.x * kRebuildChunk, kChunkLoads);
+    const FreeWords f = mark_free(c, blockIdx.x * kRebuildChunk, kChunkWords);
     const int after = after_mine<4>(f.n, &sum);
     list_moves(c, w, f, before + sum - after - f.n, m, holes);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -672,23 +677,17 @@ hipError_t launch_history_append(const AppendArgs& a, int dtype, hipStream_t s) 
 
 hipError_t launch_history_fork(const dlrm_history_cache_t& c, int n, const int32_t* src, const int32_t* dst,
                                int32_t* counts, hipStream_t s) {
-    hipLaunchKernelGGL(history_fork_kernel, dim3(n), dim3(256), 0, s, c, src, dst);
-    hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : rebuild(c, counts, s);
+    return release<kFork>(ReleaseArgs{c, src, dst, 0, 0, n}, counts, s);
 }
 
 hipError_t launch_history_truncate(const dlrm_history_cache_t& c, int n, const int32_t* slots,
                                    const int32_t* new_lens, int32_t* counts, hipStream_t s) {
-    hipLaunchKernelGGL(history_truncate_kernel, dim3(n), dim3(256), 0, s, c, slots, new_lens);
-    hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : rebuild(c, counts, s);
+    return release<kTruncate>(ReleaseArgs{c, slots, new_lens, 0, 0, n}, counts, s);
 }
 
 hipError_t launch_history_trim(const dlrm_history_cache_t& c, int n, const int32_t* slots, int64_t window,
                                int64_t sinks, int32_t* counts, hipStream_t s) {
-    hipLaunchKernelGGL(history_trim_kernel, dim3(n), dim3(256), 0, s, c, slots, window, sinks);
-    hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : rebuild(c, counts, s);
+    return release<kTrim>(ReleaseArgs{c, slots, nullptr, window, sinks, n}, counts, s);
 }
 
 hipError_t launch_history_compact(const dlrm_history_cache_t& c, int32_t* ws, hipStream_t s) {
