@@ -39,19 +39,30 @@ struct LookupArgs {
     float scale;
 };
 
-// What the reservation decided for one history of an append: its events
-// before (-1: refused), the free-list position of its first new page, the page
-// that holds its last part (-1: none), and whether that page is copied because
-// other histories hold it too.
-struct Grant {
-    int old_len, pos, src, copy;
+// What one history of an append needs: its events before (-1: refused), the
+// page that holds its last part (-1: none), whether that page is copied because
+// other histories hold it too, and how many pages it takes from the list.
+struct Need {
+    int old_len, src, copy, pages;
 };
+constexpr int kNeedBlock = 256;      // histories whose needs are summed together
+
+// The needs of all histories, the sums of their pages for each kNeedBlock of them
+// and the refusals among them, and the length of the free list before the call.
+struct NeedWs {
+    Need* need;
+    int2* sums;
+    int* n_free;
+};
+inline size_t need_bytes(int64_t batch) {
+    return (size_t)batch * sizeof(Need) + ((size_t)batch / kNeedBlock + 1) * sizeof(int2) + 16;
+}
 
 struct AppendArgs {
     dlrm_history_cache_t c;
     const int32_t* slots;
     const void *k, *v, *offsets;
-    Grant* grants;
+    NeedWs ws;
     int64_t ld_k, ld_v, n_events;
     int batch, idx32;
 };

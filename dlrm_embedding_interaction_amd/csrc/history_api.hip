@@ -62,8 +62,8 @@ size_t compact_bytes(const dlrm_history_cache_t* c) {
 
 size_t workspace_bytes(const dlrm_history_cache_t* c, int64_t batch, int32_t queries, int32_t n_heads) {
     size_t n = compact_bytes(c);
-    const size_t grants = round256((size_t)batch * sizeof(Grant));
-    n = grants > n ? grants : n;
+    const size_t needs = round256(need_bytes(batch));
+    n = needs > n ? needs : n;
     if (queries > 0) {
         const size_t l = round256(lookup_workspace_bytes(*c, batch, queries, n_heads));
         n = l > n ? l : n;
@@ -133,12 +133,14 @@ DLRM_API dlrm_status_t dlrm_history_append(const dlrm_history_cache_t* c, int64_
     if (!offsets || (n_events > 0 && (!k || !v))) return DLRM_E_NULL;
     const int64_t w = (int64_t)c->n_kv_heads * c->head_dim;
     if (ld_k < w || ld_v < w) return DLRM_E_SHAPE;
-    st = check_workspace(workspace, ws_bytes, round256((size_t)batch * sizeof(Grant)));
+    st = check_workspace(workspace, ws_bytes, round256(need_bytes(batch)));
     if (st != DLRM_OK) return st;
     AppendArgs a = {};
     a.c = *c;
     a.slots = slots, a.k = k, a.v = v, a.offsets = offsets;
-    a.grants = (Grant*)workspace;
+    a.ws.need = (Need*)workspace;
+    a.ws.sums = (int2*)(a.ws.need + batch);
+    a.ws.n_free = (int*)(a.ws.sums + batch / kNeedBlock + 1);
     a.ld_k = ld_k, a.ld_v = ld_v, a.n_events = n_events;
     a.batch = (int)batch, a.idx32 = index_bytes == 4;
     return from_hip(launch_history_append(a, dtype, (hipStream_t)stream));

@@ -115,18 +115,18 @@ struct Tile {
     bool kin, vin;                                      // the pages are there
 };
 
-// DIRECT: one block per (history, chunk of rows), its waves taking every fourth
-// tile and joining their results through LDS.
-template <int D, int PE, typename T, bool DIRECT>
-__global__ __launch_bounds__(256, 2) void history_lookup_kernel(LookupArgs a, int n_waves, int* __restrict__ meta) {
+// DIRECT waves: one block of so many per (history, chunk of rows), its waves taking
+// every DIRECT-th tile and joining their results through LDS.  0: runs of tiles.
+template <int D, int PE, typename T, int DIRECT>
+__global__ __launch_bounds__(DIRECT ? 64 * DIRECT : 256, 2) void history_lookup_kernel(LookupArgs a, int n_waves, int* __restrict__ meta) {
     constexpr int NQ = Parts<T>::q, NP = Parts<T>::p;
     constexpr int KS = D / 32;                          // 32-element steps of the first product
     constexpr int PT = kTile / PE;                      // pages per tile
     constexpr int OP = D + 4;                           // row stride of the joined results
     __shared__ int before[DIRECT ? 1 : 256];
     __shared__ int wsum[4];
-    __shared__ __attribute__((aligned(16))) float part_o[DIRECT ? 4 * 16 * OP : 4];
-    __shared__ float part_m[64], part_l[64];
+    __shared__ __attribute__((aligned(16))) float part_o[DIRECT > 1 ? DIRECT * 16 * OP : 4];
+    __shared__ float part_m[16 * (DIRECT + 1)], part_l[16 * (DIRECT + 1)];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = lane & 15, g = lane >> 4;
     const int group = a.n_heads / a.c.n_kv_heads, rows = a.queries * group;
@@ -181,10 +181,10 @@ __global__ __launch_bounds__(256, 2) void history_lookup_kernel(LookupArgs a, in
             ++b;
             continue;
         }
-        // the wave's tiles of the history: a run, or every fourth
+        // the wave's tiles of the history: a run, or every DIRECT-th
         const int i0 = DIRECT ? wave : at - start;
         const int i1 = DIRECT || sp.count < stop - start ? sp.count : stop - start;
-        constexpr int STEP = DIRECT ? 4 : 1;
+        constexpr int STEP = DIRECT ? DIRECT : 1;
         if (!DIRECT && i0 == 0 && blockIdx.y == 0 && lane == 0) meta[b] = start;
         const int slot = a.slots ? a.slots[b] : b;
         const int32_t* table = a.c.table + (int64_t)slot * a.c.max_pages;
@@ -330,29 +330,34 @@ __global__ __launch_bounds__(256, 2) void history_lookup_kernel(LookupArgs a, in
         l += swizzle_xor16(l);
         l += __shfl_xor(l, 32, 64);
 
-        if constexpr (DIRECT) {
+        if constexpr (DIRECT > 1) {
             if (g == 0) part_m[wave * 16 + n] = m;
             __syncthreads();
-            const float mx = fmaxf(fmaxf(part_m[n], part_m[16 + n]), fmaxf(part_m[32 + n], part_m[48 + n]));
+            float mx = part_m[n];
+#pragma unroll
+            for (int i = 1; i < DIRECT; ++i) mx = fmaxf(mx, part_m[16 * i + n]);
             const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mx);
             if (g == 0) part_l[wave * 16 + n] = l * f;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) *(floatx4*)&part_o[(wave * 16 + n) * OP + 16 * j + 4 * g] = o[j] * f;
             __syncthreads();
-            for (int x = tid; x < 4 * D; x += 256) {
+            for (int x = tid; x < 4 * D; x += 64 * DIRECT) {
                 const int y = x / (D / 4), d = x % (D / 4) * 4, row = r - n + y;
                 if (row >= rows) break;
-                const float sum = part_l[y] + part_l[16 + y] + part_l[32 + y] + part_l[48 + y];
+                float sum = part_l[y];
                 floatx4 v = *(const floatx4*)&part_o[y * OP + d];
 #pragma unroll
-                for (int i = 1; i < 4; ++i) v += *(const floatx4*)&part_o[(16 * i + y) * OP + d];
+                for (int i = 1; i < DIRECT; ++i) {
+                    sum += part_l[16 * i + y];
+                    v += *(const floatx4*)&part_o[(16 * i + y) * OP + d];
+                }
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 T* op = (T*)a.out + ((int64_t)b * a.queries + row / group) * a.ld_out +
                         (int64_t)(hk * group + row % group) * D + d;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) op[i] = (T)(sum == 0.f ? 0.f : v[i] * inv);
             }
-        } else if (i0 == 0 && i1 == sp.count) {
+        } else if (DIRECT || (i0 == 0 && i1 == sp.count)) {
             if (live) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 T* op = (T*)a.out + qrow * a.ld_out + (int64_t)qhead * D;
@@ -434,6 +439,16 @@ size_t lookup_workspace_bytes(const dlrm_history_cache_t& c, int64_t batch, int 
            (size_t)2 * waves_of(c, batch, queries, n_heads) * hc * cols * (c.head_dim + 2) * sizeof(float);
 }
 
+// Waves of a history's block: as many as let every block be resident at once (a
+// CU holds 8 such waves at 128 elements per head, 12 below).  1024 blocks of up to
+// 18 tiles: 2 waves 33 us, 1 or 4 42; 384 blocks of up to 24: 4 waves 18.7 us, 2 or 8 24-25.
+static int direct_waves(int64_t blocks, int dim) {
+    const int room = dim == 128 ? 8 : 12;
+    int w = 8;
+    while (w > 1 && blocks > 256 * (room / w)) w /= 2;
+    return w;
+}
+
 // A history's visible tiles at most, as the host can tell.
 static int64_t most_tiles(const LookupArgs& a) {
     const int64_t span = ((int64_t)a.c.max_pages * a.c.page_events + kTile - 1) / kTile;
@@ -449,11 +464,16 @@ static hipError_t launch_t(LookupArgs a, hipStream_t s) {
     int* meta = (int*)a.partial;
     a.partial = (float*)((char*)a.partial + meta_bytes(a.batch));
     if (most_tiles(a) <= kDirectTiles) {
-        hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, true>), dim3(a.batch, hc), dim3(256), 0, s, a, 0, meta);
+        const dim3 grid(a.batch, hc);
+        const int w = direct_waves((int64_t)a.batch * hc, D);
+        if (w == 8) hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 8>), grid, dim3(512), 0, s, a, 0, meta);
+        else if (w == 4) hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 4>), grid, dim3(256), 0, s, a, 0, meta);
+        else if (w == 2) hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 2>), grid, dim3(128), 0, s, a, 0, meta);
+        else hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 1>), grid, dim3(64), 0, s, a, 0, meta);
         return hipGetLastError();
     }
     const int waves = waves_of(a.c, a.batch, a.queries, a.n_heads);
-    hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, false>), dim3(waves / 4, hc), dim3(256), 0, s, a, waves, meta);
+    hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 0>), dim3(waves / 4, hc), dim3(256), 0, s, a, waves, meta);
     hipLaunchKernelGGL((history_join_kernel<D, T>), dim3(a.batch, hc), dim3(256), 0, s, a, meta);
     return hipGetLastError();
 }

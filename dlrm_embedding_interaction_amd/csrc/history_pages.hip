@@ -51,87 +51,99 @@ __global__ __launch_bounds__(256) void history_init_kernel(dlrm_history_cache_t 
 
 // ---- append ------------------------------------------------------------------
 
-// Pages for every history of the call, by one block: a history needs the pages
-// its events open, and one more where its last page is part filled and shared.
-// Needs are summed in batch order; a history whose sum passes the free count is
-// refused whole.  Nothing here changes refs or the table, so that every history
-// of the call sees them as they were before it.  What it takes is the chain
-// slot -> length -> page -> holders of dependent reads: four histories per thread
-// go through it together.
-__global__ __launch_bounds__(1024) void history_reserve_kernel(AppendArgs a) {
-    constexpr int PER = 4;
+// What each history needs, one thread each: the pages its events open, and one
+// more where its last page is part filled and shared.  Nothing here changes refs,
+// lengths or the table, so that every history of the call sees them as they were
+// before it.  What it takes is the chain slot -> length -> page -> holders of
+// dependent reads, spread over as many CUs as there are blocks.
+__global__ __launch_bounds__(kNeedBlock) void history_need_kernel(AppendArgs a) {
     const dlrm_history_cache_t& c = a.c;
-    __shared__ int refused, taken;
-    if (threadIdx.x == 0) refused = taken = 0;
-    __syncthreads();
-    const int n_free = c.counters[0], sh = 31 - __builtin_clz(c.page_events), mask = c.page_events - 1;
-    const int most = c.max_pages << sh;
-    int carry = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 1024 * PER) {
-        int need[PER], src[PER], copy[PER], slot[PER], old[PER], sum = 0;
-        int64_t begin[PER], end[PER];
-        bool ok[PER];
-        // every read is of something that is there, whether it is used or not: reads under conditions would wait
-        // for one another
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int b = min(b0 + (int)threadIdx.x * PER + i, a.batch - 1);
-            slot[i] = a.slots ? a.slots[b] : b;
-            begin[i] = ld_index(a.offsets, b, a.idx32);
-            end[i] = ld_index(a.offsets, min(b + 1, a.batch - 1), a.idx32);
+    const int b = blockIdx.x * kNeedBlock + threadIdx.x, pe = c.page_events;
+    const int sh = 31 - __builtin_clz(pe), mask = pe - 1;
+    Need d = {-1, -1, 0, 0};
+    bool ok = false;
+    if (b < a.batch) {
+        const int slot = a.slots ? a.slots[b] : b;
+        const int64_t begin = history_begin(a.offsets, a.idx32, b, a.n_events);
+        const int64_t count = history_end(a.offsets, a.idx32, b, a.batch, begin, a.n_events) - begin;
+        if (slot >= 0 && slot < c.n_slots) {
+            d.old_len = c.lens[slot];
+            ok = d.old_len >= 0 && d.old_len + count <= (int64_t)c.max_pages << sh;
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int b = b0 + (int)threadIdx.x * PER + i;
-            if (b + 1 >= a.batch) end[i] = a.n_events;
-            begin[i] = begin[i] < 0 ? 0 : (begin[i] > a.n_events ? a.n_events : begin[i]);
-            end[i] = end[i] < begin[i] ? begin[i] : (end[i] > a.n_events ? a.n_events : end[i]);
-            ok[i] = b < a.batch && slot[i] >= 0 && slot[i] < c.n_slots;
-            slot[i] = ok[i] ? slot[i] : 0;
-            old[i] = c.lens[slot[i]];
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            ok[i] = ok[i] && old[i] >= 0 && old[i] + (end[i] - begin[i]) <= most;
-            old[i] = ok[i] ? old[i] : 0;
-            src[i] = c.table[(int64_t)slot[i] * c.max_pages + min(old[i] >> sh, c.max_pages - 1)];
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const bool part = end[i] > begin[i] && (old[i] & mask) != 0, in = src[i] >= 0 && src[i] < c.n_pages;
-            copy[i] = c.refs[in ? src[i] : 0] > 1 && part && in;
-            if (part) ok[i] = ok[i] && in;
-            else src[i] = -1;
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int count = (int)(end[i] - begin[i]);
-            need[i] = ok[i] && count > 0 ? ((old[i] + count + mask) >> sh) - ((old[i] + mask) >> sh) + copy[i] : 0;
-            sum += need[i];
-        }
-        int total;
-        int before = carry + block_exclusive<1024>(sum, &total);
-        carry += total;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int b = b0 + threadIdx.x * PER + i;
-            if (b < a.batch) {
-                const bool granted = ok[i] && (need[i] == 0 || before + need[i] <= n_free);
-                a.grants[b] = Grant{granted ? old[i] : -1, n_free - 1 - before, src[i], copy[i]};
-                if (granted) {
-                    if (end[i] > begin[i]) c.lens[slot[i]] = old[i] + (int)(end[i] - begin[i]);
-                    if (need[i]) atomicMax(&taken, before + need[i]);
-                } else {
-                    atomicAdd(&refused, 1);
-                }
+        if (ok && count > 0) {
+            if (d.old_len & mask) {
+                d.src = c.table[(int64_t)slot * c.max_pages + (d.old_len >> sh)];
+                ok = d.src >= 0 && d.src < c.n_pages;
+                d.copy = ok && c.refs[d.src] > 1;
             }
-            before += need[i];
+            if (ok) d.pages = ((d.old_len + (int)count + mask) >> sh) - ((d.old_len + mask) >> sh) + d.copy;
         }
+        if (!ok) d.old_len = -1;
+        a.ws.need[b] = d;
     }
-    __syncthreads();
+    int pages, refused;
+    block_exclusive<kNeedBlock>(d.pages, &pages);
+    block_exclusive<kNeedBlock>(b < a.batch && !ok ? 1 : 0, &refused);
     if (threadIdx.x == 0) {
-        c.counters[0] = n_free - taken;
-        c.counters[1] += refused;
+        a.ws.sums[blockIdx.x] = make_int2(pages, refused);
+        if (blockIdx.x == 0) *a.ws.n_free = c.counters[0];
+    }
+}
+
+// Pages of the histories before b, by one wave.
+__device__ __forceinline__ int pages_before(const NeedWs& ws, int b) {
+    const int lane = threadIdx.x & 63, b0 = b / kNeedBlock * kNeedBlock;
+    int n = 0;
+    for (int i = lane; i < b / kNeedBlock; i += 64) n += ws.sums[i].x;
+#pragma unroll
+    for (int i = 0; i < kNeedBlock; i += 64)
+        if (b0 + i + lane < b) n += ws.need[b0 + i + lane].pages;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d, 64);
+    return n;
+}
+
+// Needs are met in batch order; a history whose running sum passes the free
+// count is refused whole.
+__device__ __forceinline__ bool met(const Need& d, int before, int n_free) {
+    return d.old_len >= 0 && (d.pages == 0 || before + d.pages <= n_free);
+}
+
+// The free and refused counts after the call, by one block.
+__device__ __forceinline__ void settle(const AppendArgs& a) {
+    const int tid = threadIdx.x, n_free = *a.ws.n_free;
+    int pages = 0, refused = 0, total, no;
+    for (int i = tid; i < (a.batch + kNeedBlock - 1) / kNeedBlock; i += 256) {
+        const int2 s = a.ws.sums[i];
+        pages += s.x;
+        refused += s.y;
+    }
+    block_exclusive<256>(pages, &total);
+    block_exclusive<256>(refused, &no);
+    int taken = total;
+    if (total > n_free) {                   // not everyone is met
+        int carry = 0, most = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += 256) {
+            const int b = b0 + tid;
+            const Need d = b < a.batch ? a.ws.need[b] : Need{0, -1, 0, 0};
+            int sum, out;
+            const int before = carry + block_exclusive<256>(d.pages, &sum);
+            carry += sum;
+            const bool ok = met(d, before, n_free);
+            if (ok && d.pages) most = before + d.pages;
+            block_exclusive<256>(d.old_len >= 0 && !ok ? 1 : 0, &out);
+            no += out;
+        }
+        __shared__ int top;
+        if (tid == 0) top = 0;
+        __syncthreads();
+        if (most) atomicMax(&top, most);
+        __syncthreads();
+        taken = top;
+    }
+    if (tid == 0) {
+        a.c.counters[0] = n_free - taken;
+        a.c.counters[1] += no;
     }
 }
 
@@ -214,39 +226,57 @@ __device__ __forceinline__ unsigned bytes_below(int to, int w) {
 }
 
 // One wave per (page an append touches, kv head, keys or values).  The largest
-// finite value of the new events sets the block's scale, never below the one it
-// has; the events stay in registers from the load to the codes.  A lane takes
-// four consecutive events of eight elements: the codes of the four events of one
-// element make a word of the event-minor value page, and exchanging words
-// between the four 16-lane rows makes whole 16-byte pieces of it, without LDS.
-// Events the page already holds are read only where the page is copied, its
-// scale grows, or they share a 16-byte piece with new values.
+// finite value of the new events sets the block's scale, never below the one it has; the events
+// stay in registers from the load to the codes.  A lane takes four consecutive
+// events of eight elements: the codes of the four events of one element make a
+// word of the event-minor value page, and exchanging words between the four
+// 16-lane rows makes whole 16-byte pieces of it, without LDS.  Events the page
+// already holds are read only where the page is copied, its scale grows, or they
+// share a 16-byte piece with new values.  The last block settles the counts.
 template <typename T, int D, int PE, bool WIDE>
-__global__ __launch_bounds__(256, 2) void history_append_kernel(AppendArgs a) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void history_append_kernel(AppendArgs a) {
     const dlrm_history_cache_t& c = a.c;
     constexpr int C8 = D / 8;                            // 8-element pieces of a head
     constexpr int EV = 2048 / D;                         // events of one round of the wave
     constexpr int ROUNDS = PE > EV ? PE / EV : 1;
+    if (blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y == 0) settle(a);
+        return;
+    }
     const int lane = threadIdx.x & 63;
-    const int item = __builtin_amdgcn_readfirstlane((int)blockIdx.y * 4 + (threadIdx.x >> 6));
+    const int item = __builtin_amdgcn_readfirstlane((int)blockIdx.y * 4 + (int)(threadIdx.x >> 6));
     if (item >= 2 * c.n_kv_heads) return;
-    const int hk = item >> 1;
-    const bool minor = item & 1;
     const Unit un = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, PE, 2, blockIdx.x);
     const int64_t count = un.end - un.begin;
-    const Grant g = a.grants[un.b];
+    const Need g = a.ws.need[un.b];
     const int slot = a.slots ? a.slots[un.b] : un.b;
     if (un.nth < 0 || g.old_len < 0 || count == 0) return;
     const int64_t page_no = g.old_len / PE + un.nth, stop = g.old_len + count;
     if (page_no * PE >= stop) return;
+    const int n_free = *a.ws.n_free, before = pages_before(a.ws, un.b);
+    if (!met(g, before, n_free)) return;
     const int lo = un.nth == 0 ? g.old_len % PE : 0;                               // events already in the page
     const int hi = (int)(stop - page_no * PE < PE ? stop - page_no * PE : PE);     // events after the call
     const bool kept = lo > 0 && !g.copy;
     const int opened = (int)un.nth - (g.src >= 0 && !g.copy ? 1 : 0);              // of the pages taken from the list
+    const int dst = kept ? g.src : c.free_pages[n_free - 1 - before - opened];
+    if (dst < 0 || dst >= c.n_pages) return;
+    const int src = lo > 0 ? g.src : dst;
+    const int ch = lane % C8, quad = (lane >> 4) + 4 * ((lane & 15) / C8);
+    if (item == 0 && lane == 0) {
+        if (un.nth == 0) c.lens[slot] = (int)stop;
+        if (!kept) {
+            c.table[(int64_t)slot * c.max_pages + page_no] = dst;
+            c.refs[dst] = 1;
+            // the last two holders may both take a copy: the page is then listed as free by the next release
+            if (lo > 0) atomicSub(&c.refs[src], 1);
+        }
+    }
+    const int hk = item >> 1;
+    const bool minor = item & 1;
     const int64_t ld = minor ? a.ld_v : a.ld_k;
     // the page's first event stands lo events before the call's first one
     const T* x = (const T*)(minor ? a.v : a.k) + (un.begin + page_no * PE - g.old_len) * ld + (int64_t)hk * D;
-    const int ch = lane % C8, quad = (lane >> 4) + 4 * ((lane & 15) / C8);
 
     // events outside [lo, hi) stand in as the nearest one inside
     Raw<T> raw[ROUNDS][4];
@@ -258,9 +288,6 @@ __global__ __launch_bounds__(256, 2) void history_append_kernel(AppendArgs a) {
                 const int ev = min(max(r * EV + 4 * quad + j, lo), hi - 1);
                 raw[r][j] = load_raw<WIDE>(x + (int64_t)ev * ld + ch * 8);
             }
-    const int dst = kept ? g.src : c.free_pages[g.pos - opened];
-    if (dst < 0 || dst >= c.n_pages) return;
-    const int src = lo > 0 ? g.src : dst;
     const int64_t dst_h = (int64_t)dst * c.n_kv_heads + hk, src_h = (int64_t)src * c.n_kv_heads + hk;
     uint8_t* codes = (minor ? c.v : c.k) + dst_h * (PE * D);
     const uint8_t* held = (minor ? c.v : c.k) + src_h * (PE * D);
@@ -322,15 +349,7 @@ __global__ __launch_bounds__(256, 2) void history_append_kernel(AppendArgs a) {
             }
         }
     }
-    if (lane == 0) {
-        if (!kept || s != was) scales[dst_h] = s;
-        if (item == 0 && !kept) {
-            c.table[(int64_t)slot * c.max_pages + page_no] = dst;
-            c.refs[dst] = 1;
-            // the last two holders may both take a copy: the page is then listed as free by the next release
-            if (lo > 0) atomicSub(&c.refs[src], 1);
-        }
-    }
+    if (lane == 0 && (!kept || s != was)) scales[dst_h] = s;
 }
 
 // ---- sharing and releasing -----------------------------------------------------
@@ -665,10 +684,10 @@ static void launch_append(const AppendArgs& a, dim3 grid, hipStream_t s) {
 }
 
 hipError_t launch_history_append(const AppendArgs& a, int dtype, hipStream_t s) {
-    hipLaunchKernelGGL(history_reserve_kernel, dim3(1), dim3(1024), 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.n_events == 0) return e;
-    const dim3 grid((unsigned)(a.n_events / a.c.page_events + 2 * (int64_t)a.batch), (unsigned)((2 * a.c.n_kv_heads + 3) / 4));
+    hipLaunchKernelGGL(history_need_kernel, dim3((a.batch + kNeedBlock - 1) / kNeedBlock), dim3(kNeedBlock), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const dim3 grid((unsigned)(a.n_events / a.c.page_events + 2 * (int64_t)a.batch + 1), (unsigned)((2 * a.c.n_kv_heads + 3) / 4));
     if (dtype == DLRM_DTYPE_F32) launch_append<float>(a, grid, s);
     else if (dtype == DLRM_DTYPE_BF16) launch_append<bf16>(a, grid, s);
     else launch_append<f16>(a, grid, s);

@@ -114,13 +114,13 @@ def history_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets
     ``q`` (N, n_heads, head_dim), ``k`` and ``v`` (N, n_kv_heads, head_dim), all fp32, bf16 or fp16; rows may be
     columns of a wider tensor.  History b is rows [offsets[b], offsets[b + 1]).  An event sees the last ``window``
     events of its history, itself included, and the first ``sinks``, but none whose ``padding`` byte is set."""
-    L = load()
     if not isinstance(q, torch.Tensor) or q.dtype not in DTYPES:
         raise TypeError("q must be an fp32, bf16 or fp16 tensor")
-    dev = q.device
-    ld = [_rows(t, n, q.dtype, 3, dev) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    dev, dtype = q.device, q.dtype
+    ld_q, ld_k, ld_v = _rows(q, "q", dtype, 3, dev), _rows(k, "k", dtype, 3, dev), _rows(v, "v", dtype, 3, dev)
     n, heads, dim = q.shape
-    if k.shape != v.shape or k.shape[0] != n or k.shape[2] != dim:
+    kshape = k.shape
+    if kshape != v.shape or kshape[0] != n or kshape[2] != dim:
         raise ValueError("k and v must be (N, n_kv_heads, head_dim) beside q's (N, n_heads, head_dim)")
     ib = _offsets(offsets, dev)
     if padding is not None:
@@ -130,16 +130,16 @@ def history_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets
         if tuple(padding.shape) != (n,) or padding.device != dev:
             raise ValueError("padding must hold one byte for each event")
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
-        ld.append(max(heads * dim, 1))
+        out = torch.empty((n, heads, dim), dtype=dtype, device=dev)
+        ld_out = max(heads * dim, 1)
     else:
-        ld.append(_rows(out, "out", q.dtype, 3, dev))
+        ld_out = _rows(out, "out", dtype, 3, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
-    rc = L.dlrm_history_attention(_attention(q.dtype, heads, k.shape[1], dim, window, sinks, scale), offsets.shape[0], n, offsets.data_ptr(), ib, q.data_ptr(), ld[0],
-                                  k.data_ptr(), ld[1], v.data_ptr(), ld[2],
-                                  padding.data_ptr() if padding is not None else None, out.data_ptr(), ld[3],
-                                  _stream(dev))
+    rc = load().dlrm_history_attention(_attention(dtype, heads, kshape[1], dim, window, sinks, scale),
+                                       offsets.shape[0], n, offsets.data_ptr(), ib, q.data_ptr(), ld_q, k.data_ptr(),
+                                       ld_k, v.data_ptr(), ld_v, None if padding is None else padding.data_ptr(),
+                                       out.data_ptr(), ld_out, _stream(dev))
     if rc != DLRM_OK:
         _check(rc, "dlrm_history_attention")
     return out
