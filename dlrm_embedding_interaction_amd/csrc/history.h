@@ -108,6 +108,12 @@ struct Unit {
     int64_t nth;            // number of the unit within it; below 0: no one's
     int64_t begin, end;     // the history's rows
 };
+// A value of one lane, the same for the wave: what follows from it stays in scalar registers.
+__device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {
+    const unsigned lo = __builtin_amdgcn_readlane((unsigned)v, lane);
+    const unsigned hi = __builtin_amdgcn_readlane((unsigned)((uint64_t)v >> 32), lane);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ Unit history_of_unit(const void* off, int idx32, int batch, int64_t n, int width,
                                                 int extra, int64_t u) {
     const int lane = threadIdx.x & 63, sh = 31 - __builtin_clz(width);      // a power of two
@@ -123,11 +129,11 @@ __device__ __forceinline__ Unit history_of_unit(const void* off, int idx32, int 
         lo += last * step;
         if (step == 1) {
             r.b = lo;
-            r.nth = u - __shfl(s, last, 64);
-            r.begin = __shfl(o, last, 64);
-            const int64_t next = __shfl(o, last < 63 ? last + 1 : 63, 64);
+            r.nth = u - lane_value(s, last);
+            r.begin = lane_value(o, last);
+            const int64_t next = lane_value(o, last < 63 ? last + 1 : 63);
             r.end = last < 63 && last + 1 < left ? (next < r.begin ? r.begin : next)
-                                                 : history_end(off, idx32, lo, batch, r.begin, n);
+                                                 : lane_value(history_end(off, idx32, lo, batch, r.begin, n), 0);
             return r;
         }
         const int rest = left - last * step;

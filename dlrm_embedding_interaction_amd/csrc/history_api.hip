@@ -96,6 +96,7 @@ DLRM_API dlrm_status_t dlrm_history_attention(const dlrm_attention_t* a, int64_t
     if (!q || !k || !v || !out) return DLRM_E_NULL;
     const int64_t wq = (int64_t)a->n_heads * a->head_dim, wk = (int64_t)a->n_kv_heads * a->head_dim;
     if (ld_q < wq || ld_k < wk || ld_v < wk || ld_out < wq) return DLRM_E_SHAPE;
+    if (ld_k > kIntLimit || ld_v > kIntLimit) return DLRM_E_UNSUPPORTED;
     EncodeArgs e = {};
     e.q = q, e.k = k, e.v = v, e.offsets = offsets, e.padding = padding, e.out = out;
     e.ld_q = ld_q, e.ld_k = ld_k, e.ld_v = ld_v, e.ld_out = ld_out;

@@ -121,7 +121,7 @@ __device__ __forceinline__ float halves_sum(float v) {
 #endif
 // WIDE: 16-byte loads.  PAD: padding bytes may be given.
 template <typename T, int D, int W, int BN, bool WIDE, bool PAD>
-__global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeArgs a, int heads) {
+__global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeArgs a, int heads_log2) {
     typedef typename Mul<T>::part E;
     constexpr int N = Mul<T>::parts;
     constexpr int THREADS = 64 * W;
@@ -134,16 +134,17 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
     __shared__ __attribute__((aligned(16))) float hides[BN];   // 0, or -inf for a padding event
     __shared__ int odd[2];                          // the values of even / odd tiles hold an infinity or NaN
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 31, h = lane >> 5;
-    const int BM = 32 * W / heads;
-    const int head = blockIdx.y * heads + wave % heads, hk = head / (a.n_heads / a.n_kv);
+    const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);      // conditions on it are scalar branches
+    const int BM = 32 * W >> heads_log2;
+    const int head = (blockIdx.y << heads_log2) + (wave & ((1 << heads_log2) - 1)), hk = head / (a.n_heads / a.n_kv);
     // the longest rows first: a history's last tiles see the most keys
     const Unit un = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, BM, 1,
                                     (int64_t)gridDim.x - 1 - blockIdx.x);
     const int64_t nth = un.nth, begin = un.begin;
     const int len = (int)(un.end - begin);
     if (nth < 0 || nth * BM >= len) return;
-    const int q0 = (int)nth * BM, r0 = q0 + wave / heads * 32, row = r0 + n;
+    const int q0 = (int)nth * BM, r0 = q0 + (wave >> heads_log2) * 32, row = r0 + n;
     const int last = q0 + BM < len ? q0 + BM - 1 : len - 1;
     const int window = (int)a.window, sinks = (int)a.sinks;
     const T* kg = (const T*)a.k + begin * a.ld_k + (int64_t)hk * D;
@@ -166,11 +167,9 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
             Raw<T> r = load_raw<WIDE>(qp + 16 * s + 8 * h);
-            if (a.scale < 0.f) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) r.x[i] = -r.x[i];
-            }
             to_parts(r, q[s]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) q[s][i] ^= a.scale < 0.f ? (short)0x8000 : (short)0;
         }
     }
     // exp(scale s) = 2^(c s); a scale of 0 is a c that leaves every finite score's weight at 1
@@ -187,8 +186,8 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
         for (int x = 0; x < VEC; ++x) {
             const int p = tid + x * THREADS, d = p % (D / 8) * 8;
             const int key = min(k0 + p / (D / 8), len - 1);
-            kr[x] = load_raw<WIDE>(kg + (int64_t)key * a.ld_k + d);
-            vr[x] = load_raw<WIDE>(vg + (int64_t)key * a.ld_v + d);
+            kr[x] = load_raw<WIDE>(kg + (int64_t)key * (int)a.ld_k + d);
+            vr[x] = load_raw<WIDE>(vg + (int64_t)key * (int)a.ld_v + d);
             if (PAD && pad) gone[x] = pad[key];
         }
     };
@@ -259,7 +258,11 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
                 const int k2 = k1 + 4 * h;
                 const unsigned see = up_to(row - k2) & (~up_to(row - window - k2) | up_to(sinks - 1 - k2));
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[i] = see >> (8 * (i >> 2) + (i & 3)) & 1 ? s[i] : -INFINITY;
+                for (int i = 0; i < 16; ++i) {
+                    // the bit spread over a word picks the score's bits or those of -inf, without a condition register
+                    const unsigned keep = (unsigned)((int)(see << (31 - (8 * (i >> 2) + (i & 3)))) >> 31);
+                    s[i] = __uint_as_float((__float_as_uint(s[i]) & keep) | (0xff800000u & ~keep));
+                }
             }
             float top = -INFINITY;
 #pragma unroll
@@ -321,31 +324,31 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
         for (int j = 0; j < D / 32; ++j)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                op[32 * j + 8 * (i >> 2) + 4 * h + (i & 3)] = (T)(l == 0.f ? 0.f : o[j][i] * inv);
+                op[32 * j + 8 * (i >> 2) + 4 * h + (i & 3)] = (T)(o[j][i] * inv);
     }
 }
 
 template <typename T, int D, int W>
-static hipError_t launch_w(const EncodeArgs& a, bool wide, int heads, hipStream_t s) {
+static hipError_t launch_w(const EncodeArgs& a, bool wide, int heads_log2, hipStream_t s) {
     constexpr int BN = sizeof(T) == 4 && D == 128 ? 32 : 64;
-    const dim3 grid((unsigned)(a.n_events / (32 * W / heads) + a.batch), (unsigned)(a.n_heads / heads));
+    const dim3 grid((unsigned)(a.n_events / (32 * W >> heads_log2) + a.batch), (unsigned)(a.n_heads >> heads_log2));
     const dim3 block(64 * W);
-    if (!wide) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, false, true>), grid, block, 0, s, a, heads);
-    else if (a.padding) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, true>), grid, block, 0, s, a, heads);
-    else hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, false>), grid, block, 0, s, a, heads);
+    if (!wide) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, false, true>), grid, block, 0, s, a, heads_log2);
+    else if (a.padding) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, true>), grid, block, 0, s, a, heads_log2);
+    else hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, false>), grid, block, 0, s, a, heads_log2);
     return hipGetLastError();
 }
 template <typename T, int D>
 static hipError_t launch_d(const EncodeArgs& a, bool wide, hipStream_t s) {
     const int64_t mean = a.n_events / a.batch;
     const int group = a.n_heads / a.n_kv;
-    const int heads = group % 4 == 0 ? 4 : (group % 2 == 0 ? 2 : 1);
+    const int heads = group % 4 == 0 ? 2 : (group % 2 == 0 ? 1 : 0);    // log2 of the heads that share a block
     const int rows = mean <= 32 ? 1 : (mean <= 96 ? 2 : 4);     // in 32s
     if constexpr (D > 32) {
-        if (heads * rows >= 8) return launch_w<T, D, 8>(a, wide, heads, s);
+        if (rows << heads >= 8) return launch_w<T, D, 8>(a, wide, heads, s);
     }
-    if (heads * rows >= 4) return launch_w<T, D, 4>(a, wide, heads, s);
-    if (heads * rows == 2) return launch_w<T, D, 2>(a, wide, heads, s);
+    if (rows << heads >= 4) return launch_w<T, D, 4>(a, wide, heads, s);
+    if (rows << heads == 2) return launch_w<T, D, 2>(a, wide, heads, s);
     return launch_w<T, D, 1>(a, wide, heads, s);
 }
 template <typename T>
