@@ -116,12 +116,12 @@ __device__ __forceinline__ float halves_sum(float v) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-#ifndef MINW
-#define MINW (sizeof(T) == 4 ? 2 : D == 128 ? 2 : D == 64 ? 3 : 4)
-#endif
-// WIDE: 16-byte loads.  PAD: padding bytes may be given.
+// Waves per SIMD that the registers are cut to: what fits without spilling.
+template <typename T, int D> constexpr int kWavesPerSimd = sizeof(T) == 4 || D == 128 ? 2 : (D == 64 ? 3 : 4);
+
+// WIDE: 16-byte loads and stores.  PAD: padding bytes may be given.
 template <typename T, int D, int W, int BN, bool WIDE, bool PAD>
-__global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeArgs a, int heads_log2) {
+__global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attention_kernel(EncodeArgs a, int heads_log2) {
     typedef typename Mul<T>::part E;
     constexpr int N = Mul<T>::parts;
     constexpr int THREADS = 64 * W;
@@ -131,7 +131,6 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
     static_assert(BN * D / 8 % THREADS == 0, "whole vectors per thread");
     __shared__ __attribute__((aligned(16))) E ks[N][BN][KP];
     __shared__ __attribute__((aligned(16))) E vs[N][BN][VP];
-    __shared__ __attribute__((aligned(16))) float hides[BN];   // 0, or -inf for a padding event
     __shared__ int odd[2];                          // the values of even / odd tiles hold an infinity or NaN
 
     const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
@@ -146,7 +145,8 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
     if (nth < 0 || nth * BM >= len) return;
     const int q0 = (int)nth * BM, r0 = q0 + (wave >> heads_log2) * 32, row = r0 + n;
     const int last = q0 + BM < len ? q0 + BM - 1 : len - 1;
-    const int window = (int)a.window, sinks = (int)a.sinks;
+    const int window = __builtin_amdgcn_readfirstlane((int)a.window);
+    const int sinks = __builtin_amdgcn_readfirstlane((int)a.sinks);
     const T* kg = (const T*)a.k + begin * a.ld_k + (int64_t)hk * D;
     const T* vg = (const T*)a.v + begin * a.ld_v + (int64_t)hk * D;
     const uint8_t* pad = PAD && a.padding ? a.padding + begin : nullptr;
@@ -176,19 +176,17 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
     const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-37f);
 
     Raw<T> kr[VEC], vr[VEC];
-    // padding bytes, as loaded (a comparison here would wait for the loads): of the tile's key `tid`, of the vectors
-    uint8_t hide = 0, gone[VEC] = {};
+    uint8_t hide = 0;       // the padding byte of the tile's key `lane`, as loaded: a comparison here would wait for it
     // Rows behind the history's end stand in as its last one: no row sees them.
     auto fetch = [&](int t) {
         const int k0 = key_of(t);
-        if (PAD && pad && tid < BN) hide = pad[min(k0 + tid, len - 1)];
+        if (PAD && pad && lane < BN) hide = pad[min(k0 + lane, len - 1)];
 #pragma unroll
         for (int x = 0; x < VEC; ++x) {
             const int p = tid + x * THREADS, d = p % (D / 8) * 8;
             const int key = min(k0 + p / (D / 8), len - 1);
             kr[x] = load_raw<WIDE>(kg + (int64_t)key * (int)a.ld_k + d);
             vr[x] = load_raw<WIDE>(vg + (int64_t)key * (int)a.ld_v + d);
-            if (PAD && pad) gone[x] = pad[key];
         }
     };
 
@@ -201,6 +199,7 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
     if (tid == 0) odd[0] = 0;
     for (int t = 0; t < tiles; ++t) {
         const int k0 = key_of(t);
+        const unsigned long long hidden = PAD ? __ballot(hide != 0) : 0;      // the tile's padding events
         __syncthreads();                            // the tile before has been read
         if (tid == 0) odd[(t + 1) & 1] = 0;
         unsigned big = 0;
@@ -208,7 +207,6 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
         for (int x = 0; x < VEC; ++x) {
             const int p = tid + x * THREADS, key = p / (D / 8), d = p % (D / 8) * 8;
             shortx8 kp[N], vp[N];
-            if (PAD && gone[x] != 0) kr[x] = vr[x] = Raw<T>{};
             to_parts(kr[x], kp);
             to_parts(vr[x], vp);
             top_magnitude(vr[x], big);
@@ -218,7 +216,6 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
                 *(shortx8*)&vs[i][key][d] = vp[i];
             }
         }
-        if (PAD && pad && tid < BN) hides[tid] = hide != 0 ? -INFINITY : 0.f;
         if (odd_magnitude<T>(big)) odd[t & 1] = 1;
         __syncthreads();
         if (t + 1 < tiles) fetch(t + 1);
@@ -237,14 +234,6 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
             const int k1 = k0 + 32 * u;
             if (k1 > r0 + 31 || (r0 - (k1 + 31) >= window && k1 >= sinks)) continue;
             floatx16 s = floatx16{};
-            if (PAD && pad) {                       // the sums start at -inf for padding events, whose keys are zeros
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const floatx4 z = *(const floatx4*)&hides[u * 32 + 8 * i + 4 * h];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) s[4 * i + y] = z[y];
-                }
-            }
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
                 shortx8 kk[N];
@@ -252,11 +241,14 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
                 for (int i = 0; i < N; ++i) kk[i] = *(const shortx8*)&ks[i][u * 32 + n][16 * x + 8 * h];
                 s = mul_parts<E, N>(kk, q[x], s);
             }
-            if (k1 + 31 > r0 || (r0 + 31 - k1 >= window && k1 + 32 > sinks)) {
-                // bit y: the row sees key k1 + 4 h + y
+            const unsigned off = PAD ? (unsigned)(hidden >> (32 * u)) : 0;
+            if (k1 + 31 > r0 || (r0 + 31 - k1 >= window && k1 + 32 > sinks) || off) {
+                // bit y: the row sees key k1 + 4 h + y.  Whatever stands in the other keys leaves here; their values
+                // meet weights of 0, and those that are not finite are dealt with apart.
                 auto up_to = [](int y) { return y < 0 ? 0u : y > 30 ? ~0u : (2u << y) - 1u; };      // bits 0 .. y
                 const int k2 = k1 + 4 * h;
-                const unsigned see = up_to(row - k2) & (~up_to(row - window - k2) | up_to(sinks - 1 - k2));
+                const unsigned see = up_to(row - k2) & (~up_to(row - window - k2) | up_to(sinks - 1 - k2)) &
+                                     ~(off >> (4 * h));
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     // the bit spread over a word picks the score's bits or those of -inf, without a condition register
@@ -317,14 +309,37 @@ __global__ __launch_bounds__(64 * W, MINW) void history_attention_kernel(EncodeA
         }
     }
     l = halves_sum(l);
-    if (row < len) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        T* op = (T*)a.out + (begin + row) * a.ld_out + (int64_t)head * D;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* op = (T*)a.out + (begin + row) * a.ld_out + (int64_t)head * D;
+    if constexpr (WIDE && sizeof(T) == 2) {
+        // the two halves of a row hold four elements each of every eight: exchanged, a lane stores eight at once
+        typedef unsigned u4 __attribute__((ext_vector_type(4)));
+        typedef T t2 __attribute__((ext_vector_type(2)));
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                op[32 * j + 8 * (i >> 2) + 4 * h + (i & 3)] = (T)(o[j][i] * inv);
+            for (int e = 0; e < 2; ++e) {
+                unsigned w[4];          // elements 16 e + 4 h .. + 3, and + 8
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = __builtin_bit_cast(unsigned, t2{(T)(o[j][8 * e + 2 * i] * inv), (T)(o[j][8 * e + 2 * i + 1] * inv)});
+                const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                if (row < len) *(u4*)(op + 32 * j + 16 * e + 8 * h) = u4{x[0], y[0], x[1], y[1]};
+            }
+    } else if (row < len) {
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                T* at = op + 32 * j + 2 * i + 4 * h;
+                if constexpr (WIDE) {
+                    *(floatx4*)at = floatx4{o[j][i] * inv, o[j][i + 1] * inv, o[j][i + 2] * inv, o[j][i + 3] * inv};
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) at[x] = (T)(o[j][i + x] * inv);
+                }
+            }
     }
 }
 
@@ -342,10 +357,15 @@ template <typename T, int D>
 static hipError_t launch_d(const EncodeArgs& a, bool wide, hipStream_t s) {
     const int64_t mean = a.n_events / a.batch;
     const int group = a.n_heads / a.n_kv;
-    const int heads = group % 4 == 0 ? 2 : (group % 2 == 0 ? 1 : 0);    // log2 of the heads that share a block
-    const int rows = mean <= 32 ? 1 : (mean <= 96 ? 2 : 4);     // in 32s
-    if constexpr (D > 32) {
-        if (rows << heads >= 8) return launch_w<T, D, 8>(a, wide, heads, s);
+    // log2 of the heads that share a block, and its rows in 32s
+    const int heads = group % 4 == 0 ? 2 : (group % 2 == 0 ? 1 : 0);
+    const int rows = mean <= 32 ? 1 : (mean <= 96 ? 2 : 4);
+    // Blocks of 8 waves read each tile once for twice the rows, blocks of 4 leave two to a CU, one's loads and stores
+    // beside the other's products.  Lifelong (66 tiles a block) 8 waves 294 us, 4 waves 312; grouped (10 tiles) 308
+    // against 289.
+    const int64_t tiles = (a.window < mean ? a.window : mean) / 64;
+    if constexpr (D == 128) {
+        if (rows << heads >= 8 && tiles >= 24) return launch_w<T, D, 8>(a, wide, heads, s);
     }
     if (rows << heads >= 4) return launch_w<T, D, 4>(a, wide, heads, s);
     if (rows << heads == 2) return launch_w<T, D, 2>(a, wide, heads, s);
@@ -354,8 +374,8 @@ static hipError_t launch_d(const EncodeArgs& a, bool wide, hipStream_t s) {
 template <typename T>
 static hipError_t launch_t(const EncodeArgs& a, int dim, hipStream_t s) {
     const int64_t step = 16 / sizeof(T);
-    const bool wide = a.ld_q % step == 0 && a.ld_k % step == 0 && a.ld_v % step == 0 &&
-                      (((uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v) & 15u) == 0;
+    const bool wide = a.ld_q % step == 0 && a.ld_k % step == 0 && a.ld_v % step == 0 && a.ld_out % step == 0 &&
+                      (((uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.out) & 15u) == 0;
     if (dim == 32) return launch_d<T, 32>(a, wide, s);
     if (dim == 64) return launch_d<T, 64>(a, wide, s);
     return launch_d<T, 128>(a, wide, s);
