@@ -546,3 +546,36 @@ def test_cache_calls_in_a_graph():
         assert torch.equal(outs[0], outs[1])
         for n in ("table", "lens", "refs", "counters"):
             assert torch.equal(getattr(caches[0], n), getattr(caches[1], n)), n
+
+
+# --- the example: all of them together ----------------------------------------------
+
+
+def test_example_ranking_with_histories():
+    """examples/history_ranking.py: a fork's score is the score after the click, and leaves the user's own as it
+    was; trimming and compaction change nothing; the histories' vectors match the 64-bit form."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "history_ranking.py")
+    spec = importlib.util.spec_from_file_location("history_ranking", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    out = mod.main()
+    r, lens, slots = out["ranker"], out["lens"], out["slots"]
+    assert r.cache.n_refused == 0
+    for p in ("before", "tried", "after"):
+        assert bool(((out[p] > 0) & (out[p] < 1)).all())
+    assert torch.equal(out["before"], out["again"])
+    assert torch.equal(out["tried"], out["after"])
+    assert torch.equal(out["trimmed"], out["after"])
+    q, k, v = r.project(out["events"])
+    check_encode(q.cpu(), k.cpu(), v.cpu(), lens, r.window, r.sinks, out["encoded"])
+    o = ho.Cache(400, len(lens), 40, r.heads, r.dim // r.heads, r.cache.page_events)
+    o.append(list(range(len(lens))), lens, f64(k), f64(v))
+    _, k1, v1 = r.project(out["click"])
+    o.append(list(range(len(lens))), [1] * len(lens), f64(k1), f64(v1))
+    got = r.attend(out["candidates"], slots)
+    cq = f64(next(r.project(out["candidates"]))).reshape(*out["candidates"].shape, r.heads, -1)
+    want, mag, big = o.lookup(list(range(len(lens))), cq, r.window, r.sinks, (r.dim // r.heads) ** -0.5)
+    tol = bound(want, mag, big, r.dim // r.heads, max(lens) + 1, torch.float32, U, 0.0)
+    assert (np.abs(f64(got).reshape(want.shape) - want) <= tol).all()
