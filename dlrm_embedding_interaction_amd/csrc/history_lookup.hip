@@ -386,10 +386,14 @@ __global__ __launch_bounds__(DIRECT ? 64 * DIRECT : 256, 2) void history_lookup_
     }
 }
 
-// Joins the runs that share a history: one block per (history, chunk of rows).
+// Joins the runs that share a history: blocks of (history, chunk of rows, every
+// gridDim.z-th 64 elements of its result).  The runs' maxima and sums first, then
+// each element over four groups of runs, so that the reads of a history cut into
+// many runs do not wait for one another.
 template <int D, typename T>
 __global__ __launch_bounds__(256) void history_join_kernel(LookupArgs a, const int* __restrict__ meta) {
-    const int b = blockIdx.x;
+    __shared__ float ms[16][17], ls[16][17], os[4][64];
+    const int b = blockIdx.x, tid = threadIdx.x;
     const int group = a.n_heads / a.c.n_kv_heads, rows = a.queries * group;
     const int chunks = (rows + 15) / 16;
     const int hk = blockIdx.y / chunks, r0 = (blockIdx.y % chunks) * 16;
@@ -398,25 +402,56 @@ __global__ __launch_bounds__(256) void history_join_kernel(LookupArgs a, const i
     const int start = count ? meta[b] : 0, per = meta[a.batch];
     const int w0 = start / per, w1 = count ? (start + count - 1) / per : 0;
     if (count && w0 == w1) return;                      // one wave had it all
-    for (int x = threadIdx.x; x < cols * D; x += 256) {
-        const int n = x / D, d = x % D;
-        if (r0 + n >= rows) break;
-        float m = -INFINITY, l = 0.f, o = 0.f;
-        if (count) {
-            for (int w = w0; w <= w1; ++w) {
-                const float* part = a.partial +
-                                    (((int64_t)2 * w + (w == w0 ? 1 : 0)) * gridDim.y + blockIdx.y) * cols * (D + 2) + n * (D + 2);
-                const float pm = part[D], pl = part[D + 1], po = part[d];
-                const float mx = fmaxf(m, pm), ms = mx == -INFINITY ? 0.f : mx;
-                const float f = __builtin_amdgcn_exp2f(m - ms), h = __builtin_amdgcn_exp2f(pm - ms);
-                l = l * f + pl * h;
-                o = o * f + po * h;
-                m = mx;
+    const int runs = count ? w1 - w0 + 1 : 0;
+    // run i of the history: its wave's second place for the first run, which began the history, the first for others
+    const int64_t one = (int64_t)cols * (D + 2);
+    auto run = [&](int i) {
+        return a.partial + ((int64_t)(2 * (w0 + i) + (i == 0 ? 1 : 0)) * gridDim.y + blockIdx.y) * one;
+    };
+    const int col = tid & 15, sub = tid >> 4;
+    float m = -INFINITY, l = 0.f;
+    for (int i = sub; i < runs && col < cols; i += 16) m = fmaxf(m, run(i)[col * (D + 2) + D]);
+    ms[sub][col] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, ms[i][col]);
+    const float mf = m == -INFINITY ? 0.f : m;
+    for (int i = sub; i < runs && col < cols; i += 16) {
+        const float* p = run(i) + col * (D + 2) + D;
+        l += p[1] * __builtin_amdgcn_exp2f(p[0] - mf);
+    }
+    ls[sub][col] = l;
+    __syncthreads();
+    if (sub == 0) {
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) l += ls[i][col];
+        ls[0][col] = l;
+        ms[0][col] = mf;
+    }
+    __syncthreads();
+    const int e = tid & 63, part = tid >> 6;
+    for (int x0 = blockIdx.z * 64; x0 < cols * D; x0 += gridDim.z * 64) {
+        const int x = x0 + e, n = x / D, d = x % D;
+        float o = 0.f;
+        if (x < cols * D) {
+            const float mn = ms[0][n];
+#pragma unroll 8
+            for (int i = part; i < runs; i += 4) {
+                const float* p = run(i) + n * (D + 2);
+                o += p[d] * __builtin_amdgcn_exp2f(p[D] - mn);
             }
         }
-        T* out = (T*)a.out + ((int64_t)b * a.queries + (r0 + n) / group) * a.ld_out +
-                 (int64_t)(hk * group + (r0 + n) % group) * D;
-        out[d] = (T)(l == 0.f ? 0.f : o / l);
+        os[part][e] = o;
+        __syncthreads();
+        if (part == 0 && x < cols * D && r0 + n < rows) {
+            o = os[0][e] + os[1][e] + os[2][e] + os[3][e];
+            T* out = (T*)a.out + ((int64_t)b * a.queries + (r0 + n) / group) * a.ld_out +
+                     (int64_t)(hk * group + (r0 + n) % group) * D;
+            const float sum = ls[0][n];
+            out[d] = (T)(sum == 0.f ? 0.f : o / sum);
+        }
+        __syncthreads();
     }
 }
 
@@ -474,7 +509,10 @@ static hipError_t launch_t(LookupArgs a, hipStream_t s) {
     }
     const int waves = waves_of(a.c, a.batch, a.queries, a.n_heads);
     hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 0>), dim3(waves / 4, hc), dim3(256), 0, s, a, waves, meta);
-    hipLaunchKernelGGL((history_join_kernel<D, T>), dim3(a.batch, hc), dim3(256), 0, s, a, meta);
+    // a few long histories are cut into many runs each: their elements are then spread over blocks, too
+    const int cols = rows < 16 ? rows : 16;
+    const int z = waves / a.batch >= 16 ? (cols * D + 63) / 64 : 1;
+    hipLaunchKernelGGL((history_join_kernel<D, T>), dim3(a.batch, hc, z), dim3(256), 0, s, a, meta);
     return hipGetLastError();
 }
 template <int D, int PE>

@@ -358,9 +358,10 @@ __device__ __forceinline__ void drop_page(const dlrm_history_cache_t& c, int p) 
     if (p >= 0 && p < c.n_pages) atomicSub(&c.refs[p], 1);      // its result is not waited for
 }
 
-// One block per history.  The list is written by a kernel of its own: a last
+// LANES threads per history.  The list is written by a kernel of its own: a last
 // block that wrote it here would need every block to write its caches back first,
-// which took 10 to 40 us more than the second launch.
+// which took 10 to 40 us more than the second launch.  Only where one block can
+// do the whole call does it write the list, too.
 enum Release { kFork, kTruncate, kTrim };
 struct ReleaseArgs {
     dlrm_history_cache_t c;
@@ -369,9 +370,8 @@ struct ReleaseArgs {
     int n;
 };
 
-template <Release OP>
-__global__ __launch_bounds__(256) void history_release_kernel(ReleaseArgs a) {
-    const int i = blockIdx.x, tid = threadIdx.x;
+template <Release OP, int LANES>
+__device__ __forceinline__ void release_history(const ReleaseArgs& a, int i, int tid) {
     const dlrm_history_cache_t& c = a.c;
     const int sh = 31 - __builtin_clz(c.page_events);
     const int slot = a.slots[i];
@@ -382,7 +382,7 @@ __global__ __launch_bounds__(256) void history_release_kernel(ReleaseArgs a) {
         if (ok && slot != to) {
             const int64_t f = (int64_t)slot * c.max_pages, t = (int64_t)to * c.max_pages;
             const int len = c.lens[slot];
-            for (int x = tid; x < c.max_pages; x += 256) {
+            for (int x = tid; x < c.max_pages; x += LANES) {
                 const int p = c.table[f + x], o = c.table[t + x];
                 if (p == o) continue;
                 c.table[t + x] = p;
@@ -401,7 +401,7 @@ __global__ __launch_bounds__(256) void history_release_kernel(ReleaseArgs a) {
             // the page that would be filled further may have been trimmed away
             if (ok && (want & mask)) ok = c.table[row + (want >> sh)] >= 0;
             lo = ok ? (want + mask) >> sh : hi;
-            __syncthreads();            // every thread has read the length
+            if constexpr (LANES > 64) __syncthreads();      // every thread has read the length
             if (ok && tid == 0) c.lens[slot] = want;
         } else {
             // pages whose events all lie behind the sinks and before the window
@@ -409,7 +409,7 @@ __global__ __launch_bounds__(256) void history_release_kernel(ReleaseArgs a) {
             const int64_t end = len > a.window ? (len - a.window) >> sh : 0;
             hi = ok && end < hi ? (int)end : (ok ? hi : 0);
         }
-        for (int x = lo + tid; x < hi; x += 256) {
+        for (int x = lo + tid; x < hi; x += LANES) {
             const int p = c.table[row + x];
             if (p == -1) continue;
             c.table[row + x] = -1;
@@ -417,6 +417,11 @@ __global__ __launch_bounds__(256) void history_release_kernel(ReleaseArgs a) {
         }
     }
     if (!ok && tid == 0) atomicAdd(&c.counters[1], 1);
+}
+
+template <Release OP>
+__global__ __launch_bounds__(256) void history_release_kernel(ReleaseArgs a) {
+    release_history<OP, 256>(a, blockIdx.x, threadIdx.x);
 }
 
 // The free pages of a wave's share of a block, at most 64 words of 64 pages: lane
@@ -518,8 +523,22 @@ __global__ __launch_bounds__(256) void history_rebuild_kernel(dlrm_history_cache
     list_free<4>(c, blockIdx.x * kRebuildChunk, kChunkWords, above);
 }
 
+// A wave per history, sixteen at a time, then the list: one launch for a call of a
+// few histories of a small pool.
+template <Release OP>
+__global__ __launch_bounds__(1024) void history_release_one_kernel(ReleaseArgs a) {
+    for (int i = threadIdx.x >> 6; i < a.n; i += 16) release_history<OP, 64>(a, i, threadIdx.x & 63);
+    __threadfence_block();      // the holders' counts are changed in the block's own L2 and not cached nearer
+    __syncthreads();
+    list_free<16>(a.c, 0, one_words(a.c.n_pages), 0);
+}
+
 template <Release OP>
 static hipError_t release(const ReleaseArgs& a, int32_t* counts, hipStream_t s) {
+    if (a.n <= 32 && a.c.max_pages <= 256 && a.c.n_pages <= 8192) {
+        hipLaunchKernelGGL(history_release_one_kernel<OP>, dim3(1), dim3(1024), 0, s, a);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL(history_release_kernel<OP>, dim3(a.n), dim3(256), 0, s, a);
     if (a.c.n_pages <= kOneBlockPages) {
         hipLaunchKernelGGL(history_rebuild_one_kernel, dim3(1), dim3(1024), 0, s, a.c);

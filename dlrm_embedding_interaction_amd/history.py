@@ -95,7 +95,8 @@ def _attention(dtype, heads, kv, dim, window, sinks, scale):
 
 
 def _i32(t: torch.Tensor, name: str, device: torch.device) -> torch.Tensor:
-    _dev(t, torch.int32, name)
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
+        _dev(t, torch.int32, name)
     if t.dim() != 1 or t.device != device:
         raise ValueError(f"{name} must be 1-D on {device}")
     return t
