@@ -23,6 +23,16 @@
 // 2^-24 of the whole: 6/16 of the fp32 matrix instructions' time.  16-bit
 // tensors round the weights to their own type once, an error of the size of the
 // output's own rounding; maxima, sums and outputs are held in fp32.
+//
+// Measured on MI355X, bf16: 2 histories of up to 12001 events, 8 heads on 2 kv heads
+// of 128, window 4096: 291 us, 800 TFLOP/s of visible pairs, 66% of a large library
+// product (1204).  Per 32 rows x 32 keys a wave issues 16 products (512 cycles) and
+// ~110 vector instructions (~600 cycles with the exponentials); the counters show
+// 39% and 40% of the cycles busy with either, the rest waiting for LDS and at
+// barriers.  256 histories of up to 512, 4 heads of 64, window 128: 44 us against 29
+// for its bytes, the masked edges of the window being most of the work.  Tried and
+// not kept: two LDS buffers with one barrier a tile (309 against 293 us), 64 keys at
+// a time (304), reads ordered ahead of the products, raised wave priorities.
 #include "history.h"
 
 namespace dlrm {

@@ -7,6 +7,12 @@
 // taken first, from the end.  Every call that releases pages rebuilds the list
 // from refs: its order then depends on which pages are free alone, not on the
 // order in which the atomics of a call arrived.
+//
+// Measured on MI355X: appending 128 histories of up to 1000 events, 8 kv heads of
+// 128, bf16 (466 MB): 100 us, 4.7 TB/s, against 5.0 for a large copy.  One event for
+// each of 512 histories: 9 us, of 1500 with a copied page each 48: there a wave's
+// five dependent reads (offsets, need, list, scale, codes) are what it takes.  The
+// list of 32000 pages 7 us, of 11000 5.
 #include "history.h"
 
 namespace dlrm {
