@@ -129,8 +129,9 @@ __device__ __forceinline__ float halves_sum(float v) {
 // Waves per SIMD that the registers are cut to: what fits without spilling.
 template <typename T, int D> constexpr int kWavesPerSimd = sizeof(T) == 4 || D == 128 ? 2 : (D == 64 ? 3 : 4);
 
-// WIDE: 16-byte loads and stores.  PAD: padding bytes may be given.
-template <typename T, int D, int W, int BN, bool WIDE, bool PAD>
+// WIDE: 16-byte loads and stores.  PAD: padding bytes may be given.  KS: waves that
+// share the keys of a tile among them for the same rows, and join at the end.
+template <typename T, int D, int W, int BN, bool WIDE, bool PAD, int KS>
 __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attention_kernel(EncodeArgs a, int heads_log2) {
     typedef typename Mul<T>::part E;
     constexpr int N = Mul<T>::parts;
@@ -145,15 +146,17 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
 
     const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);      // conditions on it are scalar branches
-    const int BM = 32 * W >> heads_log2;
-    const int head = (blockIdx.y << heads_log2) + (wave & ((1 << heads_log2) - 1)), hk = head / (a.n_heads / a.n_kv);
+    constexpr int PK = BN / KS;                     // keys of the tile that the wave works on
+    const int BM = 32 * (W / KS) >> heads_log2;
+    const int ks_at = wave % KS, wr = wave / KS;
+    const int head = (blockIdx.y << heads_log2) + (wr & ((1 << heads_log2) - 1)), hk = head / (a.n_heads / a.n_kv);
     // the longest rows first: a history's last tiles see the most keys
     const Unit un = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, BM, 1,
                                     (int64_t)gridDim.x - 1 - blockIdx.x);
     const int64_t nth = un.nth, begin = un.begin;
     const int len = (int)(un.end - begin);
     if (nth < 0 || nth * BM >= len) return;
-    const int q0 = (int)nth * BM, r0 = q0 + (wave >> heads_log2) * 32, row = r0 + n;
+    const int q0 = (int)nth * BM, r0 = q0 + (wr >> heads_log2) * 32, row = r0 + n;
     const int last = q0 + BM < len ? q0 + BM - 1 : len - 1;
     const int window = __builtin_amdgcn_readfirstlane((int)a.window);
     const int sinks = __builtin_amdgcn_readfirstlane((int)a.sinks);
@@ -186,11 +189,11 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
     const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-37f);
 
     Raw<T> kr[VEC], vr[VEC];
-    uint8_t hide = 0;       // the padding byte of the tile's key `lane`, as loaded: a comparison here would wait for it
+    uint8_t hide = 0;       // the padding byte of the wave's key `lane`, as loaded: a comparison here would wait for it
     // Rows behind the history's end stand in as its last one: no row sees them.
     auto fetch = [&](int t) {
         const int k0 = key_of(t);
-        if (PAD && pad && lane < BN) hide = pad[min(k0 + lane, len - 1)];
+        if (PAD && pad && lane < PK) hide = pad[min(k0 + ks_at * PK + lane, len - 1)];
 #pragma unroll
         for (int x = 0; x < VEC; ++x) {
             const int p = tid + x * THREADS, d = p % (D / 8) * 8;
@@ -209,7 +212,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
     if (tid == 0) odd[0] = 0;
     for (int t = 0; t < tiles; ++t) {
         const int k0 = key_of(t);
-        const unsigned long long hidden = PAD ? __ballot(hide != 0) : 0;      // the tile's padding events
+        const unsigned long long hidden = PAD ? __ballot(hide != 0) : 0;      // the wave's padding events
         __syncthreads();                            // the tile before has been read
         if (tid == 0) odd[(t + 1) & 1] = 0;
         unsigned big = 0;
@@ -240,15 +243,15 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
         }
         // 32 keys at a time, those that no row of the wave sees left out
 #pragma unroll
-        for (int u = 0; u < BN / 32; ++u) {
-            const int k1 = k0 + 32 * u;
+        for (int u = 0; u < PK / 32; ++u) {
+            const int k1 = k0 + ks_at * PK + 32 * u;
             if (k1 > r0 + 31 || (r0 - (k1 + 31) >= window && k1 >= sinks)) continue;
             floatx16 s = floatx16{};
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
                 shortx8 kk[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) kk[i] = *(const shortx8*)&ks[i][u * 32 + n][16 * x + 8 * h];
+                for (int i = 0; i < N; ++i) kk[i] = *(const shortx8*)&ks[i][ks_at * PK + u * 32 + n][16 * x + 8 * h];
                 s = mul_parts<E, N>(kk, q[x], s);
             }
             const unsigned off = PAD ? (unsigned)(hidden >> (32 * u)) : 0;
@@ -292,7 +295,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
                 shortx8 pp[N];
                 split8<E, N>(p, pp);
                 // keys 16 e + 4 h + {0..3} and + 8 of this half: the lane's own scores
-                const int key = u * 32 + 16 * e + 4 * h + (n >> 2 & 3), col = 16 * (lane >> 4 & 1) + 4 * (n & 3);
+                const int key = ks_at * PK + u * 32 + 16 * e + 4 * h + (n >> 2 & 3), col = 16 * (lane >> 4 & 1) + 4 * (n & 3);
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) {
                     shortx8 vv[N];
@@ -307,7 +310,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
             }
         }
         if (fix) {
-            for (int key = k0; key < k0 + BN && key < len; ++key)
+            for (int key = k0 + ks_at * PK; key < k0 + (ks_at + 1) * PK && key < len; ++key)
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
 #pragma unroll
@@ -319,6 +322,46 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
         }
     }
     l = halves_sum(l);
+    if constexpr (KS == 4) {
+        // the four waves' results against their common maximum: the upper two hand theirs to the lower two, those
+        // to the first
+        static_assert(sizeof(vs) >= W / 2 * (D / 32) * 4096, "room for the results of half the waves");
+        __shared__ float mm[W][32], ll[W][32];
+        floatx4* give = (floatx4*)&vs[0][0][0];
+        if (h == 0) mm[wave][n] = m;
+        __syncthreads();                            // also: the last tile has been read
+        const int w0 = wr * KS;
+        const float mx = fmaxf(fmaxf(mm[w0][n], mm[w0 + 1][n]), fmaxf(mm[w0 + 2][n], mm[w0 + 3][n]));
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - mx) * c);
+        if (h == 0) ll[wave][n] = l * f;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) o[j] *= f;
+#pragma unroll
+        for (int half = 2; half; half /= 2) {
+            if (ks_at >= half && ks_at < 2 * half) {
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        give[((wr * 2 + ks_at - half) * (D / 32) * 4 + j * 4 + i) * 64 + lane] =
+                            floatx4{o[j][4 * i], o[j][4 * i + 1], o[j][4 * i + 2], o[j][4 * i + 3]};
+            }
+            __syncthreads();
+            if (ks_at < half) {
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const floatx4 v = give[((wr * 2 + ks_at) * (D / 32) * 4 + j * 4 + i) * 64 + lane];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[j][4 * i + x] += v[x];
+                    }
+            }
+            __syncthreads();
+        }
+        if (ks_at != 0) return;
+        l = ll[w0][n] + ll[w0 + 1][n] + ll[w0 + 2][n] + ll[w0 + 3][n];
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     T* op = (T*)a.out + (begin + row) * a.ld_out + (int64_t)head * D;
     if constexpr (WIDE && sizeof(T) == 2) {
@@ -353,14 +396,14 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
     }
 }
 
-template <typename T, int D, int W>
+template <typename T, int D, int W, int KS = 1>
 static hipError_t launch_w(const EncodeArgs& a, bool wide, int heads_log2, hipStream_t s) {
-    constexpr int BN = sizeof(T) == 4 && D == 128 ? 32 : 64;
-    const dim3 grid((unsigned)(a.n_events / (32 * W >> heads_log2) + a.batch), (unsigned)(a.n_heads >> heads_log2));
+    constexpr int BN = (sizeof(T) == 4 && D == 128 ? 32 : 64) * KS;
+    const dim3 grid((unsigned)(a.n_events / (32 * (W / KS) >> heads_log2) + a.batch), (unsigned)(a.n_heads >> heads_log2));
     const dim3 block(64 * W);
-    if (!wide) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, false, true>), grid, block, 0, s, a, heads_log2);
-    else if (a.padding) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, true>), grid, block, 0, s, a, heads_log2);
-    else hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, false>), grid, block, 0, s, a, heads_log2);
+    if (!wide) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, false, true, KS>), grid, block, 0, s, a, heads_log2);
+    else if (a.padding) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, true, KS>), grid, block, 0, s, a, heads_log2);
+    else hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, false, KS>), grid, block, 0, s, a, heads_log2);
     return hipGetLastError();
 }
 template <typename T, int D>
@@ -374,6 +417,14 @@ static hipError_t launch_d(const EncodeArgs& a, bool wide, hipStream_t s) {
     // beside the other's products.  Lifelong (66 tiles a block) 8 waves 294 us, 4 waves 312; grouped (10 tiles) 308
     // against 289.
     const int64_t tiles = (a.window < mean ? a.window : mean) / 64;
+    // A few long histories do not fill the card, and a block's time is its row of tiles: four waves then share each
+    // row's keys.  4000 events, 4 heads of 64 (125 blocks) 78 -> 39 us; 8000, one head of 128 (63) 207 -> 112; with 376
+    // blocks it would be 48 -> 77.
+    if constexpr (sizeof(T) == 2 || D == 32) {
+        const int rows_log2 = (rows << heads >= 4 ? 7 : (rows << heads == 2 ? 6 : 5)) - heads;      // of a block
+        const int64_t blocks = ((a.n_events >> rows_log2) + 1) * (a.n_heads >> heads);
+        if (tiles >= 8 && blocks < 256) return launch_w<T, D, 8, 4>(a, wide, heads ? 1 : 0, s);
+    }
     if constexpr (D == 128) {
         if (rows << heads >= 8 && tiles >= 24) return launch_w<T, D, 8>(a, wide, heads, s);
     }

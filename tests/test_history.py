@@ -579,3 +579,39 @@ def test_example_ranking_with_histories():
     want, mag, big = o.lookup(list(range(len(lens))), cq, r.window, r.sinks, (r.dim // r.heads) ** -0.5)
     tol = bound(want, mag, big, r.dim // r.heads, max(lens) + 1, torch.float32, U, 0.0)
     assert (np.abs(f64(got).reshape(want.shape) - want) <= tol).all()
+
+
+# --- few long histories: the waves of a block share a row's keys ---------------------
+
+
+@pytest.mark.parametrize("dtype,dim", [(torch.bfloat16, 32), (torch.bfloat16, 64), (torch.float16, 128),
+                                       (torch.float32, 32)])
+@pytest.mark.parametrize("heads,kv", [(1, 1), (2, 1)])
+@pytest.mark.parametrize("window,sinks,padded", [(ALL, 0, False), (600, 5, True)])
+def test_encode_few_long_histories(dtype, dim, heads, kv, window, sinks, padded):
+    lens = [1300, 733]
+    n = sum(lens)
+    q, k, v = (randn((n, h, dim), s, dtype) for s, h in ((51, heads), (52, kv), (53, kv)))
+    pad = (torch.rand(n, generator=gen(54)) < 0.3).to(torch.uint8) if padded else None
+    if padded:
+        pad[1300:1400] = 1              # rows that see nothing
+    got = dl.history_attention(q.cuda(), k.cuda(), v.cuda(), starts(lens).cuda(), window=window, sinks=sinks,
+                               padding=None if pad is None else pad.cuda())
+    check_encode(q, k, v, lens, window, sinks, got, padding=pad)
+    if padded:
+        assert torch.all(got[1300:1400] == 0)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_encode_few_long_histories_keep_what_is_not_seen_out(bad):
+    n, window = 1500, 700
+    q, k, v = (randn((n, 1, 64), s, torch.bfloat16) for s in (55, 56, 57))
+    off = torch.zeros(1, dtype=torch.int64, device="cuda")
+    clean = dl.history_attention(q.cuda(), k.cuda(), v.cuda(), off, window=window)
+    v[500] = bad
+    k[501] = bad
+    got = dl.history_attention(q.cuda(), k.cuda(), v.cuda(), off, window=window)
+    hit = torch.zeros(n, dtype=torch.bool, device="cuda")
+    hit[500:501 + window] = True
+    assert torch.equal(got[~hit], clean[~hit])
+    assert not torch.isfinite(got[hit].float()).any()
