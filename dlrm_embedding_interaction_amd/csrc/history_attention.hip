@@ -322,28 +322,30 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
         }
     }
     l = halves_sum(l);
-    if constexpr (KS == 4) {
-        // the four waves' results against their common maximum: the upper two hand theirs to the lower two, those
-        // to the first
+    if constexpr (KS > 1) {
+        // the waves' results against their common maximum: the upper half hands theirs to the lower half, and so on
+        // down to the first
         static_assert(sizeof(vs) >= W / 2 * (D / 32) * 4096, "room for the results of half the waves");
         __shared__ float mm[W][32], ll[W][32];
         floatx4* give = (floatx4*)&vs[0][0][0];
         if (h == 0) mm[wave][n] = m;
         __syncthreads();                            // also: the last tile has been read
         const int w0 = wr * KS;
-        const float mx = fmaxf(fmaxf(mm[w0][n], mm[w0 + 1][n]), fmaxf(mm[w0 + 2][n], mm[w0 + 3][n]));
+        float mx = mm[w0][n];
+#pragma unroll
+        for (int i = 1; i < KS; ++i) mx = fmaxf(mx, mm[w0 + i][n]);
         const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - mx) * c);
         if (h == 0) ll[wave][n] = l * f;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) o[j] *= f;
 #pragma unroll
-        for (int half = 2; half; half /= 2) {
+        for (int half = KS / 2; half; half /= 2) {
             if (ks_at >= half && ks_at < 2 * half) {
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        give[((wr * 2 + ks_at - half) * (D / 32) * 4 + j * 4 + i) * 64 + lane] =
+                        give[((wr * (KS / 2) + ks_at - half) * (D / 32) * 4 + j * 4 + i) * 64 + lane] =
                             floatx4{o[j][4 * i], o[j][4 * i + 1], o[j][4 * i + 2], o[j][4 * i + 3]};
             }
             __syncthreads();
@@ -352,7 +354,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
                 for (int j = 0; j < D / 32; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const floatx4 v = give[((wr * 2 + ks_at) * (D / 32) * 4 + j * 4 + i) * 64 + lane];
+                        const floatx4 v = give[((wr * (KS / 2) + ks_at) * (D / 32) * 4 + j * 4 + i) * 64 + lane];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) o[j][4 * i + x] += v[x];
                     }
@@ -360,7 +362,9 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
             __syncthreads();
         }
         if (ks_at != 0) return;
-        l = ll[w0][n] + ll[w0 + 1][n] + ll[w0 + 2][n] + ll[w0 + 3][n];
+        l = ll[w0][n];
+#pragma unroll
+        for (int i = 1; i < KS; ++i) l += ll[w0 + i][n];
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     T* op = (T*)a.out + (begin + row) * a.ld_out + (int64_t)head * D;
@@ -417,13 +421,14 @@ static hipError_t launch_d(const EncodeArgs& a, bool wide, hipStream_t s) {
     // beside the other's products.  Lifelong (66 tiles a block) 8 waves 294 us, 4 waves 312; grouped (10 tiles) 308
     // against 289.
     const int64_t tiles = (a.window < mean ? a.window : mean) / 64;
-    // A few long histories do not fill the card, and a block's time is its row of tiles: four waves then share each
-    // row's keys.  4000 events, 4 heads of 64 (125 blocks) 78 -> 39 us; 8000, one head of 128 (63) 207 -> 112; with 376
+    // A few long histories do not fill the card, and a block's time is its row of tiles: four waves (two, where three
+    // parts of each element fill the LDS) then share each row's keys.  4000 events, 4 heads of 64 (125 blocks) 78 -> 39 us; 8000, one head of 128 (63) 207 -> 112; with 376
     // blocks it would be 48 -> 77.
-    if constexpr (sizeof(T) == 2 || D == 32) {
-        const int rows_log2 = (rows << heads >= 4 ? 7 : (rows << heads == 2 ? 6 : 5)) - heads;      // of a block
-        const int64_t blocks = ((a.n_events >> rows_log2) + 1) * (a.n_heads >> heads);
-        if (tiles >= 8 && blocks < 256) return launch_w<T, D, 8, 4>(a, wide, heads ? 1 : 0, s);
+    const int rows_log2 = (rows << heads >= 4 ? 7 : (rows << heads == 2 ? 6 : 5)) - heads;      // of a block
+    const int64_t blocks = ((a.n_events >> rows_log2) + 1) * (a.n_heads >> heads);
+    if (tiles >= 8 && blocks < 256) {
+        if constexpr (sizeof(T) == 2 || D == 32) return launch_w<T, D, 8, 4>(a, wide, heads ? 1 : 0, s);
+        else return launch_w<T, D, 4, 2>(a, wide, heads ? 1 : 0, s);
     }
     if constexpr (D == 128) {
         if (rows << heads >= 8 && tiles >= 24) return launch_w<T, D, 8>(a, wide, heads, s);

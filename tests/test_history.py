@@ -585,7 +585,7 @@ def test_example_ranking_with_histories():
 
 
 @pytest.mark.parametrize("dtype,dim", [(torch.bfloat16, 32), (torch.bfloat16, 64), (torch.float16, 128),
-                                       (torch.float32, 32)])
+                                       (torch.float32, 32), (torch.float32, 64), (torch.float32, 128)])
 @pytest.mark.parametrize("heads,kv", [(1, 1), (2, 1)])
 @pytest.mark.parametrize("window,sinks,padded", [(ALL, 0, False), (600, 5, True)])
 def test_encode_few_long_histories(dtype, dim, heads, kv, window, sinks, padded):
