@@ -35,7 +35,7 @@ struct LookupArgs {
     void* out;
     float* partial;
     int64_t ld_q, ld_out, window, sinks;
-    int batch, queries, n_heads;
+    int batch, queries, n_heads, wide;      // wide: rows of q and out are 16-byte aligned
     float scale;
 };
 
@@ -170,6 +170,18 @@ __device__ __forceinline__ Raw<T> load_raw(const T* p) {
     }
     return r;
 }
+// Four consecutive elements, at once where their row is aligned.
+template <typename T>
+__device__ __forceinline__ void store4(T* p, floatx4 v, int wide) {
+    if (wide) {
+        typedef T t4 __attribute__((ext_vector_type(4)));
+        *(t4*)p = t4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = (T)v[i];
+    }
+}
+
 // The largest magnitude among elements as bits, without their sign (16-bit
 // types: of the even and of the odd elements).  Infinities and NaN come out above
 // every finite value.

@@ -171,6 +171,8 @@ DLRM_API dlrm_status_t dlrm_history_lookup(const dlrm_history_cache_t* c, const 
     a.ld_q = ld_q, a.ld_out = ld_out;
     a.window = at->window, a.sinks = at->sinks;
     a.batch = (int)batch, a.queries = queries, a.n_heads = at->n_heads;
+    const int64_t step = at->dtype == DLRM_DTYPE_F32 ? 4 : 8;
+    a.wide = ld_q % step == 0 && ld_out % step == 0 && (((uintptr_t)q | (uintptr_t)out) & 15u) == 0;
     a.scale = at->scale;
     return from_hip(launch_history_lookup(a, at->dtype, (hipStream_t)stream));
 }

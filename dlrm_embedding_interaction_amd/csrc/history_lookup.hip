@@ -207,9 +207,10 @@ __global__ __launch_bounds__(DIRECT ? 64 * DIRECT : 256, 2) void history_lookup_
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 const int d0 = D == 32 ? g * 8 : (s >> 1) * 64 + g * 16 + (s & 1) * 8;
+                const Raw<T> raw = a.wide ? load_raw<true>(qp + d0) : load_raw<false>(qp + d0);
                 float x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = live ? (a.scale < 0.f ? -(float)qp[d0 + i] : (float)qp[d0 + i]) : 0.f;
+                for (int i = 0; i < 8; ++i) x[i] = a.scale < 0.f ? -(float)raw.x[i] : (float)raw.x[i];
                 split8<NQ>(x, q[s]);
             }
         }
@@ -373,8 +374,7 @@ __global__ __launch_bounds__(DIRECT ? 64 * DIRECT : 256, 2) void history_lookup_
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 T* op = (T*)a.out + ((int64_t)b * a.queries + row / group) * a.ld_out +
                         (int64_t)(hk * group + row % group) * D + d;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) op[i] = (T)(sum == 0.f ? 0.f : v[i] * inv);
+                store4(op, v * inv, a.wide);
             }
         } else if (DIRECT || (i0 == 0 && i1 == sp.count)) {
             if (live) {
@@ -382,8 +382,7 @@ __global__ __launch_bounds__(DIRECT ? 64 * DIRECT : 256, 2) void history_lookup_
                 T* op = (T*)a.out + qrow * a.ld_out + (int64_t)qhead * D;
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) op[16 * j + 4 * g + i] = (T)(l == 0.f ? 0.f : o[j][i] * inv);
+                    store4(op + 16 * j + 4 * g, o[j] * inv, a.wide);
             }
         } else if (n < cols) {
             // a run cuts at most the history it begins in and the one it ends in
