@@ -64,7 +64,7 @@ struct AppendArgs {
     const void *k, *v, *offsets;
     NeedWs ws;
     int64_t ld_k, ld_v, n_events;
-    int batch, idx32;
+    int batch, idx32, per_event;        // per_event: one unit of work per event (see the kernel), not per page
 };
 
 hipError_t launch_history_attention(const EncodeArgs& a, int dtype, int dim, hipStream_t s);

@@ -27,9 +27,8 @@
 // rounding them to one would add an error as large as the output's own rounding.
 //
 // Measured on MI355X: 128 histories of up to 32000 events, 8 kv heads of 128, 32
-// query heads, bf16: 817-825 us, 5.7-5.8 TB/s of codes, 92% of what a plain read
-// stream reaches (6.28 TB/s).  256 histories, window 1024, 4 kv heads of 64: 32 us,
-// 3.9 TB/s; there the dependent reads length -> page -> codes and the ~300 vector
+// query heads, bf16: 817 us, 5.8 TB/s of codes, 92% of what a plain read stream
+// reaches (6.28 TB/s).  256 histories, window 1024, 4 kv heads of 64: 31 us, 4.0 TB/s; there the dependent reads length -> page -> codes and the ~300 vector
 // instructions a tile (decoding, exponentials, splitting) show.
 #include "history.h"
 

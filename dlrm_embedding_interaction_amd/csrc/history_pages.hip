@@ -10,7 +10,7 @@
 //
 // Measured on MI355X: appending 128 histories of up to 1000 events, 8 kv heads of
 // 128, bf16 (466 MB): 100 us, 4.7 TB/s, against 5.0 for a large copy.  One event for
-// each of 512 histories: 9 us, of 1500 with a copied page each 48: there a wave's
+// each of 512 histories: 8 us, of 1500 with a copied page each 42: there a wave's
 // five dependent reads (offsets, need, list, scale, codes) are what it takes.  The
 // list of 32000 pages 7 us, of 11000 5.
 #include "history.h"
@@ -252,11 +252,19 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void history_append_ke
     const int lane = threadIdx.x & 63;
     const int item = __builtin_amdgcn_readfirstlane((int)blockIdx.y * 4 + (int)(threadIdx.x >> 6));
     if (item >= 2 * c.n_kv_heads) return;
-    const Unit un = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, PE, 2, blockIdx.x);
+    // Units are pages, with room for two more than a history's events fill; or, where that would be more, its
+    // events, of which the first in each page does the page's work.
+    Unit un = history_of_unit(a.offsets, a.idx32, a.batch, a.n_events, a.per_event ? 1 : PE, a.per_event ? 0 : 2,
+                              blockIdx.x);
     const int64_t count = un.end - un.begin;
     const Need g = a.ws.need[un.b];
     const int slot = a.slots ? a.slots[un.b] : un.b;
     if (un.nth < 0 || g.old_len < 0 || count == 0) return;
+    if (a.per_event) {
+        const int64_t at = g.old_len + un.nth;
+        if (un.nth >= count || (un.nth > 0 && at % PE != 0)) return;
+        un.nth = at / PE - g.old_len / PE;
+    }
     const int64_t page_no = g.old_len / PE + un.nth, stop = g.old_len + count;
     if (page_no * PE >= stop) return;
     const int n_free = *a.ws.n_free, before = pages_before(a.ws, un.b);
@@ -708,11 +716,14 @@ static void launch_append(const AppendArgs& a, dim3 grid, hipStream_t s) {
     else launch_append<T, 128>(a, wide, grid, s);
 }
 
-hipError_t launch_history_append(const AppendArgs& a, int dtype, hipStream_t s) {
+hipError_t launch_history_append(const AppendArgs& args, int dtype, hipStream_t s) {
+    AppendArgs a = args;
     hipLaunchKernelGGL(history_need_kernel, dim3((a.batch + kNeedBlock - 1) / kNeedBlock), dim3(kNeedBlock), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)(a.n_events / a.c.page_events + 2 * (int64_t)a.batch + 1), (unsigned)((2 * a.c.n_kv_heads + 3) / 4));
+    const int64_t by_page = a.n_events / a.c.page_events + 2 * (int64_t)a.batch;
+    a.per_event = a.n_events <= by_page;
+    const dim3 grid((unsigned)((a.per_event ? a.n_events : by_page) + 1), (unsigned)((2 * a.c.n_kv_heads + 3) / 4));
     if (dtype == DLRM_DTYPE_F32) launch_append<float>(a, grid, s);
     else if (dtype == DLRM_DTYPE_BF16) launch_append<bf16>(a, grid, s);
     else launch_append<f16>(a, grid, s);

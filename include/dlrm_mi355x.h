@@ -471,7 +471,8 @@ typedef struct dlrm_attention {
  *              seen by no one.  Infinities and NaN in events a row does not
  *              see do not reach it.
  * out must not overlap q, k or v.  Rows of 16-byte aligned tensors whose ld is
- * a multiple of 16 bytes are read 16 bytes at a time, others by element.
+ * a multiple of 16 bytes are read 16 bytes at a time, others by element.  ld_k
+ * and ld_v above 2^30 give DLRM_E_UNSUPPORTED.
  */
 dlrm_status_t dlrm_history_attention(const dlrm_attention_t* a, int64_t batch, int64_t n_events,
                                      const void* offsets, int32_t index_bytes, const void* q, int64_t ld_q,

@@ -615,3 +615,19 @@ def test_encode_few_long_histories_keep_what_is_not_seen_out(bad):
     hit[500:501 + window] = True
     assert torch.equal(got[~hit], clean[~hit])
     assert not torch.isfinite(got[hit].float()).any()
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_append_a_few_events_to_many_histories(page):
+    """Fewer events than two for each history: a page's first event does the page's work, also where a history's
+    few events open a second page, and where histories get none."""
+    p = Pair(80, 16, 5, 2, 32, page, torch.bfloat16)
+    p.append(list(range(16)), [page - 1, page, page + 1, 1, 0, 2 * page - 1, 3, page - 2] * 2)
+    for counts in ([2] * 16, [1] * 16, [0, 2, 1, 3, 5, 0, 2, 2] * 2, [0] * 15 + [1], [page + 3] + [0] * 15):
+        p.append(list(range(16)), counts, 2.0)
+        p.same()
+    p.cpu.fork([0, 1, 2], [13, 14, 15])
+    p.gpu.fork(p.slots([0, 1, 2]), p.slots([13, 14, 15]))
+    p.append([13, 14, 15, 3], [1, 2, 0, 1], 4.0)
+    p.same()
+    p.lookup(list(range(16)), 4)
