@@ -146,7 +146,6 @@ __device__ __forceinline__ float wave_max(float v) {
     for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
     return v;
 }
-__device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
 
 // Eight consecutive elements of a row, as they are in memory.
 template <typename T>
