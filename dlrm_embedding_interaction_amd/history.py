@@ -198,6 +198,7 @@ class HistoryCache:
                             refs.data_ptr(), free_pages.data_ptr(), counters.data_ptr())
         self._ref = ctypes.byref(self._desc)
         self._ws = {}           # stream -> workspace: calls on two streams may overlap
+        self._kept = []
         self._need = {}
 
     def _workspace(self, stream: int, batch: int, queries: int = 0, heads: int = 0) -> torch.Tensor:
@@ -210,7 +211,10 @@ class HistoryCache:
             self._need[key] = need
         ws = self._ws.get(stream)
         if ws is None or ws.numel() < need:
-            ws = self._ws[stream] = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            grown = 256 if ws is None else 2 * ws.numel()       # doubled: what is kept below stays under one more
+            if ws is not None:
+                self._kept.append(ws)                           # a captured graph may still write to it
+            ws = self._ws[stream] = torch.empty(max(need, grown), dtype=torch.uint8, device=self.device)
         return ws
 
     def _slots(self, slots: Optional[torch.Tensor], batch: int):

@@ -548,6 +548,33 @@ def test_cache_calls_in_a_graph():
             assert torch.equal(getattr(caches[0], n), getattr(caches[1], n)), n
 
 
+def test_graph_keeps_its_workspace_when_a_later_call_needs_more():
+    """A captured lookup, whose runs meet in the workspace, replayed after calls of larger batches on its stream and
+    after their like has been allocated anew."""
+    n = 65 * 64
+    c = dl.HistoryCache(2 * 65, 66, 65, 2, 64, 64)
+    k, v = (randn((2 * n, 2, 64), s, torch.bfloat16).cuda() for s in (51, 52))
+    c.append(k, v, torch.arange(2, dtype=torch.int64, device="cuda") * n)
+    q = randn((1, 8, 64), 53, torch.bfloat16).cuda()
+    large = randn((66, 30, 8, 64), 54, torch.bfloat16).cuda()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = c.lookup(q)
+        out = torch.empty_like(q)
+        with torch.cuda.graph(g, stream=side):
+            c.lookup(q, out=out)
+        c.lookup(large)
+        fills = [torch.full((1 << s,), 77, dtype=torch.uint8, device="cuda") for s in range(9, 26) for _ in range(3)]
+        for _ in range(3):
+            out.zero_()
+            g.replay()
+            side.synchronize()
+            assert torch.equal(out, want)
+            assert all(bool((f == 77).all()) for f in fills)
+            c.lookup(large)
+
+
 # --- the example: all of them together ----------------------------------------------
 
 
