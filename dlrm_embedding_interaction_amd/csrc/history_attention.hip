@@ -414,16 +414,21 @@ template <typename T, int D>
 static hipError_t launch_d(const EncodeArgs& a, bool wide, hipStream_t s) {
     const int64_t mean = a.n_events / a.batch;
     const int group = a.n_heads / a.n_kv;
-    // log2 of the heads that share a block, and its rows in 32s
+    // Log2 of the heads that share a block, and its rows in 32s.  Blocks of 32 rows waste fewest on short histories,
+    // larger ones share their tiles.  Measured, 32 rows against 64: 1024 histories of 20, 4 heads of 32, fp16 9.2 us to
+    // 12.4, of 32 15.9 to 13.2; 2048 of 20, 4 heads of 64, bf16 36 to 31; up to 128 events, 4 heads of 128 on two kv
+    // heads, bf16 51 to 52, up to 160 66 to 65; 4 heads of 64 on two, fp32, up to 40 41 to 39.
     const int heads = group % 4 == 0 ? 2 : (group % 2 == 0 ? 1 : 0);
-    const int rows = mean <= 32 ? 1 : (mean <= 96 ? 2 : 4);
+    const bool one = heads ? sizeof(T) == 2 && mean <= 72 : D == 32 && mean <= 24;
+    // 64 rows against 128, 2048 of up to 128, 4 heads of 64, bf16: 61 us to 62, of up to 192 106 to 110.
+    const int rows = one ? 1 : (mean <= 96 ? 2 : 4);
     // Blocks of 8 waves read each tile once for twice the rows, blocks of 4 leave two to a CU, one's loads and stores
     // beside the other's products.  Lifelong (66 tiles a block) 8 waves 294 us, 4 waves 312; grouped (10 tiles) 308
     // against 289.
     const int64_t tiles = (a.window < mean ? a.window : mean) / 64;
     // A few long histories do not fill the card, and a block's time is its row of tiles: four waves (two, where three
-    // parts of each element fill the LDS) then share each row's keys.  4000 events, 4 heads of 64 (125 blocks) 78 -> 39 us; 8000, one head of 128 (63) 207 -> 112; with 376
-    // blocks it would be 48 -> 77.
+    // parts of each element fill the LDS) then share each row's keys.  4000 events, 4 heads of 64 (125 blocks)
+    // 78 -> 39 us; 8000, one head of 128 (63) 207 -> 112; with 376 blocks it would be 48 -> 77.
     const int rows_log2 = (rows << heads >= 4 ? 7 : (rows << heads == 2 ? 6 : 5)) - heads;      // of a block
     const int64_t blocks = ((a.n_events >> rows_log2) + 1) * (a.n_heads >> heads);
     if (tiles >= 8 && blocks < 256) {
@@ -434,8 +439,10 @@ static hipError_t launch_d(const EncodeArgs& a, bool wide, hipStream_t s) {
         if (rows << heads >= 8 && tiles >= 24) return launch_w<T, D, 8>(a, wide, heads, s);
     }
     if (rows << heads >= 4) return launch_w<T, D, 4>(a, wide, heads, s);
-    if (rows << heads == 2) return launch_w<T, D, 2>(a, wide, heads, s);
-    return launch_w<T, D, 1>(a, wide, heads, s);
+    if constexpr (D == 32) {
+        if (rows << heads == 1) return launch_w<T, D, 1>(a, wide, heads, s);
+    }
+    return launch_w<T, D, 2>(a, wide, heads, s);
 }
 template <typename T>
 static hipError_t launch_t(const EncodeArgs& a, int dim, hipStream_t s) {

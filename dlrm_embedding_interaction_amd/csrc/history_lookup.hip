@@ -28,7 +28,8 @@
 //
 // Measured on MI355X: 128 histories of up to 32000 events, 8 kv heads of 128, 32
 // query heads, bf16: 817 us, 5.8 TB/s of codes, 92% of what a plain read stream
-// reaches (6.28 TB/s).  256 histories, window 1024, 4 kv heads of 64: 31 us, 4.0 TB/s; there the dependent reads length -> page -> codes and the ~300 vector
+// reaches (6.28 TB/s).  256 histories, window 1024, 4 kv heads of 64: 31 us, 4.0
+// TB/s; there the dependent reads length -> page -> codes and the ~300 vector
 // instructions a tile (decoding, exponentials, splitting) show.
 #include "history.h"
 
@@ -37,8 +38,10 @@ namespace dlrm {
 constexpr int kTile = 64;                // events per tile
 constexpr int kLookupWaves = 2048;       // waves a launch aims at: two on each SIMD
 // Histories of at most this many tiles have a block of their own: no second kernel, but the longest history sets the
-// time (96 histories of up to 24 tiles 18.7 us, in runs 30.8).
-constexpr int kDirectTiles = 32;
+// time.  Measured, blocks against runs: 96 histories of up to 24 tiles 18.7 us to 30.8; 256 (4 kv heads of 64) of up to
+// 24 27.2 to 30.0, of up to 40 40.5 to 37.4.  Where eight waves share a block the longest costs less: 64 of up to 40
+// tiles 15.4 to 24.4, eight of up to 40 11.4 to 11.9, of up to 64 15.6 to 13.8.
+constexpr int kDirectTiles = 32, kDirectTiles8 = 48;
 
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -539,9 +542,9 @@ static hipError_t launch_t(LookupArgs a, hipStream_t s) {
     const int hc = (rows + 15) / 16 * a.c.n_kv_heads;
     int* meta = (int*)a.partial;
     a.partial = (float*)((char*)a.partial + meta_bytes(a.batch));
-    if (most_tiles(a) <= kDirectTiles) {
+    const int w = direct_waves((int64_t)a.batch * hc, D == 32 || (D == 64 && Parts<T>::q == 1) ? 12 : 8);
+    if (most_tiles(a) <= (w == 8 ? kDirectTiles8 : kDirectTiles)) {
         const dim3 grid(a.batch, hc);
-        const int w = direct_waves((int64_t)a.batch * hc, D == 32 || (D == 64 && Parts<T>::q == 1) ? 12 : 8);
         if (w == 8) hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 8>), grid, dim3(512), 0, s, a, 0, meta);
         else if (w == 4) hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 4>), grid, dim3(256), 0, s, a, 0, meta);
         else if (w == 2) hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 2>), grid, dim3(128), 0, s, a, 0, meta);
@@ -550,9 +553,10 @@ static hipError_t launch_t(LookupArgs a, hipStream_t s) {
     }
     const int waves = waves_of(a.c, a.batch, a.queries, a.n_heads);
     hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 0>), dim3(waves / 4, hc), dim3(256), 0, s, a, waves, meta);
-    // a few long histories are cut into many runs each: their elements are then spread over blocks, too
+    // A few long histories are cut into many runs each: their elements are then spread over blocks, too.  64 histories
+    // of up to 64 tiles, 8 waves each: 27.5 -> 23.0 us; 256, two waves each, would go 50.9 -> 53.3.
     const int cols = rows < 16 ? rows : 16;
-    const int z = waves / a.batch >= 16 ? (cols * D + 63) / 64 : 1;
+    const int z = waves / a.batch >= 8 ? (cols * D + 63) / 64 : 1;
     hipLaunchKernelGGL((history_join_kernel<D, T>), dim3(a.batch, hc, z), dim3(256), 0, s, a, meta);
     return hipGetLastError();
 }
