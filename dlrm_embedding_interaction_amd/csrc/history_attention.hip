@@ -274,9 +274,11 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i]);
             top = halves_max(top);
             // the maximum a row's weights are taken against may lag the true one by 2^8: weights then stay below
-            // that, far from the end of every type, and most tiles leave the sums as they are
-            if (__any((top - m) * c > 8.f)) {
-                const float mx = fmaxf(m, top);
+            // that, far from the end of every type, and most tiles leave the sums as they are.  Each row decides for
+            // itself, so that its bits do not depend on the rows that share its wave.
+            const bool up = (top - m) * c > 8.f;
+            if (__any(up)) {
+                const float mx = up ? top : m;
                 const float alpha = mx == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mx) * c);
                 l *= alpha;
 #pragma unroll
