@@ -73,12 +73,19 @@ __device__ __forceinline__ floatx16 mul_parts(const shortx8* a, const shortx8* b
     }
 }
 
+// The largest fp32 value that rounds to a finite bf16 one.  Finite values beyond it
+// would have an infinite first part; cut to it, theirs is the largest bf16 and the
+// rest is exact as before.
+constexpr float kLargestFirst = 0x1.fefffep+127f;
+__device__ __forceinline__ float first_part(float x) { return fminf(fmaxf(x, -kLargestFirst), kLargestFirst); }
+
 // Eight fp32 values as N vectors of parts, the first the rounded values, each
-// next one the rounded rest.
-template <typename E, int N>
-__device__ __forceinline__ void split8(const float* x, shortx8* part) {
+// next one the rounded rest.  LARGE: values beyond kLargestFirst are met.  Returns
+// 0, or NaN where a rest is not finite.
+template <typename E, int N, bool LARGE = false>
+__device__ __forceinline__ float split8(const float* x, shortx8* part) {
     typedef E Ex8 __attribute__((ext_vector_type(8)));
-    float r[8];
+    float r[8], odd = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = x[i];
 #pragma unroll
@@ -86,19 +93,22 @@ __device__ __forceinline__ void split8(const float* x, shortx8* part) {
         Ex8 e;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            e[i] = (E)r[i];
+            e[i] = (E)(LARGE && n == 0 ? first_part(r[i]) : r[i]);
             if (n + 1 < N) r[i] -= (float)e[i];
+            if (n + 2 == N) odd = fmaf(r[i], 0.f, odd);
         }
         part[n] = __builtin_bit_cast(shortx8, e);
     }
+    return odd;
 }
 
-template <typename T>
-__device__ __forceinline__ void to_parts(const Raw<T>& r, shortx8* part) {
+template <bool LARGE = false, typename T>
+__device__ __forceinline__ float to_parts(const Raw<T>& r, shortx8* part) {
     if constexpr (Mul<T>::parts == 1) {
         part[0] = __builtin_bit_cast(shortx8, r);
+        return 0.f;
     } else {
-        split8<bf16, 3>(r.x, part);
+        return split8<bf16, 3, LARGE>(r.x, part);
     }
 }
 template <typename T>
@@ -107,6 +117,14 @@ __device__ __forceinline__ bool finite_bits(T x) {
     const unsigned short all = sizeof(T) == 2 && __is_same(T, f16) ? 0x7c00 : 0x7f80;
     if constexpr (sizeof(T) == 2) return (__builtin_bit_cast(unsigned short, x) & all) != all;
     return true;
+}
+
+// The three parts of one fp32 value, `apart` elements from one another.
+__device__ __forceinline__ void split_large(float x, bf16* part, int apart) {
+    part[0] = (bf16)first_part(x);
+    x -= (float)part[0];
+    part[apart] = (bf16)x;
+    part[2 * apart] = (bf16)(x - (float)part[apart]);
 }
 
 // Four keys of 16 columns, turned: lane j of a group of 16 points at key
@@ -142,7 +160,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
     static_assert(BN * D / 8 % THREADS == 0, "whole vectors per thread");
     __shared__ __attribute__((aligned(16))) E ks[N][BN][KP];
     __shared__ __attribute__((aligned(16))) E vs[N][BN][VP];
-    __shared__ int odd[2];                          // the values of even / odd tiles hold an infinity or NaN
+    __shared__ int odd[2];      // even / odd tiles hold an infinity or NaN among their values (fp32: parts of either)
 
     const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);      // conditions on it are scalar branches
@@ -180,7 +198,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
             Raw<T> r = load_raw<WIDE>(qp + 16 * s + 8 * h);
-            to_parts(r, q[s]);
+            to_parts<true>(r, q[s]);
 #pragma unroll
             for (int i = 0; i < N; ++i) q[s][i] ^= a.scale < 0.f ? (short)0x8000 : (short)0;
         }
@@ -216,29 +234,45 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
         __syncthreads();                            // the tile before has been read
         if (tid == 0) odd[(t + 1) & 1] = 0;
         unsigned big = 0;
+        float rest = 0.f;
 #pragma unroll
         for (int x = 0; x < VEC; ++x) {
             const int p = tid + x * THREADS, key = p / (D / 8), d = p % (D / 8) * 8;
             shortx8 kp[N], vp[N];
-            to_parts(kr[x], kp);
-            to_parts(vr[x], vp);
-            top_magnitude(vr[x], big);
+            rest += to_parts(kr[x], kp);
+            rest += to_parts(vr[x], vp);
+            if constexpr (N == 1) top_magnitude(vr[x], big);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 *(shortx8*)&ks[i][key][d] = kp[i];
                 *(shortx8*)&vs[i][key][d] = vp[i];
             }
         }
-        if (odd_magnitude<T>(big)) odd[t & 1] = 1;
+        if (N == 1 ? odd_magnitude<T>(big) : rest != 0.f) odd[t & 1] = 1;       // NaN differs from 0
         __syncthreads();
         if (t + 1 < tiles) fetch(t + 1);
         const bool fix = odd[t & 1] != 0;
         if (fix) {
-            // such values are taken out of the products and added to the rows that see them
-            for (int p = tid; p < BN * D; p += THREADS)
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (!finite_bits(vs[i][p / D][p % D])) vs[i][p / D][p % D] = (E)0.f;
+            // such values are taken out of the products and added to the rows that see them; finite fp32 keys and values
+            // whose first part is not finite are split anew
+            int p = tid;
+            asm volatile("" : "+v"(p));     // what follows from it is worked out here, not kept in registers beside the tiles
+            for (; p < BN * D; p += THREADS) {
+                const int key = p / D, d = p % D;
+                if constexpr (N > 1) {
+                    const int64_t at = min(k0 + key, len - 1);
+                    if (!finite_bits(ks[0][key][d])) {
+                        const float x = kg[at * a.ld_k + d];
+                        if (finite_bits(x)) split_large(x, &ks[0][key][d], BN * KP);
+                    }
+                    if (!finite_bits(vs[0][key][d])) {
+                        const float x = vg[at * a.ld_v + d];
+                        split_large(finite_bits(x) ? x : 0.f, &vs[0][key][d], BN * VP);
+                    }
+                } else if (!finite_bits(vs[0][key][d])) {
+                    vs[0][key][d] = (E)0.f;
+                }
+            }
             __syncthreads();
         }
         // 32 keys at a time, those that no row of the wave sees left out

@@ -37,3 +37,62 @@ def test_encode_rows_do_not_depend_on_their_neighbours(dtype, lens, dim):
     got = encode(q, k, v, lens)
     assert torch.equal(got[~loud], want[~loud])
     assert not torch.equal(got[loud], want[loud])
+
+
+# --- fp32: finite values next to the largest one ------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [MAX32, -MAX32, 3.3962e38, 3.3961e38])
+@pytest.mark.parametrize("lens,window,dim", [([90, 61, 40], 20, 64), ([90, 61, 40], 20, 128), ([1500], 700, 32),
+                                             ([1500], 700, 64), ([1300, 200], 700, 128)])
+def test_encode_fp32_large_values_do_not_reach_rows_that_do_not_see_them(value, lens, window, dim):
+    n, at = sum(lens), 50
+    q, k, v = (randn((n, 1, dim), s, torch.float32) for s in (1, 2, 3))
+    pad = torch.zeros(n, dtype=torch.uint8)
+    pad[[10, 95, 96]] = 1
+    clean = encode(q, k, v, lens, pad, window=window)
+    k2, v2 = k.clone(), v.clone()
+    for t in (k2, v2):
+        t[[10, 96]] = value
+        t[at] = value
+    hit = torch.zeros(n, dtype=torch.bool)
+    hit[at:min(at + window, lens[0])] = True
+    for kk in (k2, k):
+        got = encode(q, kk, v2, lens, pad, window=window)
+        assert torch.equal(got[~hit], clean[~hit])
+    # beside an infinity, which changes how the tile is worked on
+    v2[95] = float("inf")
+    assert torch.equal(encode(q, k2, v2, lens, pad, window=window)[~hit], clean[~hit])
+    # a row that sees a large value feels it in that element alone
+    v3 = v.clone()
+    v3[at, :, 7] = value
+    got = encode(q, k, v3, lens, pad, window=window)
+    other = torch.arange(dim) != 7
+    assert torch.equal(got[:, :, other], clean[:, :, other])
+    assert torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [3.3999e38, -3.3999e38, 3.3962e38])
+@pytest.mark.parametrize("lens", [[70, 9], [1300]])
+def test_encode_fp32_large_values_count_as_they_are(value, lens):
+    n, dim = sum(lens), 64
+    q, k, v = (randn((n, 2, dim), s, torch.float32) for s in (4, 5, 6))
+    # a large value of q or k meets zeros: it changes nothing
+    q[:, :, 3], k[:, :, 3], q[:, :, 40], k[:, :, 40] = 0, 0, 0, 0
+    clean = encode(q, k, v, lens)
+    q[20, :, 3] = value
+    k[33, :, 40] = value
+    assert torch.equal(encode(q, k, v, lens), clean)
+    # a weight of 1: six products of parts, those left out (3 u), the weight, its sum and the division
+    v[33] = value
+    v[34, :, ::2] = -value
+    got = encode(q, k, v, lens, window=1)
+    assert bool(((got.double() - v.double()).abs() <= 16 * U * v.double().abs()).all())
+    # beside a value that is not finite in the same tile
+    v[35, :, 1] = float("inf")
+    got = encode(q, k, v, lens, window=1)
+    fin = torch.isfinite(v)
+    assert bool(((got.double() - v.double()).abs() <= 16 * U * v.double().abs())[fin].all())
+    assert not torch.isfinite(got[~fin]).any()
