@@ -253,8 +253,8 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
         if (t + 1 < tiles) fetch(t + 1);
         const bool fix = odd[t & 1] != 0;
         if (fix) {
-            // such values are taken out of the products and added to the rows that see them; finite fp32 keys and values
-            // whose first part is not finite are split anew
+            // such values are taken out of the products and added to the rows that see them, fp32 keys' to the scores;
+            // finite fp32 keys and values whose first part is not finite are split anew
             int p = tid;
             asm volatile("" : "+v"(p));     // what follows from it is worked out here, not kept in registers beside the tiles
             for (; p < BN * D; p += THREADS) {
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
                     const int64_t at = min(k0 + key, len - 1);
                     if (!finite_bits(ks[0][key][d])) {
                         const float x = kg[at * a.ld_k + d];
-                        if (finite_bits(x)) split_large(x, &ks[0][key][d], BN * KP);
+                        split_large(finite_bits(x) ? x : 0.f, &ks[0][key][d], BN * KP);
                     }
                     if (!finite_bits(vs[0][key][d])) {
                         const float x = vg[at * a.ld_v + d];
@@ -287,6 +287,22 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
 #pragma unroll
                 for (int i = 0; i < N; ++i) kk[i] = *(const shortx8*)&ks[i][ks_at * PK + u * 32 + n][16 * x + 8 * h];
                 s = mul_parts<E, N>(kk, q[x], s);
+            }
+            if constexpr (N > 1) {
+                if (fix) {
+                    // infinities and NaN of the keys by the queries' first parts, which have their signs and zeros: with
+                    // all parts an infinity would meet the zeros among the others
+                    const T* kp = kg + (int64_t)min(k1 + n, len - 1) * a.ld_k + 8 * h;
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        Raw<T> r = load_raw<false>(kp + 16 * x);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) r.x[i] = finite_bits(r.x[i]) ? (T)0.f : r.x[i];
+                        shortx8 e[N];
+                        to_parts(r, e);
+                        s = mfma(e[0], q[x][0], s, E{});
+                    }
+                }
             }
             const unsigned off = PAD ? (unsigned)(hidden >> (32 * u)) : 0;
             if (k1 + 31 > r0 || (r0 + 31 - k1 >= window && k1 + 32 > sinks) || off) {

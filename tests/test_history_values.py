@@ -96,3 +96,33 @@ def test_encode_fp32_large_values_count_as_they_are(value, lens):
     fin = torch.isfinite(v)
     assert bool(((got.double() - v.double()).abs() <= 16 * U * v.double().abs())[fin].all())
     assert not torch.isfinite(got[~fin]).any()
+
+
+# --- infinite keys -------------------------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lens,dim", [([90, 61], 64), ([90, 61], 128), ([1300], 32), ([1300], 128)])
+@pytest.mark.parametrize("scale", [0.125, -0.125])
+def test_encode_a_key_of_minus_infinity_has_no_weight(dtype, lens, dim, scale):
+    """Element 3 of every query is positive, of some keys -inf (+inf where the scale is negative): their logits are
+    -inf, and they count as events that nothing sees."""
+    n, bad = sum(lens), -math.copysign(math.inf, scale)
+    q, k, v = (randn((n, 2, dim), s, dtype) for s in (7, 8, 9))
+    q[:, :, 3] = q[:, :, 3].abs() + 0.5
+    q[5, :, 3] = 1                      # one part holds it whole: the other parts are zeros
+    pad = torch.zeros(n, dtype=torch.uint8)
+    gone = [0, 4, 40, 60, 88]
+    pad[gone] = 1
+    want = encode(q, k, v, lens, pad, scale=scale)
+    k[gone, :, 3] = bad
+    got = encode(q, k, v, lens, torch.zeros_like(pad), scale=scale)
+    rows = torch.arange(n) > 0          # row 0 sees nothing else
+    assert torch.equal(got[rows], want[rows])
+    # against the sign of the queries: +inf, and what follows is not a number
+    k[60, :, 3] = -bad
+    got = encode(q, k, v, lens, torch.zeros_like(pad), scale=scale)
+    assert torch.equal(got[1:60], want[1:60])
+    assert torch.isnan(got[60:lens[0]].float()).all()
+    assert torch.equal(got[lens[0]:], want[lens[0]:])
