@@ -144,6 +144,11 @@ __device__ __forceinline__ float halves_sum(float v) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Log2 of what a weight is multiplied by, and with it the row's sum.  Weights taken
+// against a maximum that lags by 2^8 then stay below 1: a mean of large values
+// passes the type's end on its way only where their sum does.
+template <typename T> constexpr float kWeightLog2 = __is_same(T, f16) ? 0.f : -8.f;
+
 // Waves per SIMD that the registers are cut to: what fits without spilling.
 template <typename T, int D> constexpr int kWavesPerSimd = sizeof(T) == 4 || D == 128 ? 2 : (D == 64 ? 3 : 4);
 
@@ -335,7 +340,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
                 for (int j = 0; j < D / 32; ++j) o[j] *= alpha;
                 m = mx;
             }
-            const float mc = m == -INFINITY ? 0.f : m * c;
+            const float mc = m == -INFINITY ? 0.f : m * c - kWeightLog2<T>;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float p[8];

@@ -126,3 +126,23 @@ def test_encode_a_key_of_minus_infinity_has_no_weight(dtype, lens, dim, scale):
     assert torch.equal(got[1:60], want[1:60])
     assert torch.isnan(got[60:lens[0]].float()).all()
     assert torch.equal(got[lens[0]:], want[lens[0]:])
+
+
+# --- weights and their sums ----------------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("up", [3, 7])
+def test_encode_large_values_behind_a_rising_maximum(dtype, up):
+    """Key 40's logit passes those before it by less than the running maximum follows at once; its value is 2^127.
+    The weighted mean is finite, and so is the result."""
+    n, dim = 64, 64
+    q, k, v = (torch.zeros((n, 1, dim), dtype=dtype) for _ in range(3))
+    q[:, :, 0] = 1
+    k[40, :, 0] = up
+    v[40] = 2.0 ** 127
+    got = encode(q, k, v, [n], scale=math.log(2))
+    out, mag, big = ho.attention(f64(q), f64(k), f64(v), [n], ALL, 0, math.log(2))
+    tol = bound(out, mag, big, dim, n, dtype, HALF[dtype], 0.0)
+    assert bool((np.abs(f64(got) - out) <= tol).all())
