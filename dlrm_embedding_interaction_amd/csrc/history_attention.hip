@@ -146,8 +146,10 @@ __device__ __forceinline__ float halves_sum(float v) {
 
 // Log2 of what a weight is multiplied by, and with it the row's sum.  Weights taken
 // against a maximum that lags by 2^8 then stay below 1: a mean of large values
-// passes the type's end on its way only where their sum does.
-template <typename T> constexpr float kWeightLog2 = __is_same(T, f16) ? 0.f : -8.f;
+// passes the type's end on its way only where their sum does.  fp16 values are far
+// from the accumulators' end, but its weights would be 0 below 2^-25: they go up to
+// 2^15, so that those below 2^-21 are off by 2^-32 at most.
+template <typename T> constexpr float kWeightLog2 = __is_same(T, f16) ? 7.f : -8.f;
 
 // Waves per SIMD that the registers are cut to: what fits without spilling.
 template <typename T, int D> constexpr int kWavesPerSimd = sizeof(T) == 4 || D == 128 ? 2 : (D == 64 ? 3 : 4);

@@ -146,3 +146,24 @@ def test_encode_large_values_behind_a_rising_maximum(dtype, up):
     out, mag, big = ho.attention(f64(q), f64(k), f64(v), [n], ALL, 0, math.log(2))
     tol = bound(out, mag, big, dim, n, dtype, HALF[dtype], 0.0)
     assert bool((np.abs(f64(got) - out) <= tol).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [700, 4000])
+@pytest.mark.parametrize("log2", [-25.2, -28.0])
+def test_encode_fp16_small_weights_count(n, log2):
+    """One key holds nearly all weight and a value of 0; the others, of 2^log2 each, make the result.  Weights are
+    rounded to fp16 against a maximum of at least 2^7: those below 2^-21 of the largest are off by 2^-32 at most."""
+    dim = 32
+    q, k, v = (torch.zeros((n, 1, dim), dtype=torch.float16) for _ in range(3))
+    q[:, :, 0] = 1
+    k[1:, :, 0] = log2
+    v[1:] = 1
+    got = encode(q, k, v, [n], scale=math.log(2))
+    out, mag, big = ho.attention(f64(q), f64(k), f64(v), [n], ALL, 0, math.log(2))
+    # outputs below 2^-14 are off by half a step of 2^-24
+    tol = bound(out, mag, big, dim, n, torch.float32, HALF[torch.float16], 0.0) + \
+        HALF[torch.float16] * np.abs(out) + n * 2.0 ** -32 + 2.0 ** -25
+    worst = (np.abs(f64(got) - out) / tol).max()
+    print(f"worst error / bar {worst:.3f}, last row {float(got[-1, 0, 0]):.3e} for {out[-1, 0, 0]:.3e}", flush=True)
+    assert worst <= 1
