@@ -147,6 +147,13 @@ __device__ __forceinline__ float wave_max(float v) {
     return v;
 }
 
+// c of exp(scale s) = 2^(c s), a negative scale having turned the query's sign.  Never
+// 0, which would make NaN of an unseen key's -inf: the smallest fp32 number leaves
+// every finite score's weight at 1.  Never infinite, which would make NaN of a 0.
+__device__ __forceinline__ float exponent_scale(float scale) {
+    return fminf(fmaxf(fabsf(scale) * 1.44269504088896341f, 0x1p-149f), 0x1.fffffep+127f);
+}
+
 // Eight consecutive elements of a row, as they are in memory.
 template <typename T>
 struct Raw {

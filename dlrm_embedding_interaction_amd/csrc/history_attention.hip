@@ -210,8 +210,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
             for (int i = 0; i < N; ++i) q[s][i] ^= a.scale < 0.f ? (short)0x8000 : (short)0;
         }
     }
-    // exp(scale s) = 2^(c s); a scale of 0 is a c that leaves every finite score's weight at 1
-    const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-37f);
+    const float c = exponent_scale(a.scale);
 
     Raw<T> kr[VEC], vr[VEC];
     uint8_t hide = 0;       // the padding byte of the wave's key `lane`, as loaded: a comparison here would wait for it

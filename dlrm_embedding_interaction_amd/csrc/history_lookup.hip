@@ -254,9 +254,7 @@ __global__ __launch_bounds__(DIRECT ? 64 * DIRECT : 256, 2) void history_lookup_
             t.ks = a.c.k_scale[hk_k];
             t.vs = a.c.v_scale[hk_v];
         };
-        // exp(scale s) = 2^(c s), a negative scale having turned the query's sign; a scale of 0 is a c that leaves
-        // every finite score's weight at 1
-        const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-37f);
+        const float c = exponent_scale(a.scale);
         auto use = [&](int i, Tile<D>& t) {
             floatx4 s[4];
 #pragma unroll

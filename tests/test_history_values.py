@@ -167,3 +167,32 @@ def test_encode_fp16_small_weights_count(n, log2):
     worst = (np.abs(f64(got) - out) / tol).max()
     print(f"worst error / bar {worst:.3f}, last row {float(got[-1, 0, 0]):.3e} for {out[-1, 0, 0]:.3e}", flush=True)
     assert worst <= 1
+
+
+# --- scales at the ends of their range -----------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-38, -1e-38, 1e-44, 3e38, -3e38])
+def test_scales_at_the_ends_of_their_range(dtype, scale):
+    """A scale of 0 weighs all events alike, however large their products; a tiny one is not rounded up; a large one
+    leaves products of 0 at 0."""
+    n, dim = 80, 64
+    big = 0.0 if abs(scale) > 1 else 2.0 ** 63
+    q, k = (torch.zeros((n, 1, dim), dtype=dtype) for _ in range(2))
+    q[:, :, 0] = big
+    k[:, :, 0] = big * randn((n, 1), 11, torch.float32).sign().to(dtype)
+    v = randn((n, 1, dim), 12, dtype)
+    got = encode(q, k, v, [n], scale=scale)
+    out, mag, b = ho.attention(f64(q), f64(k), f64(v), [n], ALL, 0, float(np.float32(scale)))
+    tol = bound(out, mag, b, dim, n, dtype, HALF[dtype], 0.0)
+    assert bool((np.abs(f64(got) - out) <= tol).all())
+    p = Pair(10, 1, 6, 1, dim, 16, dtype)
+    k2, v2 = k.clone(), randn((n, 1, dim), 13, dtype)
+    p.cpu.append([0], [n], f64(k2), f64(v2))
+    p.gpu.append(k2.cuda(), v2.cuda(), starts([n]).cuda())
+    got = p.gpu.lookup(q[:1].cuda(), scale=scale)
+    out, mag, b = p.cpu.lookup([0], f64(q[:1])[:, None], ALL, 0, float(np.float32(scale)))
+    tol = bound(out, mag, b, dim, n, dtype, 2.0 ** -15 if dtype != torch.float32 else U, 0.0)
+    assert bool((np.abs(f64(got)[:, None] - out) <= tol).all())
