@@ -176,6 +176,14 @@ __device__ __forceinline__ unsigned code4(T a, T b, T c, T d, float s) {
     return __builtin_bit_cast(unsigned, code2<true>(code2<false>(short2v{}, a, b, s), c, d, s));
 }
 
+// At the largest scale, 2^120, code 0x78 would stand for 2^128, past every finite
+// fp32 and bf16 value: values that would round to it get the code before, 0x77.
+constexpr float kLargestScale = 0x1p120f;
+__device__ __forceinline__ unsigned keep_finite(unsigned w) {
+    const unsigned differ = ((w & 0x7f7f7f7fu) ^ 0x78787878u) + 0x7f7f7f7fu;    // bit 7 of each byte: not 0x78
+    return w - (~differ >> 7 & 0x01010101u);
+}
+
 // Word k of 16-lane row q goes to word q of row k.
 __device__ __forceinline__ void exchange4(unsigned* w) {
 #pragma unroll
@@ -319,6 +327,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void history_append_ke
     const bool rewrite = lo > 0 && (g.copy || s > was);
     const float grown = rewrite ? s / was : 1.f;         // a power of two: exact
     const int from = rewrite ? 0 : lo;
+    const bool largest = !__is_same(T, f16) && __builtin_amdgcn_readfirstlane((int)(s == kLargestScale));
 
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
@@ -333,6 +342,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void history_append_ke
                     const T* f = raw[r][j].x;
                     w.x = code4(f[0], f[1], f[2], f[3], s);
                     w.y = code4(f[4], f[5], f[6], f[7], s);
+                    if (largest) w = make_uint2(keep_finite(w.x), keep_finite(w.y));
                 } else {
                     const uint2 o = *(const uint2*)(held + ev * D + ch * 8);
                     w = make_uint2(rescale4(o.x, grown), rescale4(o.y, grown));
@@ -344,6 +354,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void history_append_ke
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 w[i] = code4(raw[r][0].x[i], raw[r][1].x[i], raw[r][2].x[i], raw[r][3].x[i], s);
+            if (largest) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = keep_finite(w[i]);
+            }
             const int e0 = r * EV + 16 * ((lane & 15) / C8);             // the lane's 16 events after the exchange
             exchange4(w);
             exchange4(w + 4);

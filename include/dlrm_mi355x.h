@@ -490,7 +490,8 @@ dlrm_status_t dlrm_history_attention(const dlrm_attention_t* a, int64_t batch, i
  *               of its page and head, the smallest power of two >= 2^-100 under
  *               which the largest finite value of the block is at most 448.
  *               It only grows while a page fills; the codes the page holds are
- *               then rounded again.  Values that are not finite are held as NaN.
+ *               then rounded again.  Values that are not finite are held as NaN,
+ *               finite ones of 248 x 2^120 and more as 240 x 2^120.
  *   table       (n_slots, max_pages): page of each history's events
  *               [i * page_events, (i + 1) * page_events), -1 where there is none
  *   lens        (n_slots) events of each history, <= max_pages * page_events

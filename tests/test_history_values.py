@@ -196,3 +196,57 @@ def test_scales_at_the_ends_of_their_range(dtype, scale):
     out, mag, b = p.cpu.lookup([0], f64(q[:1])[:, None], ALL, 0, float(np.float32(scale)))
     tol = bound(out, mag, b, dim, n, dtype, 2.0 ** -15 if dtype != torch.float32 else U, 0.0)
     assert bool((np.abs(f64(got)[:, None] - out) <= tol).all())
+
+
+# --- the cache at the ends of fp32's range --------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dim", [32, 128])
+@pytest.mark.parametrize("count", [1, 5, 40])
+def test_cache_keeps_large_finite_values_finite(dtype, dim, count):
+    """From 248 x 2^120 on the nearest code at the largest scale, 256, would stand for 2^128: 240 is held."""
+    p = Pair(10, 1, 6, 1, dim, 16, dtype)
+    top = torch.finfo(dtype).max
+    q = torch.zeros((1, 1, dim), dtype=torch.float32)
+    seen = np.zeros((0, 1, dim))
+    for sign in (1.0, -1.0):
+        k, v = (randn((count, 1, dim), s, dtype) for s in (14, 15))
+        v[0, 0, 1], v[0, 0, 2], v[0, 0, 3] = sign * 3.29e38, sign * 3.3e38, sign * top
+        v[-1, 0, 4] = sign * 3.2e38
+        k[0, 0, 5] = sign * top
+        p.gpu.append(k.cuda(), v.cuda(), starts([count]).cuda())
+        held = f64(v)
+        # the block of the first event has scale 2^120: codes are multiples of 2^111 x 1, 2, 4 .. 16 there
+        unit = 2.0 ** 120
+        for e in (0, count - 1):
+            for d in (1, 2, 3, 4):
+                x = held[e, 0, d]
+                if abs(x) > 1e38:
+                    held[e, 0, d] = np.sign(x) * min(ho.e4m3(abs(x) / unit), 240.0) * unit
+        seen = np.concatenate([seen, held])
+    torch.cuda.synchronize()
+    assert torch.isfinite(p.gpu.k_scale[p.gpu.refs > 0]).all()
+    codes = p.gpu.v[p.gpu.refs > 0].cpu().view(torch.float8_e4m3fn).float()
+    scales = p.gpu.v_scale[p.gpu.refs > 0].cpu()
+    table = p.gpu.table[0].cpu()
+    for j, row in enumerate(seen):
+        page = int(table[j // 16])
+        c = p.gpu.v[page, 0, :, j % 16].cpu().view(torch.float8_e4m3fn).double().numpy()
+        s = float(p.gpu.v_scale[page, 0])
+        for d in (1, 2, 3, 4):
+            if abs(row[0, d]) > 1e38:
+                assert c[d] * s == row[0, d], (j, d)
+    assert codes.numel() and scales.numel()
+    # one event alone in the window: the lookup gives its values, all finite
+    one = Pair(4, 1, 2, 1, dim, 16, dtype)
+    k, v = torch.zeros((1, 1, dim), dtype=dtype), torch.full((1, 1, dim), -top, dtype=dtype)
+    one.gpu.append(k.cuda(), v.cuda(), starts([1]).cuda())
+    got = one.gpu.lookup(q.cuda())
+    assert bool((got == -240 * 2.0 ** 120).all())
+    # what is not finite is still held as NaN
+    v[0, 0, 0], v[0, 0, 1] = float("inf"), float("nan")
+    one.gpu.append(k.cuda(), v.cuda(), starts([1]).cuda())
+    got = one.gpu.lookup(q.cuda(), window=1).cpu()[0, 0]
+    assert torch.isnan(got[:2]).all() and bool((got[2:] == -240 * 2.0 ** 120).all())
