@@ -325,7 +325,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void history_append_ke
     float s = page_scale(top);
     s = was > s ? was : s;
     const bool rewrite = lo > 0 && (g.copy || s > was);
-    const float grown = rewrite ? s / was : 1.f;         // a power of two: exact
+    // a power of two: exact.  From 2^19 on every code becomes 0, and fp32 does not hold all quotients.
+    const float grown = rewrite ? fminf(s / was, 0x1p20f) : 1.f;
     const int from = rewrite ? 0 : lo;
     const bool largest = !__is_same(T, f16) && __builtin_amdgcn_readfirstlane((int)(s == kLargestScale));
 

@@ -250,3 +250,25 @@ def test_cache_keeps_large_finite_values_finite(dtype, dim, count):
     one.gpu.append(k.cuda(), v.cuda(), starts([1]).cuda())
     got = one.gpu.lookup(q.cuda(), window=1).cpu()[0, 0]
     assert torch.isnan(got[:2]).all() and bool((got[2:] == -240 * 2.0 ** 120).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("first", [0.0, 2.0 ** -99, -2.0 ** -92])
+def test_cache_scale_grows_by_more_than_fp32_holds(dtype, first):
+    """A block that held zeros or tiny values gets large ones: its scale grows from 2^-100 to 2^119, a quotient that
+    fp32 does not hold; what it held becomes zeros."""
+    p = Pair(20, 4, 4, 2, 64, 16, dtype)
+    p.append([0, 1, 2], [3, 15, 1], edit=lambda k, v: (k.fill_(first), v.fill_(first)))
+    p.same()
+    p.cpu.fork([0], [3])
+    p.gpu.fork(p.slots([0]), p.slots([3]))
+
+    def edit(k, v):
+        k.fill_(2.0 ** 127)
+        v[:, 0] = 2.0 ** 60
+        v[:, 1] = -2.0 ** 126
+    p.append([0, 1, 2, 3], [1, 3, 9, 2], edit=edit)
+    p.same()
+    held = p.gpu.table[0, 0]
+    assert torch.isfinite(p.gpu.k[held].cpu().view(torch.float8_e4m3fn).float()[:, :4]).all()
