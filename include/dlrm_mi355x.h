@@ -501,10 +501,11 @@ dlrm_status_t dlrm_history_attention(const dlrm_attention_t* a, int64_t batch, i
  *   counters    (4): pages in free_pages; histories refused so far (below); two
  *               reserved
  * k, v and refs are 16-byte aligned (DLRM_E_SHAPE otherwise).  In every call, slots
- * outside [0, n_slots) are refused: nothing happens for them and counters[1]
- * grows by one; table entries outside [0, n_pages) are events that nothing
- * sees.  No slot may appear twice in one call, nor as source and destination
- * of one fork.
+ * outside [0, n_slots) are refused: nothing happens for them (a lookup gives
+ * zeros) and counters[1] grows by one; table entries outside [0, n_pages) are
+ * events that nothing sees.  No slot may appear twice in one call, nor as
+ * source and destination of one fork; a lookup, which changes no history, may
+ * name a slot more than once.
  *
  * dlrm_history_workspace_bytes -- workspace of the calls below for up to
  *   `batch` histories and, for dlrm_history_lookup, `queries` per history of

@@ -272,3 +272,22 @@ def test_cache_scale_grows_by_more_than_fp32_holds(dtype, first):
     p.same()
     held = p.gpu.table[0, 0]
     assert torch.isfinite(p.gpu.k[held].cpu().view(torch.float8_e4m3fn).float()[:, :4]).all()
+
+
+# --- refusals ------------------------------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("events", [40, 65 * 64])
+def test_lookup_counts_the_slots_it_refuses(events):
+    """In one launch and in two: bad slots give zeros, and each is counted once."""
+    p = Pair(70, 3, 66, 2, 64, 64, torch.bfloat16)
+    p.append([0, 1], [events, 5])
+    q = randn((5, 40, 4, 64), 16, torch.bfloat16).cuda()
+    got = p.gpu.lookup(q, slots=p.slots([-1, 0, 3, 1 << 30, 1]))
+    assert p.gpu.n_refused == 3
+    assert bool((got[[0, 2, 3]] == 0).all()) and bool((got[[1, 4]] != 0).any())
+    p.gpu.lookup(q, window=9, slots=p.slots([2, 0, 1, 0, -5]))
+    assert p.gpu.n_refused == 4
+    p.gpu.lookup(q[:3])
+    assert p.gpu.n_refused == 4
