@@ -198,24 +198,29 @@ class HistoryCache:
                             refs.data_ptr(), free_pages.data_ptr(), counters.data_ptr())
         self._ref = ctypes.byref(self._desc)
         self._ws = {}           # stream -> workspace: calls on two streams may overlap
-        self._kept = []
         self._need = {}
 
-    def _workspace(self, stream: int, batch: int, queries: int = 0, heads: int = 0) -> torch.Tensor:
+    def _workspace(self, stream: int, batch: int, queries: int = 0, heads: int = 0):
+        """(address, bytes, the tensor that holds them) for one call on the stream."""
         key = (batch, queries, heads)
         need = self._need.get(key)
         if need is None:
-            need = int(load().dlrm_history_workspace_bytes(self._ref, batch, queries, heads))
+            need = max(256, int(load().dlrm_history_workspace_bytes(self._ref, batch, queries, heads)))
             if len(self._need) > 256:
                 self._need.clear()
             self._need[key] = need
+        if torch.cuda.is_current_stream_capturing():
+            # The graph's own, from its pool: replays may run on any stream, beside calls and other graphs.  The pool
+            # keeps the memory for the graph once the tensor is gone.
+            return self._new_workspace(need)
         ws = self._ws.get(stream)
-        if ws is None or ws.numel() < need:
-            grown = 256 if ws is None else 2 * ws.numel()       # doubled: what is kept below stays under one more
-            if ws is not None:
-                self._kept.append(ws)                           # a captured graph may still write to it
-            ws = self._ws[stream] = torch.empty(max(need, grown), dtype=torch.uint8, device=self.device)
+        if ws is None or ws[1] < need:
+            ws = self._ws[stream] = self._new_workspace(need)
         return ws
+
+    def _new_workspace(self, size: int):
+        t = torch.empty(size, dtype=torch.uint8, device=self.device)
+        return t.data_ptr(), size, t
 
     def _slots(self, slots: Optional[torch.Tensor], batch: int):
         if slots is None:
@@ -242,7 +247,7 @@ class HistoryCache:
         ws = self._workspace(s, batch)
         rc = load().dlrm_history_append(self._ref, batch, self._slots(slots, batch), DTYPES[k.dtype], k.shape[0],
                                         offsets.data_ptr(), ib, k.data_ptr(), ld_k, v.data_ptr(), ld_v,
-                                        ws.data_ptr(), ws.numel(), s)
+                                        ws[0], ws[1], s)
         _check(rc, "dlrm_history_append")
 
     def lookup(self, q: torch.Tensor, window: int = ALL_EVENTS, sinks: int = 0, scale: Optional[float] = None,
@@ -267,7 +272,7 @@ class HistoryCache:
         s = _stream(self.device)
         ws = self._workspace(s, batch, queries, heads)
         rc = load().dlrm_history_lookup(self._ref, a, batch, self._slots(slots, batch), queries,
-                                        q.data_ptr(), ld_q, out.data_ptr(), ld_out, ws.data_ptr(), ws.numel(), s)
+                                        q.data_ptr(), ld_q, out.data_ptr(), ld_out, ws[0], ws[1], s)
         _check(rc, "dlrm_history_lookup")
         return out
 
@@ -279,8 +284,8 @@ class HistoryCache:
             raise ValueError("one destination for each source")
         s = _stream(self.device)
         ws = self._workspace(s, 1)
-        _check(load().dlrm_history_fork(self._ref, src.shape[0], src.data_ptr(), dst.data_ptr(), ws.data_ptr(),
-                                        ws.numel(), s), "dlrm_history_fork")
+        _check(load().dlrm_history_fork(self._ref, src.shape[0], src.data_ptr(), dst.data_ptr(), ws[0], ws[1],
+                                        s), "dlrm_history_fork")
 
     def truncate(self, slots: torch.Tensor, new_lens: Optional[torch.Tensor] = None) -> None:
         """Cut histories to their first new_lens[i] events (none: free them)."""
@@ -292,8 +297,8 @@ class HistoryCache:
         s = _stream(self.device)
         ws = self._workspace(s, 1)
         _check(load().dlrm_history_truncate(self._ref, slots.shape[0], slots.data_ptr(),
-                                            new_lens.data_ptr() if new_lens is not None else None, ws.data_ptr(),
-                                            ws.numel(), s), "dlrm_history_truncate")
+                                            new_lens.data_ptr() if new_lens is not None else None, ws[0],
+                                            ws[1], s), "dlrm_history_truncate")
 
     def free(self, slots: torch.Tensor) -> None:
         """Empty histories; their pages go back to the pool."""
@@ -305,13 +310,13 @@ class HistoryCache:
         s = _stream(self.device)
         ws = self._workspace(s, 1)
         _check(load().dlrm_history_trim(self._ref, slots.shape[0], slots.data_ptr(), int(window), int(sinks),
-                                        ws.data_ptr(), ws.numel(), s), "dlrm_history_trim")
+                                        ws[0], ws[1], s), "dlrm_history_trim")
 
     def compact(self) -> None:
         """Move the used pages to the front of the pool."""
         s = _stream(self.device)
         ws = self._workspace(s, 1)
-        _check(load().dlrm_history_compact(self._ref, ws.data_ptr(), ws.numel(), s), "dlrm_history_compact")
+        _check(load().dlrm_history_compact(self._ref, ws[0], ws[1], s), "dlrm_history_compact")
 
     @property
     def n_free(self) -> int:

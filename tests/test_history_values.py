@@ -291,3 +291,46 @@ def test_lookup_counts_the_slots_it_refuses(events):
     assert p.gpu.n_refused == 4
     p.gpu.lookup(q[:3])
     assert p.gpu.n_refused == 4
+
+
+# --- workspaces of captured calls ------------------------------------------------------
+
+
+@pytest.mark.gpu
+def test_captured_lookups_share_no_workspace():
+    """Two lookups, each cut into many runs that meet in a workspace, captured on one stream and replayed side by side on
+    two, beside eager ones on the stream of the capture."""
+    n = 65 * 64
+    c = dl.HistoryCache(8 * 65, 8, 65, 2, 64, 64)
+    k, v = (randn((8 * n, 2, 64), s, torch.bfloat16).cuda() for s in (20, 21))
+    c.append(k, v, torch.arange(8, dtype=torch.int64, device="cuda") * n)
+    slots = [torch.arange(a, a + 4, dtype=torch.int32, device="cuda") for a in (0, 4)]
+    qs = [randn((4, 8, 64), s, torch.bfloat16).cuda() for s in (22, 23)]
+    want = [c.lookup(q, slots=s) for q, s in zip(qs, slots)]
+    outs = [torch.empty_like(q) for q in qs]
+    side = torch.cuda.Stream()
+    graphs = []
+    held = {s: w[0] for s, w in c._ws.items()}
+    torch.cuda.synchronize()
+    for q, s, out in zip(qs, slots, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            for _ in range(10):
+                c.lookup(q, slots=s, out=out)
+        graphs.append(g)
+    # a capture neither takes a stream's workspace nor leaves one behind
+    assert {s: w[0] for s, w in c._ws.items()} == held
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for out in outs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(side):
+            eager = [c.lookup(qs[1], slots=slots[1]) for _ in range(10)]
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert torch.equal(out, w)
+        assert all(torch.equal(e, want[1]) for e in eager)
