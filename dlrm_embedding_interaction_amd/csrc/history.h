@@ -67,6 +67,11 @@ struct AppendArgs {
     int batch, idx32, per_event;        // per_event: one unit of work per event (see the kernel), not per page
 };
 
+// HIP counts the threads along a dimension of a grid in 32 bits.  Launch functions
+// return kTooLarge, having enqueued nothing, where a call would need more.
+constexpr hipError_t kTooLarge = hipErrorInvalidConfiguration;
+inline bool grid_fits(int64_t blocks, int threads) { return (uint64_t)blocks * threads <= 0xffffffffull; }
+
 hipError_t launch_history_attention(const EncodeArgs& a, int dtype, int dim, hipStream_t s);
 hipError_t launch_history_lookup(const LookupArgs& a, int dtype, hipStream_t s);
 size_t lookup_workspace_bytes(const dlrm_history_cache_t& c, int64_t batch, int queries, int n_heads);

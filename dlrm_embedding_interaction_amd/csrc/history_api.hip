@@ -12,7 +12,9 @@ using namespace dlrm;
 namespace {
 
 constexpr int64_t kIntLimit = (int64_t)1 << 30;
-inline dlrm_status_t from_hip(hipError_t e) { return e == hipSuccess ? DLRM_OK : DLRM_E_HIP; }
+inline dlrm_status_t from_hip(hipError_t e) {
+    return e == hipSuccess ? DLRM_OK : (e == kTooLarge ? DLRM_E_UNSUPPORTED : DLRM_E_HIP);
+}
 inline size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 bool known_dtype(int32_t t) { return t == DLRM_DTYPE_F32 || t == DLRM_DTYPE_BF16 || t == DLRM_DTYPE_F16; }

@@ -461,7 +461,9 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
 template <typename T, int D, int W, int KS = 1>
 static hipError_t launch_w(const EncodeArgs& a, bool wide, int heads_log2, hipStream_t s) {
     constexpr int BN = (sizeof(T) == 4 && D == 128 ? 32 : 64) * KS;
-    const dim3 grid((unsigned)(a.n_events / (32 * (W / KS) >> heads_log2) + a.batch), (unsigned)(a.n_heads >> heads_log2));
+    const int64_t tiles = a.n_events / (32 * (W / KS) >> heads_log2) + a.batch;
+    if (!grid_fits(tiles, 64 * W)) return kTooLarge;
+    const dim3 grid((unsigned)tiles, (unsigned)(a.n_heads >> heads_log2));
     const dim3 block(64 * W);
     if (!wide) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, false, true, KS>), grid, block, 0, s, a, heads_log2);
     else if (a.padding) hipLaunchKernelGGL((history_attention_kernel<T, D, W, BN, true, true, KS>), grid, block, 0, s, a, heads_log2);

@@ -551,6 +551,7 @@ static hipError_t launch_t(LookupArgs a, hipStream_t s) {
     a.partial = (float*)((char*)a.partial + meta_bytes(a.batch));
     const int w = direct_waves((int64_t)a.batch * hc, D == 32 || (D == 64 && Parts<T>::q == 1) ? 12 : 8);
     if (most_tiles(a) <= (w == 8 ? kDirectTiles8 : kDirectTiles)) {
+        if (!grid_fits(a.batch, 64 * w)) return kTooLarge;
         const dim3 grid(a.batch, hc);
         if (w == 8) hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 8>), grid, dim3(512), 0, s, a, 0, meta);
         else if (w == 4) hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 4>), grid, dim3(256), 0, s, a, 0, meta);
@@ -558,6 +559,7 @@ static hipError_t launch_t(LookupArgs a, hipStream_t s) {
         else hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 1>), grid, dim3(64), 0, s, a, 0, meta);
         return hipGetLastError();
     }
+    if (!grid_fits(a.batch, 256)) return kTooLarge;
     const int waves = waves_of(a.c, a.batch, a.queries, a.n_heads);
     hipLaunchKernelGGL((history_lookup_kernel<D, PE, T, 0>), dim3(waves / 4, hc), dim3(256), 0, s, a, waves, meta);
     // A few long histories are cut into many runs each: their elements are then spread over blocks, too.  64 histories

@@ -571,6 +571,7 @@ static hipError_t release(const ReleaseArgs& a, int32_t* counts, hipStream_t s) 
         hipLaunchKernelGGL(history_release_one_kernel<OP>, dim3(1), dim3(1024), 0, s, a);
         return hipGetLastError();
     }
+    if (!grid_fits(a.n, 256)) return kTooLarge;
     hipLaunchKernelGGL(history_release_kernel<OP>, dim3(a.n), dim3(256), 0, s, a);
     if (a.c.n_pages <= kOneBlockPages) {
         hipLaunchKernelGGL(history_rebuild_one_kernel, dim3(1), dim3(1024), 0, s, a.c);
@@ -736,12 +737,14 @@ static void launch_append(const AppendArgs& a, dim3 grid, hipStream_t s) {
 
 hipError_t launch_history_append(const AppendArgs& args, int dtype, hipStream_t s) {
     AppendArgs a = args;
+    const int64_t by_page = a.n_events / a.c.page_events + 2 * (int64_t)a.batch;
+    a.per_event = a.n_events <= by_page;
+    const int64_t units = a.per_event ? a.n_events : by_page;
+    if (!grid_fits(units + 1, 256)) return kTooLarge;
     hipLaunchKernelGGL(history_need_kernel, dim3((a.batch + kNeedBlock - 1) / kNeedBlock), dim3(kNeedBlock), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t by_page = a.n_events / a.c.page_events + 2 * (int64_t)a.batch;
-    a.per_event = a.n_events <= by_page;
-    const dim3 grid((unsigned)((a.per_event ? a.n_events : by_page) + 1), (unsigned)((2 * a.c.n_kv_heads + 3) / 4));
+    const dim3 grid((unsigned)(units + 1), (unsigned)((2 * a.c.n_kv_heads + 3) / 4));
     if (dtype == DLRM_DTYPE_F32) launch_append<float>(a, grid, s);
     else if (dtype == DLRM_DTYPE_BF16) launch_append<bf16>(a, grid, s);
     else launch_append<f16>(a, grid, s);

@@ -472,7 +472,9 @@ typedef struct dlrm_attention {
  *              see do not reach it.
  * out must not overlap q, k or v.  Rows of 16-byte aligned tensors whose ld is
  * a multiple of 16 bytes are read 16 bytes at a time, others by element.  ld_k
- * and ld_v above 2^30 give DLRM_E_UNSUPPORTED.
+ * and ld_v above 2^30 give DLRM_E_UNSUPPORTED; so do, here and in the calls on
+ * the cache below, sizes whose launch would pass 2^32 threads along batch and
+ * events (from 2^24 histories or some 2^28 events on, depending on the call).
  */
 dlrm_status_t dlrm_history_attention(const dlrm_attention_t* a, int64_t batch, int64_t n_events,
                                      const void* offsets, int32_t index_bytes, const void* q, int64_t ld_q,
