@@ -94,7 +94,8 @@ __global__ __launch_bounds__(kNeedBlock) void history_need_kernel(AppendArgs a) 
     block_exclusive<kNeedBlock>(b < a.batch && !ok ? 1 : 0, &refused);
     if (threadIdx.x == 0) {
         a.ws.sums[blockIdx.x] = make_int2(pages, refused);
-        if (blockIdx.x == 0) *a.ws.n_free = c.counters[0];
+        // the list has n_pages places, whatever the counter holds
+        if (blockIdx.x == 0) *a.ws.n_free = min(max(c.counters[0], 0), c.n_pages);
     }
 }
 

@@ -293,6 +293,23 @@ def test_lookup_counts_the_slots_it_refuses(events):
     assert p.gpu.n_refused == 4
 
 
+# --- counters that no call wrote ---------------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("count,left", [(1 << 30, 4), (7, 4), (-5, 0)])
+def test_append_reads_no_place_past_the_free_list(count, left):
+    """A count of free pages that passes the pool's size, or is below zero, is cut to what the list can hold."""
+    c = dl.HistoryCache(6, 2, 6, 1, 32, 16)
+    c.counters[0] = count
+    k = randn((20, 1, 32), 24, torch.bfloat16).cuda()
+    c.append(k, k, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    torch.cuda.synchronize()
+    assert c.n_free == left
+    assert c.table[0].tolist() == ([0, 1] + [-1] * 4 if left else [-1] * 6)
+    assert c.n_refused == (0 if left else 1)
+
+
 # --- workspaces of captured calls ------------------------------------------------------
 
 
