@@ -113,8 +113,9 @@ def history_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets
     """Every event of ragged histories attends to its own history -> (N, n_heads, head_dim).
 
     ``q`` (N, n_heads, head_dim), ``k`` and ``v`` (N, n_kv_heads, head_dim), all fp32, bf16 or fp16; rows may be
-    columns of a wider tensor.  History b is rows [offsets[b], offsets[b + 1]).  An event sees the last ``window``
-    events of its history, itself included, and the first ``sinks``, but none whose ``padding`` byte is set."""
+    columns of a wider tensor.  History b is rows [offsets[b], offsets[b + 1]); rows before offsets[0], usually 0, are
+    no one's and are not written.  An event sees the last ``window`` events of its history, itself included, and the
+    first ``sinks``, but none whose ``padding`` byte is set."""
     if not isinstance(q, torch.Tensor) or q.dtype not in DTYPES:
         raise TypeError("q must be an fp32, bf16 or fp16 tensor")
     dev, dtype = q.device, q.dtype
@@ -150,7 +151,8 @@ class HistoryCache:
     """Keys and values of many histories in 8 bits, on pages of a common pool.
 
     ``n_slots`` histories of up to ``max_pages`` pages of ``page_events`` events.  Slots are int32 CUDA tensors.
-    Calls run on the current stream and never wait for the GPU; ``n_free`` and ``n_refused`` read it back."""
+    Calls run on the current stream and never wait for the GPU; ``n_free`` and ``n_refused`` read it back.  Lookups
+    change nothing but the count of refused slots and may run on several streams, and in several graphs, at once."""
 
     def __init__(self, n_pages: int, n_slots: int, max_pages: int, n_kv_heads: int, head_dim: int,
                  page_events: int = 64, device="cuda"):
@@ -235,7 +237,8 @@ class HistoryCache:
     def append(self, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
                slots: Optional[torch.Tensor] = None) -> None:
         """Events behind histories: rows [offsets[b], offsets[b + 1]) of ``k`` and ``v`` (N, n_kv_heads, head_dim)
-        go behind history slots[b] (b without slots)."""
+        go behind history slots[b] (b without slots).  Histories without room are refused whole (``n_refused``); pages
+        are promised in batch order, so that one refused for want of them leaves none for those behind it."""
         if not isinstance(k, torch.Tensor) or k.dtype not in DTYPES:
             raise TypeError("k must be an fp32, bf16 or fp16 tensor")
         ld_k, ld_v = (_rows(t, n, k.dtype, 3, self.device) for t, n in ((k, "k"), (v, "v")))
@@ -320,7 +323,7 @@ class HistoryCache:
 
     @property
     def n_free(self) -> int:
-        """Pages without a holder (waits for the GPU)."""
+        """Pages that appends can take (waits for the GPU)."""
         return int(self.counters[0].item())
 
     @property

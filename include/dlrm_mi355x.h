@@ -439,13 +439,19 @@ dlrm_status_t dlrm_pair_index_map(int32_t n_feat, int32_t* i_out, int32_t* j_out
  * included, and the first `sinks`.  A row that sees nothing gives zeros, as an
  * empty bag does.
  *   dtype       of q, k, v and out; products, softmax statistics and sums are
- *               held in fp32 (fp32 inputs lose nothing to the matrix cores:
- *               they are multiplied as sums of bf16 parts)
+ *               held in fp32.  fp32 factors are multiplied as sums of three bf16
+ *               parts, which hold all their bits down to 2^-134.  Where they meet
+ *               the values, the weights of bf16 and fp16 calls are rounded:
+ *               once to that type by dlrm_history_attention, to two bf16 parts
+ *               (2^-16) by dlrm_history_lookup; the sum that divides the result
+ *               is taken of the weights as they were.  Values are weighed
+ *               before the division: a row whose weighted values add up to more
+ *               than fp32 holds, at a largest weight of 1, is infinite there
  *   n_heads     a multiple of n_kv_heads, at most 4096
  *   head_dim    32, 64 or 128, else DLRM_E_UNSUPPORTED
  *   window      >= 1 (a value no history reaches: all earlier events)
  *   sinks       >= 0
- *   scale       of the products, usually head_dim^-1/2; finite
+ *   scale       of the products, usually head_dim^-1/2; of magnitude <= 3e38
  */
 typedef struct dlrm_attention {
     int32_t dtype;
@@ -462,14 +468,16 @@ typedef struct dlrm_attention {
  * dlrm_history_attention -- every event of `batch` ragged histories attends to
  * its own history.  History b is the rows [offsets[b], offsets[b+1]) of q, k,
  * v and out, the last one ending at n_events (the bags' convention; histories
- * may be empty).
+ * may be empty).  Rows before offsets[0], which is usually 0, belong to no
+ * history: out is left as it was there.
  *   n_events   total rows, >= 0 (0: nothing is enqueued)
  *   offsets    device (batch) integers of index_bytes
  *   q, out     device (n_events, ld_q / ld_out), n_heads * head_dim columns used
  *   k, v       device (n_events, ld_k / ld_v), n_kv_heads * head_dim columns used
  *   padding    device (n_events) bytes or NULL; events with a nonzero byte are
- *              seen by no one.  Infinities and NaN in events a row does not
- *              see do not reach it.
+ *              seen by no one.  What stands in events that a row does not see,
+ *              infinities and NaN included, changes none of its bits, and
+ *              neither do other rows' queries.
  * out must not overlap q, k or v.  Rows of 16-byte aligned tensors whose ld is
  * a multiple of 16 bytes are read 16 bytes at a time, others by element.  ld_k
  * and ld_v above 2^30 give DLRM_E_UNSUPPORTED; so do, here and in the calls on
@@ -499,7 +507,10 @@ dlrm_status_t dlrm_history_attention(const dlrm_attention_t* a, int64_t batch, i
  *   lens        (n_slots) events of each history, <= max_pages * page_events
  *   refs        (n_pages) histories that hold the page
  *   free_pages  (n_pages): its first counters[0] entries are the pages without a
- *               holder, in descending order; the last one is taken first
+ *               holder, in descending order; the last one is taken first.  Pages
+ *               that an append leaves without one, because all their holders
+ *               copied them in that call, are entered by the next call of fork,
+ *               truncate, trim or compact
  *   counters    (4): pages in free_pages; histories refused so far (below); two
  *               reserved
  * k, v and refs are 16-byte aligned (DLRM_E_SHAPE otherwise).  In every call, slots
@@ -544,9 +555,12 @@ dlrm_status_t dlrm_history_init(const dlrm_history_cache_t* c, void* stream);
  * itself when slots is NULL) grows by the rows [offsets[b], offsets[b+1]) of k
  * and v, the last one ending at n_events; a history may get none, one or many.
  * Pages are taken as needed; a part-filled last page that other histories hold
- * too is copied first.  Pages are granted in batch order; a history that would
- * pass the last free page or max_pages, or whose part-filled last page is not
- * there, is refused whole: it stays as it was and counters[1] grows by one.
+ * too is copied first.  A history that would pass max_pages, or whose
+ * part-filled last page is not there, is refused whole: it stays as it was and
+ * counters[1] grows by one.  So is one for which the listed pages do not
+ * suffice: they are promised in batch order by the running sum of what the
+ * histories before it need, those refused for want of pages included, so that
+ * behind such a one only histories that need no page are served.
  *   dtype   of k and v; ld_k, ld_v as in dlrm_history_attention
  */
 dlrm_status_t dlrm_history_append(const dlrm_history_cache_t* c, int64_t batch, const int32_t* slots,
