@@ -21,15 +21,17 @@
 // fp32 tensors are multiplied as three bf16 parts each (rounded, so that the
 // parts hold all 24 bits), in the six products of parts that are not below
 // 2^-24 of the whole: 6/16 of the fp32 matrix instructions' time.  16-bit
-// tensors round the weights to their own type once, an error of the size of the
-// output's own rounding; maxima, sums and outputs are held in fp32.
+// tensors round the weights to their own type once: against the 64-bit form
+// 0.0020 of the output's size in bf16, where rounding the output alone gives
+// 0.0016, 0.00026 against 0.00020 in fp16; maxima, sums and outputs are held in
+// fp32.
 //
 // Measured on MI355X, bf16: 2 histories of up to 12001 events, 8 heads on 2 kv heads
-// of 128, window 4096: 291 us, 800 TFLOP/s of visible pairs, 66% of a large library
+// of 128, window 4096: 287 us, 810 TFLOP/s of visible pairs, 67% of a large library
 // product (1204).  Per 32 rows x 32 keys a wave issues 16 products (512 cycles) and
 // ~110 vector instructions (~600 cycles with the exponentials); the counters show
 // 39% and 40% of the cycles busy with either, the rest waiting for LDS and at
-// barriers.  256 histories of up to 512, 4 heads of 64, window 128: 44 us against 29
+// barriers.  256 histories of up to 512, 4 heads of 64, window 128: 43 us against 29
 // for its bytes, the masked edges of the window being most of the work.  Tried and
 // not kept: two LDS buffers with one barrier a tile (309 against 293 us), 64 keys at
 // a time (304), reads ordered ahead of the products, raised wave priorities.
@@ -151,7 +153,8 @@ __device__ __forceinline__ float halves_sum(float v) {
 // 2^15, so that those below 2^-21 are off by 2^-32 at most.
 template <typename T> constexpr float kWeightLog2 = __is_same(T, f16) ? 7.f : -8.f;
 
-// Waves per SIMD that the registers are cut to: what fits without spilling.
+// Waves per SIMD that the registers are cut to.  All fits but at heads of 128, where 13 of the 99 kernels keep 36 to 156
+// bytes a lane in scratch: fp32 in blocks of rows of their own, 16-bit with padding in two waves or with shared keys.
 template <typename T, int D> constexpr int kWavesPerSimd = sizeof(T) == 4 || D == 128 ? 2 : (D == 64 ? 3 : 4);
 
 // WIDE: 16-byte loads and stores.  PAD: padding bytes may be given.  KS: waves that
@@ -480,7 +483,10 @@ static hipError_t launch_d(const EncodeArgs& a, bool wide, hipStream_t s) {
     // heads, bf16 51 to 52, up to 160 66 to 65; 4 heads of 64 on two, fp32, up to 40 41 to 39.
     const int heads = group % 4 == 0 ? 2 : (group % 2 == 0 ? 1 : 0);
     const bool one = heads ? sizeof(T) == 2 && mean <= 72 : D == 32 && mean <= 24;
-    // 64 rows against 128, 2048 of up to 128, 4 heads of 64, bf16: 61 us to 62, of up to 192 106 to 110.
+    // 64 rows against 128: 2048 of up to 128, 4 heads of 64, bf16 60 us to 64, of up to 192 108 to 111; of 48 37 to 49.
+    // Histories that fill their 64 or 96 rows go the other way, and so do small heads: 2048 of 64 65 to 56, of 96 97 to
+    // 93; 1024 of 64, 4 heads of 32, fp16 28 to 22, of up to 128 28 to 26; 512 of 64, 2 heads of 64, fp32 39 to 25.  The
+    // mean does not tell the two apart.
     const int rows = one ? 1 : (mean <= 96 ? 2 : 4);
     // Blocks of 8 waves read each tile once for twice the rows, blocks of 4 leave two to a CU, one's loads and stores
     // beside the other's products.  Lifelong (66 tiles a block) 8 waves 294 us, 4 waves 312; grouped (10 tiles) 308

@@ -27,8 +27,8 @@
 // rounding them to one would add an error as large as the output's own rounding.
 //
 // Measured on MI355X: 128 histories of up to 32000 events, 8 kv heads of 128, 32
-// query heads, bf16: 817 us, 5.8 TB/s of codes, 92% of what a plain read stream
-// reaches (6.28 TB/s).  256 histories, window 1024, 4 kv heads of 64: 31 us, 4.0
+// query heads, bf16: 812 us, 5.8 TB/s of codes, 93% of what a plain read stream
+// reaches (6.28 TB/s).  256 histories, window 1024, 4 kv heads of 64: 32 us, 4.0
 // TB/s; there the dependent reads length -> page -> codes and the ~300 vector
 // instructions a tile (decoding, exponentials, splitting) show.
 #include "history.h"
@@ -38,9 +38,11 @@ namespace dlrm {
 constexpr int kTile = 64;                // events per tile
 constexpr int kLookupWaves = 2048;       // waves a launch aims at: two on each SIMD
 // Histories of at most this many tiles have a block of their own: no second kernel, but the longest history sets the
-// time.  Measured, blocks against runs: 96 histories of up to 24 tiles 18.7 us to 30.8; 256 (4 kv heads of 64) of up to
-// 24 27.2 to 30.0, of up to 40 40.5 to 37.4.  Where eight waves share a block the longest costs less: 64 of up to 40
-// tiles 15.4 to 24.4, eight of up to 40 11.4 to 11.9, of up to 64 15.6 to 13.8.
+// time.  The table's room counts, which the host knows, not what is held.  Measured on ragged histories, blocks against
+// runs: 96 of up to 24 tiles (4 heads of 64) 16.1 us to 18.8, of up to 32 19.6 to 21.4, of up to 48 26.1 to 25.5; 256 (16
+// heads on 4) of up to 24 28.5 to 31.0, of up to 40 42.9 to 43.0, of up to 64 81 to 73.  Where eight waves share a block
+// the longest costs less: 64 of up to 40 tiles 15.9 to 20.8, eight of up to 48 12.4 to 13.1, of up to 64 15.2 to 14.3;
+// 64 of up to 64 would still be faster in blocks, 21.3 to 24.6, and of up to 96, 28.6 to 31.3.
 constexpr int kDirectTiles = 32, kDirectTiles8 = 48;
 
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -130,6 +132,7 @@ struct Tile {
     bool kin, vin;                                      // the pages are there
 };
 
+// Two waves per SIMD: all fits but in the runs of fp32 heads of 128, which keep 12 to 20 bytes a lane in scratch.
 // DIRECT waves: one block of so many per (history, chunk of rows), its waves taking
 // every DIRECT-th tile and joining their results through LDS.  0: runs of tiles.
 template <int D, int PE, typename T, int DIRECT>

@@ -9,7 +9,7 @@
 // order in which the atomics of a call arrived.
 //
 // Measured on MI355X: appending 128 histories of up to 1000 events, 8 kv heads of
-// 128, bf16 (466 MB): 100 us, 4.7 TB/s, against 5.0 for a large copy.  One event for
+// 128, bf16 (466 MB): 101 us, 4.6 TB/s, against 5.0 for a large copy.  One event for
 // each of 512 histories: 8 us, of 1500 with a copied page each 42: there a wave's
 // five dependent reads (offsets, need, list, scale, codes) are what it takes.  The
 // list of 32000 pages 7 us, of 11000 5.
