@@ -119,3 +119,14 @@ def test_trimmed_histories_in_a_pool_of_many_blocks():
         assert [[p for p in row if p >= 0] for row in c.table.tolist()] == \
             [[p for p in row if p is not None] for row in o.lists]
     assert np.sum([len(r) for r in o.lists]) > 0
+
+
+def test_append_refused_for_want_of_pages_takes_none():
+    """One history is refused for want of pages, the next needs none and is served: the list stays as it was."""
+    c = dl.HistoryCache(4, 3, 8, 1, 32, 16)
+    k = randn((82, 1, 32), 10, torch.bfloat16).cuda()
+    c.append(k[:1], k[:1], torch.zeros(1, dtype=torch.int64, device="cuda"))
+    c.append(k[1:], k[1:], starts([66, 15]).cuda(), slots=torch.tensor([1, 0], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert c.lens.tolist() == [16, 0, 0] and c.refs.tolist() == [1, 0, 0, 0]
+    assert c.n_refused == 1 and c.n_free == 3 and c.free_pages[:3].tolist() == [3, 2, 1]
