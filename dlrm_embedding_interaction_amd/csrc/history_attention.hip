@@ -121,14 +121,6 @@ __device__ __forceinline__ bool finite_bits(T x) {
     return true;
 }
 
-// The three parts of one fp32 value, `apart` elements from one another.
-__device__ __forceinline__ void split_large(float x, bf16* part, int apart) {
-    part[0] = (bf16)first_part(x);
-    x -= (float)part[0];
-    part[apart] = (bf16)x;
-    part[2 * apart] = (bf16)(x - (float)part[apart]);
-}
-
 // Four keys of 16 columns, turned: lane j of a group of 16 points at key
 // j / 4, columns 4 (j % 4) .. + 3, and receives column j of the four keys.
 __device__ __forceinline__ shortx4 read_turned(const void* p) {
@@ -257,33 +249,32 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
                 *(shortx8*)&vs[i][key][d] = vp[i];
             }
         }
-        if (N == 1 ? odd_magnitude<T>(big) : rest != 0.f) odd[t & 1] = 1;       // NaN differs from 0
-        __syncthreads();
-        if (t + 1 < tiles) fetch(t + 1);
-        const bool fix = odd[t & 1] != 0;
-        if (fix) {
-            // such values are taken out of the products and added to the rows that see them, fp32 keys' to the scores;
-            // finite fp32 keys and values whose first part is not finite are split anew
-            int p = tid;
-            asm volatile("" : "+v"(p));     // what follows from it is worked out here, not kept in registers beside the tiles
-            for (; p < BN * D; p += THREADS) {
-                const int key = p / D, d = p % D;
-                if constexpr (N > 1) {
-                    const int64_t at = min(k0 + key, len - 1);
-                    if (!finite_bits(ks[0][key][d])) {
-                        const float x = kg[at * a.ld_k + d];
-                        split_large(finite_bits(x) ? x : 0.f, &ks[0][key][d], BN * KP);
-                    }
-                    if (!finite_bits(vs[0][key][d])) {
-                        const float x = vg[at * a.ld_v + d];
-                        split_large(finite_bits(x) ? x : 0.f, &vs[0][key][d], BN * VP);
-                    }
-                } else if (!finite_bits(vs[0][key][d])) {
-                    vs[0][key][d] = (E)0.f;
+        if (__builtin_expect(N == 1 ? odd_magnitude<T>(big) : rest != 0.f, 0)) {       // NaN differs from 0
+            // infinities and NaN are taken out of the products and added to the rows that see them, fp32 keys' to the
+            // scores; finite fp32 keys and values whose first part is not finite are split anew
+            odd[t & 1] = 1;
+#pragma unroll
+            for (int x = 0; x < VEC; ++x) {
+                const int p = tid + x * THREADS, key = p / (D / 8), d = p % (D / 8) * 8;
+                Raw<T> kf = kr[x], vf = vr[x];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    kf.x[i] = finite_bits(kf.x[i]) ? kf.x[i] : (T)0.f;
+                    vf.x[i] = finite_bits(vf.x[i]) ? vf.x[i] : (T)0.f;
+                }
+                shortx8 kp[N], vp[N];
+                to_parts<true>(kf, kp);
+                to_parts<true>(vf, vp);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    if (N > 1) *(shortx8*)&ks[i][key][d] = kp[i];
+                    *(shortx8*)&vs[i][key][d] = vp[i];
                 }
             }
-            __syncthreads();
         }
+        __syncthreads();
+        if (t + 1 < tiles) fetch(t + 1);
+        const bool fix = __builtin_amdgcn_readfirstlane(odd[t & 1]) != 0;
         // 32 keys at a time, those that no row of the wave sees left out
 #pragma unroll
         for (int u = 0; u < PK / 32; ++u) {
@@ -298,7 +289,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
                 s = mul_parts<E, N>(kk, q[x], s);
             }
             if constexpr (N > 1) {
-                if (fix) {
+                if (__builtin_expect(fix, 0)) {
                     // infinities and NaN of the keys by the queries' first parts, which have their signs and zeros: with
                     // all parts an infinity would meet the zeros among the others
                     const T* kp = kg + (int64_t)min(k1 + n, len - 1) * a.ld_k + 8 * h;
@@ -370,7 +361,7 @@ __global__ __launch_bounds__(64 * W, (kWavesPerSimd<T, D>)) void history_attenti
                 }
             }
         }
-        if (fix) {
+        if (__builtin_expect(fix, 0)) {
             for (int key = k0 + ks_at * PK; key < k0 + (ks_at + 1) * PK && key < len; ++key)
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
