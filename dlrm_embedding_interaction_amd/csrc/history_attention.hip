@@ -27,10 +27,10 @@
 // fp32.
 //
 // Measured on MI355X, bf16: 2 histories of up to 12001 events, 8 heads on 2 kv heads
-// of 128, window 4096: 287 us, 810 TFLOP/s of visible pairs, 67% of a large library
+// of 128, window 4096: 279 us, 830 TFLOP/s of visible pairs, 69% of a large library
 // product (1204).  Per 32 rows x 32 keys a wave issues 16 products (512 cycles) and
 // ~110 vector instructions (~600 cycles with the exponentials); the counters show
-// 39% and 40% of the cycles busy with either, the rest waiting for LDS and at
+// 40% and 40% of the cycles busy with either, the rest waiting for LDS and at
 // barriers.  256 histories of up to 512, 4 heads of 64, window 128: 43 us against 29
 // for its bytes, the masked edges of the window being most of the work.  Tried and
 // not kept: two LDS buffers with one barrier a tile (309 against 293 us), 64 keys at
@@ -145,7 +145,7 @@ __device__ __forceinline__ float halves_sum(float v) {
 // 2^15, so that those below 2^-21 are off by 2^-32 at most.
 template <typename T> constexpr float kWeightLog2 = __is_same(T, f16) ? 7.f : -8.f;
 
-// Waves per SIMD that the registers are cut to.  All fits but at heads of 128, where 13 of the 99 kernels keep 36 to 156
+// Waves per SIMD that the registers are cut to.  All fits but at heads of 128, where 13 of the 99 kernels keep 44 to 140
 // bytes a lane in scratch: fp32 in blocks of rows of their own, 16-bit with padding in two waves or with shared keys.
 template <typename T, int D> constexpr int kWavesPerSimd = sizeof(T) == 4 || D == 128 ? 2 : (D == 64 ? 3 : 4);
 

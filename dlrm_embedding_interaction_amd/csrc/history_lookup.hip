@@ -78,7 +78,7 @@ __device__ __forceinline__ Span span_of(const LookupArgs& a, int b) {
 
 // A slot that is none is counted, by one thread of the history's blocks.
 __device__ __forceinline__ void count_refused(const LookupArgs& a, int b) {
-    if (a.slots && (a.slots[b] < 0 || a.slots[b] >= a.c.n_slots)) atomicAdd(&a.c.counters[1], 1);
+    if (a.slots[b] < 0 || a.slots[b] >= a.c.n_slots) atomicAdd(&a.c.counters[1], 1);
 }
 
 // fp32 values as sums of bf16 parts cut off at 8 bits each: the high halves of
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(DIRECT ? 64 * DIRECT : 256, 2) void history_lookup_
             }
         }
         if constexpr (DIRECT) {
-            if (blockIdx.y == 0 && tid == 0) count_refused(a, b);
+            if (__builtin_expect(sp.count == 0, 0) && a.slots && blockIdx.y == 0 && tid == 0) count_refused(a, b);
             break;
         }
         at = start + i1;
@@ -429,7 +429,7 @@ __global__ __launch_bounds__(256) void history_join_kernel(LookupArgs a, const i
     const int cols = rows < 16 ? rows : 16;
     const int count = span_of(a, b).count;
     const int start = count ? meta[b] : 0, per = meta[a.batch];
-    if (count == 0 && (int)blockIdx.y + (int)blockIdx.z + tid == 0) count_refused(a, b);
+    if (a.slots && count == 0 && (int)blockIdx.y + (int)blockIdx.z + tid == 0) count_refused(a, b);
     const int w0 = start / per, w1 = count ? (start + count - 1) / per : 0;
     if (count && w0 == w1) return;                      // one wave had it all
     const int runs = count ? w1 - w0 + 1 : 0;

@@ -344,7 +344,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void history_append_ke
                     const T* f = raw[r][j].x;
                     w.x = code4(f[0], f[1], f[2], f[3], s);
                     w.y = code4(f[4], f[5], f[6], f[7], s);
-                    if (largest) w = make_uint2(keep_finite(w.x), keep_finite(w.y));
+                    if (__builtin_expect(largest, 0)) w = make_uint2(keep_finite(w.x), keep_finite(w.y));
                 } else {
                     const uint2 o = *(const uint2*)(held + ev * D + ch * 8);
                     w = make_uint2(rescale4(o.x, grown), rescale4(o.y, grown));
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void history_append_ke
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 w[i] = code4(raw[r][0].x[i], raw[r][1].x[i], raw[r][2].x[i], raw[r][3].x[i], s);
-            if (largest) {
+            if (__builtin_expect(largest, 0)) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[i] = keep_finite(w[i]);
             }
