@@ -27,8 +27,8 @@
 // fp32.
 //
 // Measured on MI355X, bf16: 2 histories of up to 12001 events, 8 heads on 2 kv heads
-// of 128, window 4096: 279 us, 830 TFLOP/s of visible pairs, 69% of a large library
-// product (1204).  Per 32 rows x 32 keys a wave issues 16 products (512 cycles) and
+// of 128, window 4096: 279 to 288 us, 810 to 830 TFLOP/s of visible pairs, 67 to 69%
+// of a large library product (1204).  Per 32 rows x 32 keys a wave issues 16 products (512 cycles) and
 // ~110 vector instructions (~600 cycles with the exponentials); the counters show
 // 40% and 40% of the cycles busy with either, the rest waiting for LDS and at
 // barriers.  256 histories of up to 512, 4 heads of 64, window 128: 43 us against 29
