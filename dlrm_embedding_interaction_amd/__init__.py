@@ -14,6 +14,7 @@ Functions take CUDA (HIP) torch tensors:
 * ``Model(...)`` holding DLRMv1 parameters, with ``forward(dense, indices, offsets)``
 * ``check_indices(...)``, ``pair_index_map(F)``, ``workspace_bytes``
 * ``history_attention(q, k, v, offsets, window, sinks)`` and ``HistoryCache``, the event-history operators
+* ``history_select(logits, scores, keep)``, the best continuations of beams over histories
 """
 from __future__ import annotations
 
@@ -585,4 +586,4 @@ def probe_l2_stream(src: torch.Tensor, blocks: int = 256, sink: Optional[torch.T
     return sink
 
 
-from .history import HistoryCache, declare as declare_history, history_attention  # noqa: E402,F401
+from .history import HistoryCache, declare as declare_history, history_attention, history_select  # noqa: E402,F401

@@ -19,7 +19,7 @@ LIBRARY = os.path.join(HERE, "libdlrm_mi355x.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ("api.hip", "embbag_interact.hip", "embbag_ex.hip", "gemm.hip", "fused_forward.hip", "hbm_probe.hip",
            "noalloc.hip", "gram_interact.hip", "history_api.hip", "history_attention.hip", "history_lookup.hip",
-           "history_pages.hip")
+           "history_pages.hip", "history_select.hip", "history_shared.hip")
 ARCH = "gfx950"
 
 

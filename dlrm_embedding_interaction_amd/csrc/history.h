@@ -67,6 +67,27 @@ struct AppendArgs {
     int batch, idx32, per_event;        // per_event: one unit of work per event (see the kernel), not per page
 };
 
+// Arguments of the selection of continuations.  ld_allowed 0: one row of bytes for all.
+constexpr int kMostBeams = 128, kMostKept = 128, kMostGroup = 128;
+constexpr int kItemBits = 25;           // of an item's number among a candidate's bits
+constexpr int64_t kMostItems = (int64_t)1 << kItemBits;
+struct SelectArgs {
+    const void* logits;
+    const float* scores;
+    const uint8_t *allowed, *ended;
+    float* out_scores;
+    int32_t *out_parents, *out_items;
+    int64_t ld_logits, ld_allowed;
+    int batch, beams, items, keep, end_item, segs;
+};
+
+// Arguments of the lookup of groups of histories: those of the lookup, and the groups.
+struct SharedArgs {
+    LookupArgs l;
+    const void* groups;                     // offsets, or NULL: batch / n_groups rows each
+    int n_groups, idx32;
+};
+
 // HIP counts the threads along a dimension of a grid in 32 bits.  Launch functions
 // return kTooLarge, having enqueued nothing, where a call would need more.
 constexpr hipError_t kTooLarge = hipErrorInvalidConfiguration;
@@ -75,11 +96,17 @@ inline bool grid_fits(int64_t blocks, int threads) { return (uint64_t)blocks * t
 hipError_t launch_history_attention(const EncodeArgs& a, int dtype, int dim, hipStream_t s);
 hipError_t launch_history_lookup(const LookupArgs& a, int dtype, hipStream_t s);
 size_t lookup_workspace_bytes(const dlrm_history_cache_t& c, int64_t batch, int queries, int n_heads);
+hipError_t launch_history_lookup_shared(const SharedArgs& a, int dtype, void* workspace, hipStream_t s);
+size_t shared_workspace_bytes(const dlrm_history_cache_t& c, int64_t batch, int64_t n_groups, int queries, int n_heads);
+hipError_t launch_history_select(const SelectArgs& a, int dtype, void* workspace, hipStream_t s);
+size_t select_workspace_bytes(int64_t batch, int beams, int64_t items, int keep);
 
 hipError_t launch_history_init(const dlrm_history_cache_t& c, hipStream_t s);
 hipError_t launch_history_append(const AppendArgs& a, int dtype, hipStream_t s);
 hipError_t launch_history_fork(const dlrm_history_cache_t& c, int n, const int32_t* src, const int32_t* dst,
                                int32_t* counts, hipStream_t s);
+hipError_t launch_history_reorder(const dlrm_history_cache_t& c, int n_groups, int group, const int32_t* slots,
+                                  const int32_t* parents, int32_t* counts, hipStream_t s);
 hipError_t launch_history_truncate(const dlrm_history_cache_t& c, int n, const int32_t* slots,
                                    const int32_t* new_lens, int32_t* counts, hipStream_t s);
 hipError_t launch_history_trim(const dlrm_history_cache_t& c, int n, const int32_t* slots, int64_t window,

@@ -149,10 +149,12 @@ DLRM_API dlrm_status_t dlrm_history_append(const dlrm_history_cache_t* c, int64_
     return from_hip(launch_history_append(a, dtype, (hipStream_t)stream));
 }
 
-DLRM_API dlrm_status_t dlrm_history_lookup(const dlrm_history_cache_t* c, const dlrm_attention_t* at, int64_t batch,
-                                           const int32_t* slots, int32_t queries, const void* q, int64_t ld_q,
-                                           void* out, int64_t ld_out, void* workspace, size_t ws_bytes,
-                                           void* stream) {
+namespace {
+
+// Checks and arguments that the lookups share.
+dlrm_status_t lookup_args(const dlrm_history_cache_t* c, const dlrm_attention_t* at, int64_t batch,
+                          const int32_t* slots, int32_t queries, const void* q, int64_t ld_q, void* out,
+                          int64_t ld_out, LookupArgs* a) {
     dlrm_status_t st = check_ready(c);
     if (st != DLRM_OK) return st;
     st = check_attention(at);
@@ -164,19 +166,95 @@ DLRM_API dlrm_status_t dlrm_history_lookup(const dlrm_history_cache_t* c, const 
     if (batch > kIntLimit || !lookup_fits(c, batch, queries, at->n_heads)) return DLRM_E_UNSUPPORTED;
     const int64_t w = (int64_t)at->n_heads * at->head_dim;
     if (ld_q < w || ld_out < w) return DLRM_E_SHAPE;
+    a->c = *c;
+    a->slots = slots, a->q = q, a->out = out;
+    a->ld_q = ld_q, a->ld_out = ld_out;
+    a->window = at->window, a->sinks = at->sinks;
+    a->batch = (int)batch, a->queries = queries, a->n_heads = at->n_heads;
+    const int64_t step = at->dtype == DLRM_DTYPE_F32 ? 4 : 8;
+    a->wide = ld_q % step == 0 && ld_out % step == 0 && (((uintptr_t)q | (uintptr_t)out) & 15u) == 0;
+    a->scale = at->scale;
+    return DLRM_OK;
+}
+
+}  // namespace
+
+DLRM_API dlrm_status_t dlrm_history_lookup(const dlrm_history_cache_t* c, const dlrm_attention_t* at, int64_t batch,
+                                           const int32_t* slots, int32_t queries, const void* q, int64_t ld_q,
+                                           void* out, int64_t ld_out, void* workspace, size_t ws_bytes,
+                                           void* stream) {
+    LookupArgs a = {};
+    dlrm_status_t st = lookup_args(c, at, batch, slots, queries, q, ld_q, out, ld_out, &a);
+    if (st != DLRM_OK) return st;
     st = check_workspace(workspace, ws_bytes, round256(lookup_workspace_bytes(*c, batch, queries, at->n_heads)));
     if (st != DLRM_OK) return st;
-    LookupArgs a = {};
-    a.c = *c;
-    a.slots = slots, a.q = q, a.out = out;
     a.partial = (float*)workspace;
-    a.ld_q = ld_q, a.ld_out = ld_out;
-    a.window = at->window, a.sinks = at->sinks;
-    a.batch = (int)batch, a.queries = queries, a.n_heads = at->n_heads;
-    const int64_t step = at->dtype == DLRM_DTYPE_F32 ? 4 : 8;
-    a.wide = ld_q % step == 0 && ld_out % step == 0 && (((uintptr_t)q | (uintptr_t)out) & 15u) == 0;
-    a.scale = at->scale;
     return from_hip(launch_history_lookup(a, at->dtype, (hipStream_t)stream));
+}
+
+namespace {
+
+// Whether the rows of a call over groups can be counted and chunked.
+bool shared_fits(const dlrm_history_cache_t* c, int64_t batch, int64_t n_groups, int32_t queries, int32_t n_heads) {
+    return n_groups <= kIntLimit && lookup_fits(c, batch, queries, n_heads);
+}
+
+dlrm_status_t check_select(const dlrm_select_t* d, int64_t batch) {
+    if (!d) return DLRM_E_NULL;
+    if (!known_dtype(d->dtype) || d->beams < 1 || d->keep < 1 || d->n_items < 1 || batch < 1) return DLRM_E_SHAPE;
+    if (d->beams > kMostBeams || d->keep > kMostKept || d->n_items > kMostItems || batch > kIntLimit / kMostBeams)
+        return DLRM_E_UNSUPPORTED;
+    return DLRM_OK;
+}
+
+}  // namespace
+
+DLRM_API size_t dlrm_history_shared_workspace_bytes(const dlrm_history_cache_t* c, int64_t batch, int64_t n_groups,
+                                                    int32_t queries, int32_t n_heads) {
+    if (check_cache(c) != DLRM_OK || batch < 1 || batch > kIntLimit || n_groups < 1 || queries < 1) return 0;
+    if (n_heads < 1 || n_heads > 4096 || n_heads % c->n_kv_heads != 0) return 0;
+    if (!shared_fits(c, batch, n_groups, queries, n_heads)) return 0;
+    return round256(shared_workspace_bytes(*c, batch, n_groups, queries, n_heads));
+}
+
+DLRM_API dlrm_status_t dlrm_history_lookup_shared(const dlrm_history_cache_t* c, const dlrm_attention_t* at,
+                                                  int64_t batch, const int32_t* slots, int64_t n_groups,
+                                                  const void* groups, int32_t index_bytes, int32_t queries,
+                                                  const void* q, int64_t ld_q, void* out, int64_t ld_out,
+                                                  void* workspace, size_t ws_bytes, void* stream) {
+    LookupArgs l = {};
+    dlrm_status_t st = lookup_args(c, at, batch, slots, queries, q, ld_q, out, ld_out, &l);
+    if (st != DLRM_OK) return st;
+    if (n_groups < 1 || (groups ? index_bytes != 4 && index_bytes != 8 : batch % n_groups != 0)) return DLRM_E_SHAPE;
+    if (!shared_fits(c, batch, n_groups, queries, at->n_heads)) return DLRM_E_UNSUPPORTED;
+    st = check_workspace(workspace, ws_bytes,
+                         round256(shared_workspace_bytes(*c, batch, n_groups, queries, at->n_heads)));
+    if (st != DLRM_OK) return st;
+    const SharedArgs a = {l, groups, (int)n_groups, index_bytes == 4};
+    return from_hip(launch_history_lookup_shared(a, at->dtype, workspace, (hipStream_t)stream));
+}
+
+DLRM_API size_t dlrm_history_select_workspace_bytes(const dlrm_select_t* d, int64_t batch) {
+    if (check_select(d, batch) != DLRM_OK) return 0;
+    return round256(select_workspace_bytes(batch, d->beams, d->n_items, d->keep));
+}
+
+DLRM_API dlrm_status_t dlrm_history_select(const dlrm_select_t* d, int64_t batch, const void* logits, int64_t ld_logits,
+                                           const float* scores, const uint8_t* allowed, int64_t ld_allowed,
+                                           const uint8_t* ended, float* out_scores, int32_t* out_parents,
+                                           int32_t* out_items, void* workspace, size_t ws_bytes, void* stream) {
+    dlrm_status_t st = check_select(d, batch);
+    if (st != DLRM_OK) return st;
+    if (!logits || !out_scores || !out_parents || !out_items) return DLRM_E_NULL;
+    if (ld_logits < d->n_items || (allowed && ld_allowed != 0 && ld_allowed < d->n_items)) return DLRM_E_SHAPE;
+    st = check_workspace(workspace, ws_bytes, round256(select_workspace_bytes(batch, d->beams, d->n_items, d->keep)));
+    if (st != DLRM_OK) return st;
+    SelectArgs a = {};
+    a.logits = logits, a.scores = scores, a.allowed = allowed, a.ended = ended;
+    a.out_scores = out_scores, a.out_parents = out_parents, a.out_items = out_items;
+    a.ld_logits = ld_logits, a.ld_allowed = ld_allowed;
+    a.batch = (int)batch, a.beams = d->beams, a.items = (int)d->n_items, a.keep = d->keep, a.end_item = d->end_item;
+    return from_hip(launch_history_select(a, d->dtype, workspace, (hipStream_t)stream));
 }
 
 namespace {
@@ -200,6 +278,18 @@ DLRM_API dlrm_status_t dlrm_history_fork(const dlrm_history_cache_t* c, int64_t 
     if (st != DLRM_OK) return st;
     if (!dst) return DLRM_E_NULL;
     return from_hip(launch_history_fork(*c, (int)n, src, dst, (int32_t*)workspace, (hipStream_t)stream));
+}
+
+DLRM_API dlrm_status_t dlrm_history_reorder(const dlrm_history_cache_t* c, int64_t n_groups, int32_t group,
+                                            const int32_t* slots, const int32_t* parents, void* workspace,
+                                            size_t ws_bytes, void* stream) {
+    const dlrm_status_t st = check_release(c, n_groups, parents, workspace, ws_bytes);
+    if (st != DLRM_OK) return st;
+    if (group < 1) return DLRM_E_SHAPE;
+    if (!slots && n_groups * group > c->n_slots) return DLRM_E_SHAPE;
+    if (group > kMostGroup) return DLRM_E_UNSUPPORTED;
+    return from_hip(launch_history_reorder(*c, (int)n_groups, group, slots, parents, (int32_t*)workspace,
+                                           (hipStream_t)stream));
 }
 
 DLRM_API dlrm_status_t dlrm_history_truncate(const dlrm_history_cache_t* c, int64_t n, const int32_t* slots,

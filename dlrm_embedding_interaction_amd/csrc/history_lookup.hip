@@ -31,11 +31,10 @@
 // reaches (6.28 TB/s).  256 histories, window 1024, 4 kv heads of 64: 32 us, 4.0
 // TB/s; there the dependent reads length -> page -> codes and the ~300 vector
 // instructions a tile (decoding, exponentials, splitting) show.
-#include "history.h"
+#include "history_tile.h"
 
 namespace dlrm {
 
-constexpr int kTile = 64;                // events per tile
 constexpr int kLookupWaves = 2048;       // waves a launch aims at: two on each SIMD
 // Histories of at most this many tiles have a block of their own: no second kernel, but the longest history sets the
 // time.  The table's room counts, which the host knows, not what is held.  Measured on ragged histories, blocks against
@@ -45,99 +44,12 @@ constexpr int kLookupWaves = 2048;       // waves a launch aims at: two on each 
 // 64 of up to 64 would still be faster in blocks, 21.3 to 24.6, and of up to 96, 28.6 to 31.3.
 constexpr int kDirectTiles = 32, kDirectTiles8 = 48;
 
-typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-
-// The visible tiles of a history: `lead` tiles from its start, then the tiles
-// from `first` on, `count` in all.
-struct Span {
-    int len, low, lead_events, first, lead, count;
-};
-
-__device__ __forceinline__ Span span_of(const LookupArgs& a, int b) {
-    Span s;
-    const int slot = a.slots ? a.slots[b] : b;
-    const bool held = slot >= 0 && slot < a.c.n_slots;
-    const int most = a.c.max_pages * a.c.page_events;
-    int len = held ? a.c.lens[slot] : 0;
-    len = len < 0 ? 0 : (len > most ? most : len);
-    int low = len > a.window ? len - (int)a.window : 0;
-    int lead = (int)(a.sinks < low ? a.sinks : low);
-    if (lead == low) low = lead = 0;     // the sinks reach the window: everything is seen
-    s.len = len;
-    s.low = low;
-    s.lead_events = lead;
-    s.first = low / kTile;
-    s.lead = (lead + kTile - 1) / kTile;
-    s.lead = s.lead < s.first ? s.lead : s.first;
-    s.count = len ? s.lead + (len + kTile - 1) / kTile - s.first : 0;
-    return s;
-}
-
-// A slot that is none is counted, by one thread of the history's blocks.
-__device__ __forceinline__ void count_refused(const LookupArgs& a, int b) {
-    if (a.slots[b] < 0 || a.slots[b] >= a.c.n_slots) atomicAdd(&a.c.counters[1], 1);
-}
-
-// fp32 values as sums of bf16 parts cut off at 8 bits each: the high halves of
-// two words, packed.
-__device__ __forceinline__ unsigned pack_hi(float a, float b) {
-    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-}
-__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-
-template <int N>
-__device__ __forceinline__ void split8(const float* x, bf16x8* part) {
-    float r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = x[i];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        u32x4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = pack_hi(r[2 * i], r[2 * i + 1]);
-        part[n] = __builtin_bit_cast(bf16x8, w);
-        if (n + 1 < N) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] -= cut(r[i]);
-        }
-    }
-}
-
-// Eight codes times their scale as bf16.
-__device__ __forceinline__ bf16x8 decode8(unsigned lo, unsigned hi, float scale) {
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
-    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
-    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
-    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
-    const u32x4 w = {__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b),
-                     __builtin_bit_cast(unsigned, c), __builtin_bit_cast(unsigned, d)};
-    return __builtin_bit_cast(bf16x8, w);
-}
-
-template <typename T> struct Parts;
-template <> struct Parts<bf16> { static constexpr int q = 1, p = 2; };
-template <> struct Parts<f16> { static constexpr int q = 2, p = 2; };
-template <> struct Parts<float> { static constexpr int q = 3, p = 3; };
-
-// The codes of one tile as the products take them.
-template <int D>
-struct Tile {
-    static constexpr int KL = D >= 64 ? D / 64 : 1;     // 16-byte loads of a key row per lane (D 32: 8 bytes)
-    u32x4 k[4][KL];
-    u32x4 v[D / 16];
-    float ks, vs;
-    bool kin, vin;                                      // the pages are there
-};
-
 // Two waves per SIMD: all fits but in the runs of fp32 heads of 128, which keep 12 to 20 bytes a lane in scratch.
 // DIRECT waves: one block of so many per (history, chunk of rows), its waves taking
 // every DIRECT-th tile and joining their results through LDS.  0: runs of tiles.
 template <int D, int PE, typename T, int DIRECT>
 __global__ __launch_bounds__(DIRECT ? 64 * DIRECT : 256, 2) void history_lookup_kernel(LookupArgs a, int n_waves, int* __restrict__ meta) {
-    constexpr int NQ = Parts<T>::q, NP = Parts<T>::p;
+    constexpr int NQ = Parts<T>::q;
     constexpr int KS = D / 32;                          // 32-element steps of the first product
     constexpr int PT = kTile / PE;                      // pages per tile
     constexpr int OP = D + 4;                           // row stride of the joined results
@@ -207,134 +119,23 @@ __global__ __launch_bounds__(DIRECT ? 64 * DIRECT : 256, 2) void history_lookup_
         const int slot = a.slots ? a.slots[b] : b;
         const int32_t* table = a.c.table + (int64_t)slot * a.c.max_pages;
 
-        // the lane's query column: elements l 64 + g 16 + 8 u + i (D 32: g 8 + i) for step 2 l + u
         bf16x8 q[KS][NQ];
         const bool live = r < rows;
         const int64_t qrow = (int64_t)b * a.queries + (live ? r / group : 0);
         const int qhead = hk * group + (live ? r % group : 0);
-        {
-            const T* qp = (const T*)a.q + qrow * a.ld_q + (int64_t)qhead * D;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const int d0 = D == 32 ? g * 8 : (s >> 1) * 64 + g * 16 + (s & 1) * 8;
-                const Raw<T> raw = a.wide ? load_raw<true>(qp + d0) : load_raw<false>(qp + d0);
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = a.scale < 0.f ? -(float)raw.x[i] : (float)raw.x[i];
-                split8<NQ>(x, q[s]);
-            }
-        }
+        load_query<D>((const T*)a.q + qrow * a.ld_q + (int64_t)qhead * D, a.scale, a.wide, g, q);
         floatx4 o[D / 16];
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) o[j] = floatx4{0.f, 0.f, 0.f, 0.f};
         float m = -INFINITY, l = 0.f;
 
         auto tile_of = [&](int i) { return i < sp.lead ? i : sp.first + (i - sp.lead); };
-        auto load = [&](int i, Tile<D>& t) {
-            const int p0 = tile_of(i) * PT;
-            int pk, pv;
-            if constexpr (PT == 1) {
-                pk = pv = table[p0];
-            } else {
-                const int ik = p0 + (n >> 2) * PT / 4, iv = p0 + g * PT / 4;
-                pk = ik < a.c.max_pages ? table[ik] : -1;
-                pv = iv < a.c.max_pages ? table[iv] : -1;
-            }
-            t.kin = pk >= 0 && pk < a.c.n_pages;
-            t.vin = pv >= 0 && pv < a.c.n_pages;
-            const int64_t hk_k = (int64_t)(t.kin ? pk : 0) * a.c.n_kv_heads + hk;
-            const int64_t hk_v = (int64_t)(t.vin ? pv : 0) * a.c.n_kv_heads + hk;
-            const uint8_t* kp = a.c.k + (hk_k * PE + (n >> 2) * 16 % PE + (n & 3)) * D + g * (D == 32 ? 8 : 16);
-            const uint8_t* vp = a.c.v + (hk_v * D + n) * PE + g * 16 % PE;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int c = 0; c < Tile<D>::KL; ++c) {
-                    if constexpr (D == 32) {
-                        const u32x2 x = *(const u32x2*)(kp + e * 4 * D);
-                        t.k[e][c] = u32x4{x[0], x[1], 0u, 0u};
-                    } else {
-                        t.k[e][c] = *(const u32x4*)(kp + e * 4 * D + c * 64);
-                    }
-                }
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) t.v[j] = *(const u32x4*)(vp + j * 16 * PE);
-            t.ks = a.c.k_scale[hk_k];
-            t.vs = a.c.v_scale[hk_v];
-        };
+        auto load = [&](int i, Tile<D>& t) { load_tile<D, PE>(a.c, table, tile_of(i) * PT, hk, n, g, t); };
         const float c = exponent_scale(a.scale);
         auto use = [&](int i, Tile<D>& t) {
-            floatx4 s[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[e] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < Tile<D>::KL; ++c)
-#pragma unroll
-                    for (int u = 0; u < (D == 32 ? 1 : 2); ++u) {
-                        const bf16x8 kk = decode8(t.k[e][c][2 * u], t.k[e][c][2 * u + 1], t.ks);
-#pragma unroll
-                        for (int x = 0; x < NQ; ++x)
-                            s[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[2 * c + u][x], s[e], 0, 0, 0);
-                    }
-            }
-            // events of the tile's ends, and of pages that are not there, leave: score -inf, codes 0
             const int e0 = tile_of(i) * kTile;
-            unsigned seen = 0xffffu;                     // of the lane group's 16 events
             const bool whole = (e0 >= sp.low || e0 + kTile <= sp.lead_events) && e0 + kTile <= sp.len;
-            if (!whole || __any(!t.vin)) {
-                seen = 0;
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const int j = e0 + g * 16 + x;
-                    seen |= (t.vin && j < sp.len && (j >= sp.low || j < sp.lead_events)) ? 1u << x : 0u;
-                }
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    if (!(seen >> x & 1)) s[x >> 2][x & 3] = -INFINITY;
-                u32x4 keep;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const unsigned f = seen >> (4 * x) & 15u;
-                    keep[x] = (f & 1 ? 0xffu : 0u) | (f & 2 ? 0xff00u : 0u) | (f & 4 ? 0xff0000u : 0u) |
-                              (f & 8 ? 0xff000000u : 0u);
-                }
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) t.v[j] &= keep;
-                t.vs = seen ? t.vs : 1.f;
-            }
-            float top = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < 16; ++x) top = fmaxf(top, s[x >> 2][x & 3]);
-            top = fmaxf(top, swizzle_xor16(top));
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float mx = fmaxf(m, top);
-            if (__any(mx > m)) {
-                const float alpha = mx == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mx) * c);
-                l *= alpha;
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) o[j] *= alpha;
-                m = mx;
-            }
-            const float mc = m == -INFINITY ? 0.f : m * c;
-            float p[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                p[x] = __builtin_amdgcn_exp2f(fmaf(s[x >> 2][x & 3], c, -mc));
-                l += p[x];
-            }
-            bf16x8 pp[2][NP];
-            split8<NP>(p, pp[0]);
-            split8<NP>(p + 8, pp[1]);
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const bf16x8 vv = decode8(t.v[j][2 * h], t.v[j][2 * h + 1], t.vs);
-#pragma unroll
-                    for (int x = 0; x < NP; ++x)
-                        o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pp[h][x], o[j], 0, 0, 0);
-                }
+            use_tile<D, T>(t, q, c, e0, whole, sp.low, sp.lead_events, sp.len, g, o, m, l);
         };
 
         // one tile is on its way while the other is used; where registers allow, the two take turns instead of being

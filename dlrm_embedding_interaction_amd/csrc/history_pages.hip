@@ -555,6 +555,17 @@ __global__ __launch_bounds__(256) void history_rebuild_kernel(dlrm_history_cache
     list_free<4>(c, blockIdx.x * kRebuildChunk, kChunkWords, above);
 }
 
+static hipError_t rebuild(const dlrm_history_cache_t& c, int32_t* counts, hipStream_t s) {
+    if (c.n_pages <= kOneBlockPages) {
+        hipLaunchKernelGGL(history_rebuild_one_kernel, dim3(1), dim3(1024), 0, s, c);
+    } else {
+        const int n = rebuild_chunks(c.n_pages);
+        hipLaunchKernelGGL(history_count_kernel, dim3(n), dim3(256), 0, s, c, counts);
+        hipLaunchKernelGGL(history_rebuild_kernel, dim3(n), dim3(256), 0, s, c, counts);
+    }
+    return hipGetLastError();
+}
+
 // A wave per history, sixteen at a time, then the list: one launch for a call of a
 // few histories of a small pool.  Of 8192 pages, 32 histories: 7.4 us, in launches of
 // its own 8.4; 128 histories 9.8 against 7.5.
@@ -574,14 +585,64 @@ static hipError_t release(const ReleaseArgs& a, int32_t* counts, hipStream_t s) 
     }
     if (!grid_fits(a.n, 256)) return kTooLarge;
     hipLaunchKernelGGL(history_release_kernel<OP>, dim3(a.n), dim3(256), 0, s, a);
-    if (a.c.n_pages <= kOneBlockPages) {
-        hipLaunchKernelGGL(history_rebuild_one_kernel, dim3(1), dim3(1024), 0, s, a.c);
-    } else {
-        const int n = rebuild_chunks(a.c.n_pages);
-        hipLaunchKernelGGL(history_count_kernel, dim3(n), dim3(256), 0, s, a.c, counts);
-        hipLaunchKernelGGL(history_rebuild_kernel, dim3(n), dim3(256), 0, s, a.c, counts);
+    return rebuild(a.c, counts, s);
+}
+
+// ---- reordering ------------------------------------------------------------------
+
+// Histories slots[g group + i] take over those of slots[g group + parents[g group + i]],
+// all at once.  Column x of the page lists depends on column x alone, so a block takes
+// COLS columns of one group: it reads them all before it writes any, and nothing has to
+// be set aside in memory.  Pages that a history keeps, like those that all of a group
+// share, cost their reading alone.
+struct ReorderArgs {
+    dlrm_history_cache_t c;
+    const int32_t *slots, *parents;
+    int n_groups, group;
+};
+constexpr int kReorderCols = 64;
+constexpr int kFreed = -1, kRefused = -2;
+
+__global__ __launch_bounds__(256) void history_reorder_kernel(ReorderArgs a) {
+    __shared__ int slot[kMostGroup], from[kMostGroup], len[kMostGroup];
+    __shared__ int page[kMostGroup][kReorderCols];
+    const dlrm_history_cache_t& c = a.c;
+    const int64_t first = (int64_t)blockIdx.x * a.group;
+    const int tid = threadIdx.x;
+    for (int i = tid; i < a.group; i += 256) {
+        const int s = a.slots ? a.slots[first + i] : (int)(first + i);
+        slot[i] = s >= 0 && s < c.n_slots ? s : -1;
+        if (slot[i] >= 0 && blockIdx.y == 0) len[i] = c.lens[s];
     }
-    return hipGetLastError();
+    __syncthreads();
+    for (int i = tid; i < a.group; i += 256) {
+        const int p = a.parents[first + i];
+        bool ok = slot[i] >= 0 && (p == kFreed || (p >= 0 && p < a.group && slot[p] >= 0));
+        for (int j = 0; j < i; ++j) ok = ok && slot[j] != slot[i];          // a slot that came before
+        from[i] = ok ? p : kRefused;
+    }
+    for (int64_t x0 = (int64_t)blockIdx.y * kReorderCols; x0 < c.max_pages; x0 += (int64_t)gridDim.y * kReorderCols) {
+        for (int e = tid; e < a.group * kReorderCols; e += 256) {
+            const int i = e / kReorderCols, x = e % kReorderCols;
+            if (slot[i] >= 0 && x0 + x < c.max_pages) page[i][x] = c.table[(int64_t)slot[i] * c.max_pages + x0 + x];
+        }
+        __syncthreads();
+        for (int e = tid; e < a.group * kReorderCols; e += 256) {
+            const int i = e / kReorderCols, x = e % kReorderCols;
+            if (from[i] == kRefused || x0 + x >= c.max_pages) continue;
+            const int p = from[i] == kFreed ? -1 : page[from[i]][x], o = page[i][x];
+            if (p == o) continue;
+            c.table[(int64_t)slot[i] * c.max_pages + x0 + x] = p;
+            if (p >= 0 && p < c.n_pages) atomicAdd(&c.refs[p], 1);
+            drop_page(c, o);
+        }
+        __syncthreads();
+    }
+    if (blockIdx.y == 0)
+        for (int i = tid; i < a.group; i += 256) {
+            if (from[i] == kRefused) atomicAdd(&c.counters[1], 1);
+            else c.lens[slot[i]] = from[i] == kFreed ? 0 : len[from[i]];
+        }
 }
 
 // ---- compaction ------------------------------------------------------------------
@@ -755,6 +816,16 @@ hipError_t launch_history_append(const AppendArgs& args, int dtype, hipStream_t 
 hipError_t launch_history_fork(const dlrm_history_cache_t& c, int n, const int32_t* src, const int32_t* dst,
                                int32_t* counts, hipStream_t s) {
     return release<kFork>(ReleaseArgs{c, src, dst, 0, 0, n}, counts, s);
+}
+
+hipError_t launch_history_reorder(const dlrm_history_cache_t& c, int n_groups, int group, const int32_t* slots,
+                                  const int32_t* parents, int32_t* counts, hipStream_t s) {
+    const ReorderArgs a = {c, slots, parents, n_groups, group};
+    const int cols = (c.max_pages + kReorderCols - 1) / kReorderCols;
+    if (!grid_fits(n_groups, 256)) return kTooLarge;
+    hipLaunchKernelGGL(history_reorder_kernel, dim3(n_groups, cols < 65535 ? cols : 65535), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : rebuild(c, counts, s);
 }
 
 hipError_t launch_history_truncate(const dlrm_history_cache_t& c, int n, const int32_t* slots,

@@ -1,12 +1,13 @@
-"""Event histories: windowed attention over ragged histories and the 8-bit paged history cache.
+"""Event histories: windowed attention over ragged histories, the 8-bit paged history cache and its continuation
+with beams.
 
 Thin marshalling over the ``dlrm_history_*`` calls of ``include/dlrm_mi355x.h``, re-exported by the
-package: ``history_attention`` and ``HistoryCache``.
+package: ``history_attention``, ``history_select`` and ``HistoryCache``.
 """
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+from typing import Optional, Tuple, Union
 
 import torch
 
@@ -28,9 +29,14 @@ class _Cache(ctypes.Structure):
                [(n, _vp) for n in ("k", "v", "k_scale", "v_scale", "table", "lens", "refs", "free_pages", "counters")]
 
 
+class _Select(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("beams", ctypes.c_int32), ("keep", ctypes.c_int32),
+                ("end_item", ctypes.c_int32), ("n_items", ctypes.c_int64)]
+
+
 def declare(L: ctypes.CDLL) -> None:
     i32, i64, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-    att, cache = ctypes.POINTER(_Attention), ctypes.POINTER(_Cache)
+    att, cache, select = ctypes.POINTER(_Attention), ctypes.POINTER(_Cache), ctypes.POINTER(_Select)
     L.dlrm_history_attention.argtypes = [att, i64, i64, _vp, i32, _vp, i64, _vp, i64, _vp, i64, _vp, _vp, i64, _vp]
     L.dlrm_history_workspace_bytes.argtypes = [cache, i64, i32, i32]
     L.dlrm_history_workspace_bytes.restype = size
@@ -41,7 +47,16 @@ def declare(L: ctypes.CDLL) -> None:
     L.dlrm_history_truncate.argtypes = [cache, i64, _vp, _vp, _vp, size, _vp]
     L.dlrm_history_trim.argtypes = [cache, i64, _vp, i64, i64, _vp, size, _vp]
     L.dlrm_history_compact.argtypes = [cache, _vp, size, _vp]
-    for f in ("attention", "init", "append", "lookup", "fork", "truncate", "trim", "compact"):
+    L.dlrm_history_reorder.argtypes = [cache, i64, i32, _vp, _vp, _vp, size, _vp]
+    L.dlrm_history_shared_workspace_bytes.argtypes = [cache, i64, i64, i32, i32]
+    L.dlrm_history_shared_workspace_bytes.restype = size
+    L.dlrm_history_lookup_shared.argtypes = [cache, att, i64, _vp, i64, _vp, i32, i32, _vp, i64, _vp, i64, _vp, size,
+                                             _vp]
+    L.dlrm_history_select_workspace_bytes.argtypes = [select, i64]
+    L.dlrm_history_select_workspace_bytes.restype = size
+    L.dlrm_history_select.argtypes = [select, i64, _vp, i64, _vp, _vp, i64, _vp, _vp, _vp, _vp, _vp, size, _vp]
+    for f in ("attention", "init", "append", "lookup", "fork", "truncate", "trim", "compact", "reorder",
+              "lookup_shared", "select"):
         getattr(L, f"dlrm_history_{f}").restype = ctypes.c_int
 
 
@@ -147,6 +162,91 @@ def history_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets
     return out
 
 
+_SELECT = {}        # descriptors and workspace sizes by their values
+
+
+def _bytes(t: torch.Tensor, name: str, device: torch.device) -> torch.Tensor:
+    """A tensor of bytes or truth values as bytes."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor of bool or uint8")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t.view(torch.uint8) if t.dtype is torch.bool else t
+
+
+def _item_rows(t: torch.Tensor, name: str) -> int:
+    """Row stride of (groups, beams, items) rows."""
+    groups, beams, items = t.shape
+    stride = t.stride()
+    if items > 1 and stride[2] != 1:
+        raise ValueError(f"the items of one row of {name} must lie side by side")
+    if groups > 1 and beams > 1 and stride[0] != beams * stride[1]:
+        raise ValueError(f"{name} must have evenly spaced rows")
+    return stride[1] if beams > 1 else (stride[0] if groups > 1 else max(items, 1))
+
+
+def history_select(logits: torch.Tensor, scores: Optional[torch.Tensor] = None, keep: Optional[int] = None,
+                   allowed: Optional[torch.Tensor] = None, ended: Optional[torch.Tensor] = None,
+                   end_item: int = -1) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The best continuations of groups of beams -> (scores, parents, items), each (groups, keep).
+
+    ``logits`` (groups, beams, items), fp32, bf16 or fp16: of each beam's next item; rows may be columns of a wider
+    tensor.  ``scores`` (groups, beams) fp32: the sums of log-probabilities so far (none: 0).  A continuation's score
+    is its beam's plus the log-probability of its item; the ``keep`` (none: as many as there are beams) best of each
+    group come in descending order, equal ones by beam, then by item; what is missing is -inf, -1 and -1.
+    ``allowed`` (items,) or (groups, beams, items), truth values: items that may be taken.  ``ended`` (groups, beams),
+    truth values: beams that are carried over as they are, with ``end_item`` as their item.  A beam whose score is not
+    finite, or with NaN or +inf among its allowed logits, gives no continuations."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in DTYPES or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA (HIP) tensor of fp32, bf16 or fp16")
+    if logits.dim() != 3:
+        raise ValueError("logits must be (groups, beams, items)")
+    dev = logits.device
+    groups, beams, items = logits.shape
+    keep = beams if keep is None else int(keep)
+    ld = _item_rows(logits, "logits")
+    if scores is not None:
+        _dev(scores, torch.float32, "scores")
+        if tuple(scores.shape) != (groups, beams) or scores.device != dev:
+            raise ValueError(f"scores must be (groups, beams) on {dev}")
+    ld_allowed = 0
+    if allowed is not None:
+        allowed = _bytes(allowed, "allowed", dev)
+        if tuple(allowed.shape) == (items,):
+            if items > 1 and allowed.stride(0) != 1:
+                raise ValueError("the items of one row of allowed must lie side by side")
+        elif tuple(allowed.shape) == (groups, beams, items):
+            ld_allowed = _item_rows(allowed, "allowed")
+        else:
+            raise ValueError("allowed must be (items,) or (groups, beams, items)")
+    if ended is not None:
+        ended = _bytes(ended, "ended", dev)
+        if tuple(ended.shape) != (groups, beams) or not ended.is_contiguous():
+            raise ValueError("ended must be contiguous (groups, beams)")
+    if dev.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return history_select(logits, scores, keep, allowed, ended, end_item)
+    key = (logits.dtype, beams, keep, end_item, items, groups)
+    entry = _SELECT.get(key)
+    if entry is None:
+        d = _Select(DTYPES[logits.dtype], beams, keep, int(end_item), items)
+        if len(_SELECT) > 1024:
+            _SELECT.clear()
+        entry = _SELECT[key] = (ctypes.byref(d), int(load().dlrm_history_select_workspace_bytes(ctypes.byref(d),
+                                                                                                groups)))
+    ws = torch.empty(max(entry[1], 256), dtype=torch.uint8, device=dev)
+    out_scores = torch.empty((groups, max(keep, 0)), dtype=torch.float32, device=dev)
+    out = torch.empty((2, groups, max(keep, 0)), dtype=torch.int32, device=dev)
+    rc = load().dlrm_history_select(entry[0], groups, logits.data_ptr(), ld,
+                                    None if scores is None else scores.data_ptr(),
+                                    None if allowed is None else allowed.data_ptr(), ld_allowed,
+                                    None if ended is None else ended.data_ptr(), out_scores.data_ptr(),
+                                    out[0].data_ptr(), out[1].data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev))
+    if rc != DLRM_OK:
+        _check(rc, "dlrm_history_select")
+    return out_scores, out[0], out[1]
+
+
 class HistoryCache:
     """Keys and values of many histories in 8 bits, on pages of a common pool.
 
@@ -202,12 +302,14 @@ class HistoryCache:
         self._ws = {}           # stream -> workspace: calls on two streams may overlap
         self._need = {}
 
-    def _workspace(self, stream: int, batch: int, queries: int = 0, heads: int = 0):
+    def _workspace(self, stream: int, batch: int, queries: int = 0, heads: int = 0, groups: int = 0):
         """(address, bytes, the tensor that holds them) for one call on the stream."""
-        key = (batch, queries, heads)
+        key = (batch, queries, heads, groups)
         need = self._need.get(key)
         if need is None:
-            need = max(256, int(load().dlrm_history_workspace_bytes(self._ref, batch, queries, heads)))
+            L = load()
+            need = max(256, int(L.dlrm_history_shared_workspace_bytes(self._ref, batch, groups, queries, heads)
+                                if groups else L.dlrm_history_workspace_bytes(self._ref, batch, queries, heads)))
             if len(self._need) > 256:
                 self._need.clear()
             self._need[key] = need
@@ -253,10 +355,8 @@ class HistoryCache:
                                         ws[0], ws[1], s)
         _check(rc, "dlrm_history_append")
 
-    def lookup(self, q: torch.Tensor, window: int = ALL_EVENTS, sinks: int = 0, scale: Optional[float] = None,
-               slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """Queries (batch, n_heads, head_dim) or (batch, queries, n_heads, head_dim) over the histories slots[b]
-        (b without slots): the last ``window`` events and the first ``sinks`` of each -> out of q's shape."""
+    def _queries(self, q, window, sinks, scale, out):
+        """The checked arguments of a lookup."""
         if not isinstance(q, torch.Tensor) or q.dtype not in DTYPES:
             raise TypeError("q must be an fp32, bf16 or fp16 tensor")
         if q.dim() not in (3, 4):
@@ -272,12 +372,69 @@ class HistoryCache:
         batch, heads, dim = q.shape[0], q.shape[-2], q.shape[-1]
         queries = q.shape[1] if q.dim() == 4 else 1
         a = _attention(q.dtype, heads, self.n_kv_heads, dim, window, sinks, scale)
+        return a, batch, queries, heads, ld_q, out, ld_out
+
+    def lookup(self, q: torch.Tensor, window: int = ALL_EVENTS, sinks: int = 0, scale: Optional[float] = None,
+               slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Queries (batch, n_heads, head_dim) or (batch, queries, n_heads, head_dim) over the histories slots[b]
+        (b without slots): the last ``window`` events and the first ``sinks`` of each -> out of q's shape."""
+        a, batch, queries, heads, ld_q, out, ld_out = self._queries(q, window, sinks, scale, out)
         s = _stream(self.device)
         ws = self._workspace(s, batch, queries, heads)
         rc = load().dlrm_history_lookup(self._ref, a, batch, self._slots(slots, batch), queries,
                                         q.data_ptr(), ld_q, out.data_ptr(), ld_out, ws[0], ws[1], s)
         _check(rc, "dlrm_history_lookup")
         return out
+
+    def lookup_shared(self, q: torch.Tensor, groups: Union[int, torch.Tensor], window: int = ALL_EVENTS, sinks: int = 0,
+                      scale: Optional[float] = None, slots: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """``lookup`` of histories in groups that share what came first, as forks of one history do: the events that
+        lie on the same pages in all of a group are read once for the group.
+
+        ``groups``: how many histories of the batch, one behind the other, each group has; or ascending offsets
+        (n_groups,), group g being the histories [groups[g], groups[g + 1]).  What is shared is found in the page
+        lists, so that the result is ``lookup``'s whatever the groups are, up to the order of its sums."""
+        a, batch, queries, heads, ld_q, out, ld_out = self._queries(q, window, sinks, scale, out)
+        if isinstance(groups, torch.Tensor):
+            ib, n_groups, at = _offsets(groups, self.device), groups.shape[0], groups.data_ptr()
+        else:
+            groups = int(groups)
+            if groups < 1 or batch % groups != 0:
+                raise ValueError("the batch must hold whole groups")
+            ib, n_groups, at = 8, batch // groups, None
+        if self.device.index != torch._C._cuda_getDevice():
+            with torch.cuda.device(self.device):
+                return self.lookup_shared(q, groups, window, sinks, scale, slots, out)
+        s = _stream(self.device)
+        ws = self._workspace(s, batch, queries, heads, max(n_groups, 1))
+        rc = load().dlrm_history_lookup_shared(self._ref, a, batch, self._slots(slots, batch), n_groups, at, ib, queries,
+                                               q.data_ptr(), ld_q, out.data_ptr(), ld_out, ws[0], ws[1], s)
+        if rc != DLRM_OK:
+            _check(rc, "dlrm_history_lookup_shared")
+        return out
+
+    def reorder(self, parents: torch.Tensor, slots: Optional[torch.Tensor] = None) -> None:
+        """The histories of groups change places, all at once: in each group g history slots[g, i] becomes what
+        slots[g, parents[g, i]] was, on shared pages; a parent of -1 frees it.
+
+        ``parents`` (groups, beams) int32, as ``history_select`` gives them; ``slots`` the same shape (none: 0, 1,
+        2 ...).  A parent may come any number of times; slots may come once in the call."""
+        _dev(parents, torch.int32, "parents")
+        if parents.dim() != 2 or parents.device != self.device:
+            raise ValueError(f"parents must be (groups, beams) on {self.device}")
+        if slots is not None:
+            _dev(slots, torch.int32, "slots")
+            if slots.shape != parents.shape or slots.device != self.device:
+                raise ValueError("one slot for each parent")
+        if self.device.index != torch._C._cuda_getDevice():
+            with torch.cuda.device(self.device):
+                return self.reorder(parents, slots)
+        s = _stream(self.device)
+        ws = self._workspace(s, 1)
+        _check(load().dlrm_history_reorder(self._ref, parents.shape[0], parents.shape[1],
+                                           None if slots is None else slots.data_ptr(), parents.data_ptr(), ws[0],
+                                           ws[1], s), "dlrm_history_reorder")
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor) -> None:
         """History dst[i] becomes a copy of src[i] on shared pages; an append copies what it has to."""

@@ -580,6 +580,30 @@ dlrm_status_t dlrm_history_lookup(const dlrm_history_cache_t* c, const dlrm_atte
                                   int64_t ld_out, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * dlrm_history_lookup_shared -- the same for histories in groups that share what
+ * came first, as forks do: events that lie on the same pages in all histories of a
+ * group are read once for the group.  Which these are is found in the page lists:
+ * the groups say only which histories to look at together.  Out is dlrm_history_lookup's, up to
+ * the order of its sums.
+ *   n_groups    >= 1
+ *   groups      device (n_groups) ascending integers of index_bytes: group g is the
+ *               histories [groups[g], groups[g+1]) of the batch, the last one
+ *               ending at its end, the first one beginning at 0 whatever groups[0]
+ *               holds; groups may be empty.  NULL: groups of batch / n_groups,
+ *               which has to be whole
+ *   workspace   of dlrm_history_shared_workspace_bytes (host only; 0 on invalid
+ *               arguments), a few MB and 64 head_dim bytes for each query row and
+ *               each of a group's kv heads on top
+ */
+size_t dlrm_history_shared_workspace_bytes(const dlrm_history_cache_t* c, int64_t batch, int64_t n_groups,
+                                           int32_t queries, int32_t n_heads);
+dlrm_status_t dlrm_history_lookup_shared(const dlrm_history_cache_t* c, const dlrm_attention_t* a, int64_t batch,
+                                         const int32_t* slots, int64_t n_groups, const void* groups,
+                                         int32_t index_bytes, int32_t queries, const void* q, int64_t ld_q,
+                                         void* out, int64_t ld_out, void* workspace, size_t ws_bytes,
+                                         void* stream);
+
+/*
  * Pages.  Each of these calls takes n device slots.
  *
  * dlrm_history_fork      dst[i] lets go of what it held and takes over src[i]'s
@@ -601,6 +625,62 @@ dlrm_status_t dlrm_history_truncate(const dlrm_history_cache_t* c, int64_t n, co
 dlrm_status_t dlrm_history_trim(const dlrm_history_cache_t* c, int64_t n, const int32_t* slots, int64_t window,
                                 int64_t sinks, void* workspace, size_t ws_bytes, void* stream);
 dlrm_status_t dlrm_history_compact(const dlrm_history_cache_t* c, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * dlrm_history_reorder -- the histories of groups change places: in group g the
+ * history slots[g * group + i] becomes what slots[g * group + parents[g * group + i]] was before
+ * the call, for all i at once; pages are shared as by a fork.  A parent may be
+ * named many times or not at all; -1 frees the history.  Other parents outside
+ * [0, group), parents whose slot is none, and slots that stand in their group a
+ * second time are refused: those histories stay as they were.  No slot may appear
+ * in two groups.
+ *   slots     device (n_groups * group), or NULL: 0, 1, 2 ...
+ *   parents   device (n_groups * group)
+ *   group     at most 128
+ */
+dlrm_status_t dlrm_history_reorder(const dlrm_history_cache_t* c, int64_t n_groups, int32_t group,
+                                   const int32_t* slots, const int32_t* parents, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
+/*
+ * dlrm_history_select -- the best continuations of groups of histories (beams).
+ * Row b * beams + w of logits belongs to beam w of group b, which has the score
+ * scores[b * beams + w] so far.  Its continuation by item v has the score
+ *   score + logits[v] - log(sum over allowed u of exp(logits[u])).
+ * Of each group the `keep` best are written in descending order: score, beam
+ * (parent) and item; equal scores by the lowest beam, then the lowest item.  Where
+ * there are fewer, the rest is -inf, -1 and -1.  With one beam and no scores: the
+ * best items of a row and their log-probabilities.
+ *   dtype     of logits; sums and scores are held in 64 bits, so that the order is
+ *             that of the logits given, and scores are rounded when written
+ *   beams, keep  1 to 128; n_items up to 2^25
+ *   logits    device (batch * beams, ld_logits).  -inf: an item that is never taken
+ *   scores    device (batch * beams) or NULL (all 0).  A beam whose score is not
+ *             finite gives no continuations, and its logits are not read
+ *   allowed   device bytes (batch * beams, ld_allowed), or one row for all
+ *             (ld_allowed 0), or NULL: an item whose byte is 0 is not taken, and
+ *             whatever its logit holds changes nothing
+ *   ended     device (batch * beams) bytes or NULL: a beam whose byte is not 0 is
+ *             carried over: its only continuation is end_item at its own score.
+ *             Its logits are not read
+ * A beam with NaN or +inf among its allowed logits, or without a finite one, gives
+ * no continuations.
+ *
+ * dlrm_history_select_workspace_bytes -- its workspace; 0 on invalid arguments.
+ */
+typedef struct dlrm_select {
+    int32_t dtype;
+    int32_t beams;
+    int32_t keep;
+    int32_t end_item;
+    int64_t n_items;
+} dlrm_select_t;
+
+size_t dlrm_history_select_workspace_bytes(const dlrm_select_t* d, int64_t batch);
+dlrm_status_t dlrm_history_select(const dlrm_select_t* d, int64_t batch, const void* logits, int64_t ld_logits,
+                                  const float* scores, const uint8_t* allowed, int64_t ld_allowed,
+                                  const uint8_t* ended, float* out_scores, int32_t* out_parents,
+                                  int32_t* out_items, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Measurement helpers (not part of the forward).  They set the bandwidth
