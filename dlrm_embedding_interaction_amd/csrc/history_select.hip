@@ -12,24 +12,26 @@ namespace dlrm {
 
 typedef unsigned long long u64;
 
-constexpr int kSelectTile = 512;         // logits a wave takes at a time: eight a lane
-constexpr int kSelectRoom = 1024;        // candidates a wave has room for
+constexpr int kSelectHalf = 512;         // logits of half a tile in the 16-bit types, or of a whole one: eight a lane
+constexpr int kSelectRoom = 512;         // candidates a wave has room for
+constexpr int kGroups = 16;              // groups of tiles in a wave's part
 constexpr int kSelectWaves = 4096;       // waves a launch aims at: sixteen on each CU
+constexpr int kSelectBlock = 8;          // waves of a block
 constexpr int kJoinWaves = 8;
 constexpr int kJoinRoom = 512;
 constexpr int kMostLists = 4096;         // parts of a group's rows
 
 // What one wave leaves of its part of a row: the sum of exponentials against `ref`,
-// the largest logit, and whether a NaN was among them.
+// the largest logit, how many candidates it lists, and whether a NaN was among them.
 struct SelectSum {
     double sum;
     float ref, top;
-    int bad;
+    int n, bad;
 };
 
 struct SelectWs {
     SelectSum* sums;     // (rows, segs)
-    u64* keys;           // (rows, segs, keep): 0 where there is none
+    u64* keys;           // (rows, segs, keep)
 };
 
 // Bits in the order of the values they stand for; -0 must have become 0.
@@ -111,7 +113,7 @@ __device__ __forceinline__ Best kth(const Best (&e)[ROOM], u64 all, u64 any, int
     return t;
 }
 template <int ROOM, typename K>
-__device__ __forceinline__ K keep_largest(K* buf, int n, int keep) {
+__device__ __forceinline__ K keep_among(K* buf, int n, int keep) {
     const int lane = threadIdx.x & 63;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     K e[ROOM / 64];
@@ -135,11 +137,18 @@ __device__ __forceinline__ K keep_largest(K* buf, int n, int keep) {
     return t;
 }
 
-// The keep-th largest of two values per lane, 1 <= keep <= 128.
+template <int ROOM, typename K>
+__device__ __forceinline__ K keep_largest(K* buf, int n, int keep) {
+    return n <= 128 ? keep_among<128>(buf, n, keep) : keep_among<ROOM>(buf, n, keep);
+}
+
+// The keep-th largest of two values per lane, 1 <= keep <= 128, or a little less: its
+// bits from LOW on.
+template <int LOW>
 __device__ __forceinline__ float kth_of_lanes(float a, float b, int keep) {
     const unsigned x = ordered(a + 0.f), y = ordered(b + 0.f);
     unsigned t = 0;
-    for (unsigned bit = 0x80000000u; bit; bit >>= 1) {
+    for (unsigned bit = 0x80000000u; bit >> LOW; bit >>= 1) {
         const int count = __popcll(__ballot(x >= (t | bit))) + __popcll(__ballot(y >= (t | bit)));
         if (count >= keep) t |= bit;
         if (count == keep) break;
@@ -209,62 +218,136 @@ __device__ __forceinline__ void values_of(const Eight<T>& r, float* f) {
     }
 }
 
-// One wave's part of a row.  The sum is taken against `ref`, which needs only be near
-// the largest logit: 64 bits hold e^300 times too much, so that it moves in no
-// ordinary row, and no tile waits for a maximum over the wave.  Only logits that reach
-// `floor` can be among the best: the keep-th largest of 128 groups of logits, and of
-// the candidates when their room was last full.  Most tiles have none.
+// What the waves of a block leave for one another and for themselves.
+struct SelectShared {
+    u64 room[kSelectBlock][kSelectRoom];
+    float tops[kSelectBlock][kGroups][64];  // later the numbers of those that reach the floor
+    float found[kSelectBlock];
+};
+
+// One wave's part of a row, every wave of the block taking part.
+//
+// The sum is taken against `ref`, which needs only be near the largest logit: 64 bits
+// hold e^300 times too much, so that no tile waits for a maximum over the wave.  It is
+// a multiple of 512, 0 in ordinary rows: a logit then adds the same wherever it
+// stands, and rows of the same logits in another order have sums that differ by their
+// additions' rounding alone (see the join).
+//
+// Of the logits themselves the pass over them keeps the largest of each group that a
+// lane sees.  Only logits that reach `floor` can be among the best: the keep-th largest
+// of 128 of the part's groups, or the least of what the `sharing` waves of the row find
+// so for the keep / sharing-th, whichever is larger.  The few groups that reach it are
+// then read once more, from a cache.  Collecting candidates on the way took twice as
+// long as the sums: nearly every tile has one while the floor still rises.
 template <typename T, bool MASKED>
-__device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs& ws, int64_t unit, u64* buf) {
-    const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs& ws, int64_t unit, SelectShared& s) {
+    constexpr int HALVES = sizeof(T) == 2 ? 2 : 1, E = 8 * HALVES, TILE = kSelectHalf * HALVES;
+    constexpr int LOW = __is_same(T, bf16) ? 16 : (__is_same(T, f16) ? 13 : 10);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int64_t row = unit / a.segs;
     const int seg = (int)(unit - row * a.segs);
-    if (a.scores && !(fabsf(a.scores[row]) < INFINITY)) return;      // nothing of the row is read, here or by the join
-    if (a.ended && a.ended[row]) return;
-    const int tiles = (a.items + kSelectTile - 1) / kSelectTile;
-    const int t0 = (int)((int64_t)tiles * seg / a.segs), t1 = (int)((int64_t)tiles * (seg + 1) / a.segs);
+    const int sharing = a.segs < kSelectBlock ? a.segs : kSelectBlock, share = (a.keep + sharing - 1) / sharing;
+    // of a row without continuations nothing is read, here or by the join
+    const bool live = row < (int64_t)a.batch * a.beams && (!a.scores || fabsf(a.scores[row]) < INFINITY) &&
+                      !(a.ended && a.ended[row]);
+    const int tiles = (a.items + TILE - 1) / TILE;
+    const int t0 = (int)((int64_t)tiles * seg / a.segs), t1 = live ? (int)((int64_t)tiles * (seg + 1) / a.segs) : t0;
+    const int group = (t1 - t0 + kGroups - 1) / kGroups;        // tiles
     const T* x = (const T*)a.logits + row * a.ld_logits;
     const uint8_t* may = MASKED ? a.allowed + row * a.ld_allowed : nullptr;
 
-    int n = 0;
-    u64 least = 0;                 // candidates have to be larger
-    float ref = -3.4028235e38f, floor = -INFINITY, low = -INFINITY, high = -INFINITY;
+    float ref = -3.4028235e38f, low = -INFINITY, high = -INFINITY, most = -INFINITY;
     double sum = 0;
     bool bad = false;
-    Eight<T> next = load_eight<T, MASKED>(x, may, t0 * kSelectTile + lane * 8, a.items);
-    for (int t = t0; t < t1; ++t) {
-        const int at = t * kSelectTile + lane * 8;
-        const Eight<T> raw = next;
-        if (t + 1 < t1) next = load_eight<T, MASKED>(x, may, at + kSelectTile, a.items);
-        float f[8];
-        values_of<T, MASKED>(raw, f);
+    Eight<T> next[HALVES];
+    if (t0 < t1)
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) bad |= __builtin_isunordered(f[i], f[i + 1]);
-        const float l = fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), h = fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7]));
+        for (int h = 0; h < HALVES; ++h)
+            next[h] = load_eight<T, MASKED>(x, may, t0 * TILE + h * kSelectHalf + lane * 8, a.items);
+    int groups = 0, left = group;
+    for (int t = t0; t < t1; ++t) {
+        const int at = t * TILE + lane * 8;
+        float f[E];
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+            values_of<T, MASKED>(next[h], f + 8 * h);
+            if (t + 1 < t1) next[h] = load_eight<T, MASKED>(x, may, at + TILE + h * kSelectHalf, a.items);
+        }
+        float l = f[0], h = f[E / 2];
+#pragma unroll
+        for (int i = 0; i < E; i += 2) bad |= __builtin_isunordered(f[i], f[i + 1]);
+#pragma unroll
+        for (int i = 1; i < E / 2; ++i) {
+            l = fmaxf(l, f[i]);
+            h = fmaxf(h, f[E / 2 + i]);
+        }
         low = fmaxf(low, l);
         high = fmaxf(high, h);
         const float top = fmaxf(l, h);
+        most = fmaxf(most, top);
+        if (--left == 0 || t + 1 == t1) {
+            s.tops[wave][groups++][lane] = most;
+            most = -INFINITY;
+            left = group;
+        }
         if (__builtin_expect(__any(top > ref + 300.f), 0)) {
-            const float to = wave_max(top);
+            const float to = 512.f * rintf(wave_max(top) / 512.f);
             sum *= weight((double)ref - (double)to);
             ref = to;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += weight((double)f[i] - (double)ref);
-        const int done = t - t0 + 1;
-        if ((done & (done - 1)) == 0) floor = fmaxf(floor, kth_of_lanes(low, high, a.keep));
-        if (__any(top >= floor)) {
-            if (n > kSelectRoom - kSelectTile) {
-                least = keep_largest<kSelectRoom>(buf, n, a.keep);
-                floor = fmaxf(floor, unordered((unsigned)(least >> 32)));
-                n = a.keep;
-            }
+        for (int i = 0; i < E; ++i) sum += weight((double)f[i] - (double)ref);
+    }
+    float floor = kth_of_lanes<LOW>(low, high, a.keep);
+    if (sharing > 1) {
+        const float own = kth_of_lanes<LOW>(low, high, share);
+        if (lane == 0) s.found[wave] = own;
+        __syncthreads();
+        float all = INFINITY;
+        for (int i = 0; i < sharing; ++i) all = fminf(all, s.found[wave / sharing * sharing + i]);
+        floor = fmaxf(floor, all);
+    }
+    if (!live) return;
+
+    // the groups that reach the floor, in order
+    unsigned short* which = (unsigned short*)s.tops[wave];
+    int reach = 0;
+    for (int j = 0; j < groups; ++j) {
+        const float top = s.tops[wave][j][lane];
+        const bool in = top >= floor && top > -INFINITY;
+        const u64 go = __ballot(in);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (in) which[reach + __popcll(go & ((1ull << lane) - 1))] = (unsigned short)(j * 64 + lane);
+        reach += __popcll(go);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    u64* buf = s.room[wave];
+    int n = 0;
+    u64 least = 0;                 // candidates have to be larger
+    for (int e = 0; e < reach; e += 64) {
+        const int g = e + lane < reach ? (int)which[e + lane] : -1;
+        for (int k = 0; k < group; ++k) {
+            const int t = t0 + (g >> 6) * group + k;
+            const int at = g >= 0 && t < t1 ? t * TILE + (g & 63) * 8 : a.items;
+            Eight<T> raw[HALVES];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const u64 key = (u64)ordered(f[i] + 0.f) << 32 | (0xffffffffu - (unsigned)(at + i));
-                const u64 in = __ballot(f[i] >= floor && f[i] > -INFINITY && key > least);
-                if (in >> lane & 1) buf[n + __popcll(in & ((1ull << lane) - 1))] = key;
-                n += __popcll(in);
+            for (int h = 0; h < HALVES; ++h) raw[h] = load_eight<T, MASKED>(x, may, at + h * kSelectHalf, a.items);
+#pragma unroll 1
+            for (int h = 0; h < HALVES; ++h) {
+                float f[8];
+                values_of<T, MASKED>(HALVES == 2 && h ? raw[HALVES - 1] : raw[0], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const u64 key = (u64)ordered(f[i] + 0.f) << 32 | (0xffffffffu - (unsigned)(at + h * kSelectHalf + i));
+                    const u64 in = __ballot(f[i] >= floor && f[i] > -INFINITY && key > least);
+                    if (!in) continue;
+                    if (n > kSelectRoom - 64) {
+                        least = keep_largest<kSelectRoom>(buf, n, a.keep);
+                        n = a.keep;
+                    }
+                    if (in >> lane & 1) buf[n + __popcll(in & ((1ull << lane) - 1))] = key;
+                    n += __popcll(in);
+                }
             }
         }
     }
@@ -274,12 +357,12 @@ __device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs&
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     u64* keys = ws.keys + unit * a.keep;
-    for (int i = lane; i < a.keep; i += 64) keys[i] = i < n ? buf[i] : 0;
-    const float most = wave_max(fmaxf(low, high));
+    for (int i = lane; i < n; i += 64) keys[i] = buf[i];
+    most = wave_max(fmaxf(low, high));
 #pragma unroll
     for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
     const int any = __any(bad);
-    if (lane == 0) ws.sums[unit] = SelectSum{sum, ref, most, any};
+    if (lane == 0) ws.sums[unit] = SelectSum{sum, ref, most, n, any};
 }
 
 // The largest fp32 value that is not above x.
@@ -297,6 +380,13 @@ struct JoinShared {
     int lists, held[kJoinWaves];
 };
 
+// The score of a beam whose row has this sum against `ref`, less the logarithm.  Whole
+// multiples of 2^-40: rows of the same logits tie, whatever their order and their
+// sums' last bits.
+__device__ __forceinline__ double base_of(double score, float ref, double sum, bool bad) {
+    return bad || !(ref < INFINITY) ? NAN : score - rint(((double)ref + log(sum)) * 0x1p40) * 0x1p-40;
+}
+
 // Joins the parts of a group's rows, by a block of kJoinWaves waves.  No list whose
 // largest logit gives less than the keep-th largest of the lists' is read.
 __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& ws, int group, JoinShared& s) {
@@ -305,26 +395,44 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
     const int lists = a.beams * a.segs;
     const SelectSum* sums = ws.sums + row0 * a.segs;
     const u64* keys = ws.keys + row0 * a.segs * a.keep;
-    for (int w = wave; w < a.beams; w += kJoinWaves) {
-        const double score = a.scores ? (double)a.scores[row0 + w] : 0.;
-        const bool over = a.ended && a.ended[row0 + w];
-        double to = NAN;
-        if (fabs(score) < INFINITY && !over) {
+    auto score_of = [&](int w) { return a.scores ? (double)a.scores[row0 + w] : 0.; };
+    auto over = [&](int w) { return a.ended && a.ended[row0 + w]; };
+    if (a.segs <= 16) {                     // a thread for each row, else a wave
+        for (int w = tid; w < a.beams; w += 64 * kJoinWaves) {
+            const double score = score_of(w);
+            const bool none = !(fabs(score) < INFINITY) || over(w);
             const SelectSum* p = sums + w * a.segs;
             float m = -INFINITY;
             bool bad = false;
-            for (int i = lane; i < a.segs; i += 64) {
-                m = fmaxf(m, p[i].ref);
-                bad |= p[i].bad != 0;
+            for (int i = 0; i < a.segs; ++i) {
+                m = none ? m : fmaxf(m, p[i].ref);
+                bad |= !none && p[i].bad;
             }
-            m = wave_max(m);
             double sum = 0;
-            for (int i = lane; i < a.segs; i += 64) sum += p[i].sum * weight((double)p[i].ref - (double)m);
-#pragma unroll
-            for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
-            if (!__any(bad) && m < INFINITY) to = score - ((double)m + log(sum));
+            for (int i = 0; i < a.segs; ++i) sum += none ? 0. : p[i].sum * weight((double)p[i].ref - (double)m);
+            s.base[w] = none ? NAN : base_of(score, m, sum, bad);
         }
-        if (lane == 0) s.base[w] = to;
+    } else {
+        for (int w = wave; w < a.beams; w += kJoinWaves) {
+            const double score = score_of(w);
+            double to = NAN;
+            if (fabs(score) < INFINITY && !over(w)) {
+                const SelectSum* p = sums + w * a.segs;
+                float m = -INFINITY;
+                bool bad = false;
+                for (int i = lane; i < a.segs; i += 64) {
+                    m = fmaxf(m, p[i].ref);
+                    bad |= p[i].bad != 0;
+                }
+                m = wave_max(m);
+                double sum = 0;
+                for (int i = lane; i < a.segs; i += 64) sum += p[i].sum * weight((double)p[i].ref - (double)m);
+#pragma unroll
+                for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
+                to = base_of(score, m, sum, __any(bad));
+            }
+            if (lane == 0) s.base[w] = to;
+        }
     }
     if (tid == 0) s.lists = 0;
     __syncthreads();
@@ -342,7 +450,7 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
         low = fmaxf(low, best_of(i, &in));
         if (i + 64 < lists) high = fmaxf(high, best_of(i + 64, &in));
     }
-    const float floor = kth_of_lanes(low, high, a.keep);
+    const float floor = lists < a.keep ? -INFINITY : kth_of_lanes<10>(low, high, a.keep);
     for (int i = tid; i < lists; i += 64 * kJoinWaves) {
         const float b = best_of(i, &in);
         if (in && b >= floor) s.list[atomicAdd(&s.lists, 1)] = (unsigned short)i;
@@ -353,11 +461,12 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
     int n = 0;
     Best least{};
     auto enter = [&](bool in, const Best& k) {
+        const u64 go = __ballot(in && above(k, least));
+        if (!go) return;
         if (n > kJoinRoom - 64) {
             least = keep_largest<kJoinRoom>(buf, n, a.keep);
             n = a.keep;
         }
-        const u64 go = __ballot(in && above(k, least));
         if (go >> lane & 1) buf[n + __popcll(go & ((1ull << lane) - 1))] = k;
         n += __popcll(go);
     };
@@ -369,19 +478,22 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
     const int count = s.lists;
-    for (int i0 = wave; i0 < count; i0 += 2 * kJoinWaves)
-        for (int j = lane; j - lane < a.keep; j += 64) {
-            u64 key[2];
-            int l[2];
+    for (int i0 = wave; i0 < count; i0 += 4 * kJoinWaves) {
+        int l[4], held[4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int i = i0 + u * kJoinWaves;
-                l[u] = __builtin_amdgcn_readfirstlane(i < count ? (int)s.list[i] : -1);
-                key[u] = l[u] >= 0 && j < a.keep ? keys[(int64_t)l[u] * a.keep + j] : 0;
-            }
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kJoinWaves;
+            l[u] = __builtin_amdgcn_readfirstlane(i < count ? (int)s.list[i] : 0);
+            held[u] = __builtin_amdgcn_readfirstlane(i < count ? sums[l[u]].n : 0);
+        }
+        for (int j0 = 0; j0 < a.keep; j0 += 64) {
+            const int j = j0 + lane;
+            u64 key[4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (l[u] < 0) continue;
+            for (int u = 0; u < 4; ++u) key[u] = j < held[u] ? keys[(int64_t)l[u] * a.keep + j] : 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (j0 >= held[u]) continue;
                 const int w = l[u] / a.segs;
                 const double score = s.base[w] + (double)unordered((unsigned)(key[u] >> 32)) + 0.;
                 const unsigned item = 0xffffffffu - (unsigned)key[u];
@@ -390,22 +502,32 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
                                                ((1u << kItemBits) - 1 - item)});
             }
         }
+    }
     if (a.ended && wave == 0)               // beams that ended carry themselves over
         for (int w0 = 0; w0 < a.beams; w0 += 64) {
             const int w = w0 + lane;
-            const bool over = w < a.beams && a.ended[row0 + w];
-            const double score = over && a.scores ? (double)a.scores[row0 + w] : 0.;
-            enter(over && fabs(score) < INFINITY, Best{ordered(score + 0.), (u64)(kMostBeams - 1 - w) << 57});
+            const bool carry = w < a.beams && over(w);
+            const double score = carry ? score_of(w) : 0.;
+            enter(carry && fabs(score) < INFINITY, Best{ordered(score + 0.), (u64)(kMostBeams - 1 - w) << 57});
         }
     settle();
     if (lane == 0) s.held[wave] = n;
     __syncthreads();
     if (wave != 0) return;
-    for (int o = 1; o < kJoinWaves; ++o)
-        for (int i0 = 0; i0 < s.held[o]; i0 += 64) {
-            const int i = i0 + lane;
-            enter(i < s.held[o], i < s.held[o] ? s.room[o][i] : Best{});
+    int first[kJoinWaves + 1] = {0, 0};     // of the other waves' candidates
+#pragma unroll
+    for (int o = 1; o < kJoinWaves; ++o) first[o + 1] = first[o] + s.held[o];
+    for (int i0 = 0; i0 < first[kJoinWaves]; i0 += 64) {
+        const int i = i0 + lane;
+        int o = 1, at = 0;
+#pragma unroll
+        for (int k = 2; k < kJoinWaves; ++k) {
+            o = i >= first[k] ? k : o;
+            at = i >= first[k] ? first[k] : at;
         }
+        const bool is = i < first[kJoinWaves];
+        enter(is, is ? s.room[o][i - at] : Best{});
+    }
     settle();
     // each one's place: how many are above it
     const int64_t out = (int64_t)group * a.keep;
@@ -417,21 +539,20 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
         }
         const Best k = buf[i];
         int place = 0;
+#pragma unroll 8
         for (int j = 0; j < n; ++j) place += above(buf[j], k) ? 1 : 0;
         const int w = kMostBeams - 1 - (int)(k.rest >> 57);
-        const bool over = a.ended && a.ended[row0 + w];
         a.out_scores[out + place] = (float)unordered(k.score);
         a.out_parents[out + place] = w;
-        a.out_items[out + place] = over ? a.end_item : (1 << kItemBits) - 1 - (int)(k.rest & ((1u << kItemBits) - 1));
+        a.out_items[out + place] = over(w) ? a.end_item : (1 << kItemBits) - 1 - (int)(k.rest & ((1u << kItemBits) - 1));
     }
 }
 
 template <typename T, bool MASKED>
-__global__ __launch_bounds__(256) void history_select_kernel(SelectArgs a, SelectWs ws) {
-    __shared__ u64 room[4][kSelectRoom];
+__global__ __launch_bounds__(64 * kSelectBlock, 4) void history_select_kernel(SelectArgs a, SelectWs ws) {
+    __shared__ SelectShared s;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
-    if (unit < (int64_t)a.batch * a.beams * a.segs) select_part<T, MASKED>(a, ws, unit, room[wave]);
+    select_part<T, MASKED>(a, ws, (int64_t)blockIdx.x * kSelectBlock + wave, s);
 }
 
 __global__ __launch_bounds__(64 * kJoinWaves) void history_select_join_kernel(SelectArgs a, SelectWs ws) {
@@ -439,35 +560,35 @@ __global__ __launch_bounds__(64 * kJoinWaves) void history_select_join_kernel(Se
     join_group(a, ws, blockIdx.x, s);
 }
 
-// Parts that a row is cut into: enough waves to fill the card, four tiles at least for each, and no more lists and
-// candidates than a block can join.
-static int segs_of(int64_t batch, int beams, int64_t items, int keep) {
-    const int64_t rows = batch * beams, tiles = (items + kSelectTile - 1) / kSelectTile;
+// Parts that a row is cut into: enough waves to fill the card, 2048 logits at least for each, and no more lists than
+// a block can join.  A power of two, or whole blocks, so that the waves of a block know each other's rows.
+static int segs_of(int64_t batch, int beams, int64_t items) {
+    const int64_t rows = batch * beams, least = (items + 2047) / 2048;
     int64_t s = (kSelectWaves + rows - 1) / rows;
-    s = s < (tiles + 3) / 4 ? s : (tiles + 3) / 4;
-    const int64_t most = kMostLists / beams;
-    s = s < most ? s : most;
-    return (int)(s < 1 ? 1 : s);
+    s = s < least ? s : least;
+    s = s < kMostLists / beams ? s : kMostLists / beams;
+    if (s >= kSelectBlock) return (int)(s / kSelectBlock * kSelectBlock);
+    return s >= 4 ? 4 : (s >= 2 ? 2 : 1);
 }
 
 static size_t sums_bytes(int64_t units) { return ((size_t)units * sizeof(SelectSum) + 255) / 256 * 256; }
 
 size_t select_workspace_bytes(int64_t batch, int beams, int64_t items, int keep) {
-    const int64_t units = batch * beams * segs_of(batch, beams, items, keep);
+    const int64_t units = batch * beams * segs_of(batch, beams, items);
     return sums_bytes(units) + (size_t)units * keep * sizeof(u64);
 }
 
 template <typename T>
 static void launch_select(const SelectArgs& a, const SelectWs& ws, int64_t blocks, hipStream_t s) {
-    if (a.allowed) hipLaunchKernelGGL((history_select_kernel<T, true>), dim3(blocks), dim3(256), 0, s, a, ws);
-    else hipLaunchKernelGGL((history_select_kernel<T, false>), dim3(blocks), dim3(256), 0, s, a, ws);
+    if (a.allowed) hipLaunchKernelGGL((history_select_kernel<T, true>), dim3(blocks), dim3(64 * kSelectBlock), 0, s, a, ws);
+    else hipLaunchKernelGGL((history_select_kernel<T, false>), dim3(blocks), dim3(64 * kSelectBlock), 0, s, a, ws);
 }
 
 hipError_t launch_history_select(const SelectArgs& args, int dtype, void* workspace, hipStream_t s) {
     SelectArgs a = args;
-    a.segs = segs_of(a.batch, a.beams, a.items, a.keep);
-    const int64_t units = (int64_t)a.batch * a.beams * a.segs, blocks = (units + 3) / 4;
-    if (!grid_fits(blocks, 256) || !grid_fits(a.batch, 64 * kJoinWaves)) return kTooLarge;
+    a.segs = segs_of(a.batch, a.beams, a.items);
+    const int64_t units = (int64_t)a.batch * a.beams * a.segs, blocks = (units + kSelectBlock - 1) / kSelectBlock;
+    if (!grid_fits(blocks, 64 * kSelectBlock) || !grid_fits(a.batch, 64 * kJoinWaves)) return kTooLarge;
     SelectWs ws;
     ws.sums = (SelectSum*)workspace;
     ws.keys = (u64*)((char*)workspace + sums_bytes(units));
