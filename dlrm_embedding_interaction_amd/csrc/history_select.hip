@@ -16,17 +16,18 @@ constexpr int kSelectHalf = 512;         // logits of half a tile in the 16-bit 
 constexpr int kSelectRoom = 512;         // candidates a wave has room for
 constexpr int kGroups = 16;              // groups of tiles in a wave's part
 constexpr int kSelectWaves = 4096;       // waves a launch aims at: sixteen on each CU
-constexpr int kSelectBlock = 8;          // waves of a block
-constexpr int kJoinWaves = 8;
-constexpr int kJoinRoom = 512;
-constexpr int kMostLists = 4096;         // parts of a group's rows
+constexpr int kBlockWaves = 8;
+constexpr int kMostSegs = 256;           // parts of a row, of all rows of a group
+constexpr int kMostLists = 4096;
+constexpr int kJoinRoom = 256;           // candidates a wave of the join has room for, and all of them together
+constexpr int kPool = 512;
 
 // What one wave leaves of its part of a row: the sum of exponentials against `ref`,
-// the largest logit, how many candidates it lists, and whether a NaN was among them.
-struct SelectSum {
+// the largest logit (NaN if one was among them), and how many candidates it lists.
+struct __attribute__((aligned(32))) SelectSum {
     double sum;
     float ref, top;
-    int n, bad;
+    int n, unused[3];
 };
 
 struct SelectWs {
@@ -156,23 +157,35 @@ __device__ __forceinline__ float kth_of_lanes(float a, float b, int keep) {
     return unordered(t > 0x007fffffu ? t : 0x007fffffu);        // below -inf there are only NaN
 }
 
-// e^d for d up to 600, to 2^-34 of its value; below -690 as if it were -690, which is
-// nothing against any sum that counts.  d log2 e is split into a whole number and a
-// rest of at most a half by adding and taking away 1.5 x 2^52; a polynomial of the
-// seventh degree, fitted to the least relative error, gives 2 to the rest.
-__device__ __forceinline__ double weight(double d) {
-    constexpr double L = 1.4426950408889634, SHIFT = 0x1.8p52;
-    d = fmax(d, -690.);
-    const double k = fma(d, L, SHIFT), f = fma(d, L, SHIFT - k);
-    double p = 0x1.fe17826c2a406p-17;
-    p = fma(p, f, 0x1.446a1fd688addp-13);
-    p = fma(p, f, 0x1.5d8a708988ddcp-10);
-    p = fma(p, f, 0x1.3b29dc40dc8a4p-7);
-    p = fma(p, f, 0x1.c6b08aaf2db33p-5);
-    p = fma(p, f, 0x1.ebfbe0a4be78ap-3);
-    p = fma(p, f, 0x1.62e42ff116296p-1);
-    p = fma(p, f, 0x1.ffffffffabbcdp-1);
+// Sums of exponentials are held as sum x 2^whole(ref).  ref is a multiple of 512, so
+// that it is 0 in ordinary rows and a logit adds the same wherever it stands; logits
+// beyond 2^20 (far) are taken less ref before the exponential, and sums stand against
+// e^ref.
+constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453;
+constexpr double kShift = 0x1.8p52;      // adding and taking away: a whole number
+__device__ __forceinline__ bool far(float ref) { return !(fabsf(ref) <= 0x1p20f); }
+__device__ __forceinline__ double whole(float ref) { return rint((double)ref * kLog2e); }
+
+// e^x 2^-w with shift = kShift - w, to 2^-29 of its value, where the result has an
+// exponent within double's.  x log2 e is split into a whole number and a rest of at most
+// a half; a polynomial of the sixth degree, fitted to the least relative error
+// (1.86e-9), gives 2 to the rest.
+__device__ __forceinline__ double power(double x, double shift) {
+    const double k = fma(x, kLog2e, shift), f = fma(x, kLog2e, shift - k);
+    double p = 0x1.41d332c59dceep-13;
+    p = fma(p, f, 0x1.5f456a892d64dp-10);
+    p = fma(p, f, 0x1.3b2dbbc1f415fp-7);
+    p = fma(p, f, 0x1.c6aed4b954ea2p-5);
+    p = fma(p, f, 0x1.ebfbdadcaf500p-3);
+    p = fma(p, f, 0x1.62e430c7e91f8p-1);
+    p = fma(p, f, 0x1.0000000261502p+0);
     return __hiloint2double(__double2hiint(p) + (__double2loint(k) << 20), __double2loint(p));
+}
+// What a sum against `from` has to be multiplied by to stand against `to`.
+__device__ __forceinline__ double moved(float from, float to) {
+    if (far(from) || far(to)) return power(fmax((double)from - (double)to, -690.), kShift);
+    const double d = fmax(whole(from) - whole(to), -1000.);
+    return __hiloint2double((1023 + (int)d) << 20, 0);
 }
 
 // Eight elements of a row at any alignment, and their bytes of a mask.
@@ -220,18 +233,18 @@ __device__ __forceinline__ void values_of(const Eight<T>& r, float* f) {
 
 // What the waves of a block leave for one another and for themselves.
 struct SelectShared {
-    u64 room[kSelectBlock][kSelectRoom];
-    float tops[kSelectBlock][kGroups][64];  // later the numbers of those that reach the floor
-    float found[kSelectBlock];
+    u64 room[kBlockWaves][kSelectRoom];
+    float tops[kBlockWaves][kGroups][64];  // later the numbers of those that reach the floor
+    float found[kBlockWaves];
 };
 
 // One wave's part of a row, every wave of the block taking part.
 //
 // The sum is taken against `ref`, which needs only be near the largest logit: 64 bits
-// hold e^300 times too much, so that no tile waits for a maximum over the wave.  It is
-// a multiple of 512, 0 in ordinary rows: a logit then adds the same wherever it
-// stands, and rows of the same logits in another order have sums that differ by their
-// additions' rounding alone (see the join).
+// hold e^300 times too much, so that no tile waits for a maximum over the wave, and
+// rows of the same logits in another order have sums that differ by their additions'
+// rounding alone (see the join).  Logits more than 690 below ref count as if they were
+// 690 below, which is nothing against any sum that counts.
 //
 // Of the logits themselves the pass over them keeps the largest of each group that a
 // lane sees.  Only logits that reach `floor` can be among the best: the keep-th largest
@@ -246,7 +259,7 @@ __device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs&
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int64_t row = unit / a.segs;
     const int seg = (int)(unit - row * a.segs);
-    const int sharing = a.segs < kSelectBlock ? a.segs : kSelectBlock, share = (a.keep + sharing - 1) / sharing;
+    const int sharing = a.segs < kBlockWaves ? a.segs : kBlockWaves, share = (a.keep + sharing - 1) / sharing;
     // of a row without continuations nothing is read, here or by the join
     const bool live = row < (int64_t)a.batch * a.beams && (!a.scores || fabsf(a.scores[row]) < INFINITY) &&
                       !(a.ended && a.ended[row]);
@@ -257,8 +270,8 @@ __device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs&
     const uint8_t* may = MASKED ? a.allowed + row * a.ld_allowed : nullptr;
 
     float ref = -3.4028235e38f, low = -INFINITY, high = -INFINITY, most = -INFINITY;
-    double sum = 0;
-    bool bad = false;
+    double sum[2] = {0., 0.}, least_x = -INFINITY, shift = kShift;
+    bool is_far = true;
     Eight<T> next[HALVES];
     if (t0 < t1)
 #pragma unroll
@@ -273,18 +286,16 @@ __device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs&
             values_of<T, MASKED>(next[h], f + 8 * h);
             if (t + 1 < t1) next[h] = load_eight<T, MASKED>(x, may, at + TILE + h * kSelectHalf, a.items);
         }
-        float l = f[0], h = f[E / 2];
-#pragma unroll
-        for (int i = 0; i < E; i += 2) bad |= __builtin_isunordered(f[i], f[i + 1]);
+        float l = f[0], h = f[E / 2];        // a NaN stays one
 #pragma unroll
         for (int i = 1; i < E / 2; ++i) {
-            l = fmaxf(l, f[i]);
-            h = fmaxf(h, f[E / 2 + i]);
+            l = __builtin_elementwise_maximum(l, f[i]);
+            h = __builtin_elementwise_maximum(h, f[E / 2 + i]);
         }
-        low = fmaxf(low, l);
-        high = fmaxf(high, h);
-        const float top = fmaxf(l, h);
-        most = fmaxf(most, top);
+        low = __builtin_elementwise_maximum(low, l);
+        high = __builtin_elementwise_maximum(high, h);
+        const float top = __builtin_elementwise_maximum(l, h);
+        most = __builtin_elementwise_maximum(most, top);
         if (--left == 0 || t + 1 == t1) {
             s.tops[wave][groups++][lane] = most;
             most = -INFINITY;
@@ -292,20 +303,30 @@ __device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs&
         }
         if (__builtin_expect(__any(top > ref + 300.f), 0)) {
             const float to = 512.f * rintf(wave_max(top) / 512.f);
-            sum *= weight((double)ref - (double)to);
+            const double by = moved(ref, to);
+            sum[0] *= by;
+            sum[1] *= by;
             ref = to;
+            is_far = far(ref);
+            least_x = (double)ref - 690.;
+            shift = kShift - whole(ref);
         }
+        if (__builtin_expect(is_far, 0)) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) sum += weight((double)f[i] - (double)ref);
+            for (int i = 0; i < E; ++i) sum[0] += power(fmax((double)f[i] - (double)ref, -690.), kShift);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) sum[i & 1] += power(fmax((double)f[i], least_x), shift);
+        }
     }
     float floor = kth_of_lanes<LOW>(low, high, a.keep);
     if (sharing > 1) {
         const float own = kth_of_lanes<LOW>(low, high, share);
         if (lane == 0) s.found[wave] = own;
         __syncthreads();
-        float all = INFINITY;
-        for (int i = 0; i < sharing; ++i) all = fminf(all, s.found[wave / sharing * sharing + i]);
-        floor = fmaxf(floor, all);
+        float every = INFINITY;
+        for (int i = 0; i < sharing; ++i) every = fminf(every, s.found[wave / sharing * sharing + i]);
+        floor = fmaxf(floor, every);
     }
     if (!live) return;
 
@@ -335,7 +356,12 @@ __device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs&
 #pragma unroll 1
             for (int h = 0; h < HALVES; ++h) {
                 float f[8];
-                values_of<T, MASKED>(HALVES == 2 && h ? raw[HALVES - 1] : raw[0], f);
+                Eight<T> one = raw[0];
+                if (HALVES == 2 && h) {
+                    one.w = raw[HALVES - 1].w;
+                    one.may = raw[HALVES - 1].may;
+                }
+                values_of<T, MASKED>(one, f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const u64 key = (u64)ordered(f[i] + 0.f) << 32 | (0xffffffffu - (unsigned)(at + h * kSelectHalf + i));
@@ -358,11 +384,13 @@ __device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs&
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     u64* keys = ws.keys + unit * a.keep;
     for (int i = lane; i < n; i += 64) keys[i] = buf[i];
-    most = wave_max(fmaxf(low, high));
+    most = __builtin_elementwise_maximum(low, high);
+    const bool bad = __any(most != most);
+    most = wave_max(most);
+    double all = sum[0] + sum[1];
 #pragma unroll
-    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
-    const int any = __any(bad);
-    if (lane == 0) ws.sums[unit] = SelectSum{sum, ref, most, n, any};
+    for (int d = 32; d; d >>= 1) all += __shfl_xor(all, d, 64);
+    if (lane == 0) ws.sums[unit] = SelectSum{all, ref, bad ? NAN : most, n, {}};
 }
 
 // The largest fp32 value that is not above x.
@@ -375,20 +403,20 @@ __device__ __forceinline__ float round_down(double x) {
 
 struct JoinShared {
     double base[kMostBeams];                // score - log of the sum; NaN: the beam gives no candidates
-    Best room[kJoinWaves][kJoinRoom];
+    Best room[kBlockWaves][kJoinRoom], pool[kPool];
+    double part_sum[kMostLists / 8 + kMostBeams];
+    float part_ref[kMostLists / 8 + kMostBeams], part_top[kMostLists / 8 + kMostBeams];
+    float best[kMostLists];                 // the best score of a list, rounded down
+    unsigned char held[kMostLists];         // its candidates
     unsigned short list[kMostLists];        // the lists that may hold one of the best
-    int lists, held[kJoinWaves];
+    int place[kPool];
+    int lists, count[kBlockWaves];
+    float found[kBlockWaves];
 };
 
-// The score of a beam whose row has this sum against `ref`, less the logarithm.  Whole
-// multiples of 2^-40: rows of the same logits tie, whatever their order and their
-// sums' last bits.
-__device__ __forceinline__ double base_of(double score, float ref, double sum, bool bad) {
-    return bad || !(ref < INFINITY) ? NAN : score - rint(((double)ref + log(sum)) * 0x1p40) * 0x1p-40;
-}
-
-// Joins the parts of a group's rows, by a block of kJoinWaves waves.  No list whose
-// largest logit gives less than the keep-th largest of the lists' is read.
+// Joins the parts of a group's rows, by a block.  No list whose largest logit gives
+// less than the keep-th largest of the lists' is read, and no candidate taken further
+// that is below what the waves find together.
 __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& ws, int group, JoinShared& s) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t row0 = (int64_t)group * a.beams;
@@ -397,64 +425,64 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
     const u64* keys = ws.keys + row0 * a.segs * a.keep;
     auto score_of = [&](int w) { return a.scores ? (double)a.scores[row0 + w] : 0.; };
     auto over = [&](int w) { return a.ended && a.ended[row0 + w]; };
-    if (a.segs <= 16) {                     // a thread for each row, else a wave
-        for (int w = tid; w < a.beams; w += 64 * kJoinWaves) {
-            const double score = score_of(w);
-            const bool none = !(fabs(score) < INFINITY) || over(w);
-            const SelectSum* p = sums + w * a.segs;
-            float m = -INFINITY;
-            bool bad = false;
-            for (int i = 0; i < a.segs; ++i) {
-                m = none ? m : fmaxf(m, p[i].ref);
-                bad |= !none && p[i].bad;
-            }
-            double sum = 0;
-            for (int i = 0; i < a.segs; ++i) sum += none ? 0. : p[i].sum * weight((double)p[i].ref - (double)m);
-            s.base[w] = none ? NAN : base_of(score, m, sum, bad);
+    // a thread for each list: the sums of up to eight neighbours of a row
+    const int near = a.segs < 8 ? a.segs : 8, parts = a.segs / near;
+    for (int i = tid; i - lane < lists; i += 64 * kBlockWaves) {
+        SelectSum p = {0., -3.4028235e38f, -INFINITY, 0, {}};
+        if (i < lists) p = sums[i];         // of a row that was not read: anything
+        float ref = p.ref, top = p.top;
+        for (int d = 1; d < near; d <<= 1) {
+            ref = fmaxf(ref, __shfl_xor(ref, d, 64));
+            top = __builtin_elementwise_maximum(top, __shfl_xor(top, d, 64));
         }
-    } else {
-        for (int w = wave; w < a.beams; w += kJoinWaves) {
-            const double score = score_of(w);
-            double to = NAN;
-            if (fabs(score) < INFINITY && !over(w)) {
-                const SelectSum* p = sums + w * a.segs;
-                float m = -INFINITY;
-                bool bad = false;
-                for (int i = lane; i < a.segs; i += 64) {
-                    m = fmaxf(m, p[i].ref);
-                    bad |= p[i].bad != 0;
-                }
-                m = wave_max(m);
-                double sum = 0;
-                for (int i = lane; i < a.segs; i += 64) sum += p[i].sum * weight((double)p[i].ref - (double)m);
-#pragma unroll
-                for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
-                to = base_of(score, m, sum, __any(bad));
+        double sum = p.sum * moved(p.ref, ref);
+        for (int d = 1; d < near; d <<= 1) sum += __shfl_xor(sum, d, 64);
+        if (i < lists) {
+            s.best[i] = p.top;
+            s.held[i] = (unsigned char)p.n;
+            if (i % near == 0) {
+                s.part_sum[i / near] = sum;
+                s.part_ref[i / near] = ref;
+                s.part_top[i / near] = top;
             }
-            if (lane == 0) s.base[w] = to;
         }
     }
     if (tid == 0) s.lists = 0;
     __syncthreads();
-
-    // the best score of list i, rounded down, and whether it has one
-    auto best_of = [&](int i, bool* in) {
-        const double b = s.base[i / a.segs];
-        const float top = b == b ? sums[i].top : -INFINITY;
-        *in = top > -INFINITY;
-        return *in ? round_down(b + (double)top) : -INFINITY;
-    };
-    bool in;
+    for (int w = tid; w < a.beams; w += 64 * kBlockWaves) {
+        const double score = score_of(w);
+        double to = NAN;
+        if (fabs(score) < INFINITY && !over(w)) {
+            float ref = s.part_ref[w * parts], top = s.part_top[w * parts];
+            for (int i = 1; i < parts; ++i) {
+                ref = fmaxf(ref, s.part_ref[w * parts + i]);
+                top = __builtin_elementwise_maximum(top, s.part_top[w * parts + i]);
+            }
+            double sum = 0;
+            for (int i = 0; i < parts; ++i) sum += s.part_sum[w * parts + i] * moved(s.part_ref[w * parts + i], ref);
+            // The logarithm in whole multiples of 2^-40: rows of the same logits tie, whatever their order and their
+            // sums' last bits.
+            const double l = (far(ref) ? (double)ref : whole(ref) * kLn2) + log(sum);
+            if (top < INFINITY) to = score - rint(l * 0x1p40) * 0x1p-40;
+        }
+        s.base[w] = to;
+    }
+    __syncthreads();
+    for (int i = tid; i < lists; i += 64 * kBlockWaves) {
+        const double b = s.base[(unsigned)i / (unsigned)a.segs];
+        const bool in = b == b && s.best[i] > -INFINITY;
+        s.best[i] = in ? round_down(b + (double)s.best[i]) : -INFINITY;
+        if (!in) s.held[i] = 0;
+    }
+    __syncthreads();
     float low = -INFINITY, high = -INFINITY;
     for (int i = lane; i < lists; i += 128) {
-        low = fmaxf(low, best_of(i, &in));
-        if (i + 64 < lists) high = fmaxf(high, best_of(i + 64, &in));
+        low = fmaxf(low, s.best[i]);
+        if (i + 64 < lists) high = fmaxf(high, s.best[i + 64]);
     }
-    const float floor = lists < a.keep ? -INFINITY : kth_of_lanes<10>(low, high, a.keep);
-    for (int i = tid; i < lists; i += 64 * kJoinWaves) {
-        const float b = best_of(i, &in);
-        if (in && b >= floor) s.list[atomicAdd(&s.lists, 1)] = (unsigned short)i;
-    }
+    float floor = lists < a.keep ? -INFINITY : kth_of_lanes<10>(low, high, a.keep);
+    for (int i = tid; i < lists; i += 64 * kBlockWaves)
+        if (s.held[i] && s.best[i] >= floor) s.list[atomicAdd(&s.lists, 1)] = (unsigned short)i;
     __syncthreads();
 
     Best* buf = s.room[wave];
@@ -470,21 +498,14 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
         if (go >> lane & 1) buf[n + __popcll(go & ((1ull << lane) - 1))] = k;
         n += __popcll(go);
     };
-    auto settle = [&] {
-        if (n > a.keep) {
-            least = keep_largest<kJoinRoom>(buf, n, a.keep);
-            n = a.keep;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    };
     const int count = s.lists;
-    for (int i0 = wave; i0 < count; i0 += 4 * kJoinWaves) {
+    for (int i0 = wave; i0 < count; i0 += 4 * kBlockWaves) {
         int l[4], held[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * kJoinWaves;
+            const int i = i0 + u * kBlockWaves;
             l[u] = __builtin_amdgcn_readfirstlane(i < count ? (int)s.list[i] : 0);
-            held[u] = __builtin_amdgcn_readfirstlane(i < count ? sums[l[u]].n : 0);
+            held[u] = __builtin_amdgcn_readfirstlane(i < count ? (int)s.held[l[u]] : 0);
         }
         for (int j0 = 0; j0 < a.keep; j0 += 64) {
             const int j = j0 + lane;
@@ -510,64 +531,99 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
             const double score = carry ? score_of(w) : 0.;
             enter(carry && fabs(score) < INFINITY, Best{ordered(score + 0.), (u64)(kMostBeams - 1 - w) << 57});
         }
-    settle();
-    if (lane == 0) s.held[wave] = n;
-    __syncthreads();
-    if (wave != 0) return;
-    int first[kJoinWaves + 1] = {0, 0};     // of the other waves' candidates
-#pragma unroll
-    for (int o = 1; o < kJoinWaves; ++o) first[o + 1] = first[o] + s.held[o];
-    for (int i0 = 0; i0 < first[kJoinWaves]; i0 += 64) {
-        const int i = i0 + lane;
-        int o = 1, at = 0;
-#pragma unroll
-        for (int k = 2; k < kJoinWaves; ++k) {
-            o = i >= first[k] ? k : o;
-            at = i >= first[k] ? first[k] : at;
-        }
-        const bool is = i < first[kJoinWaves];
-        enter(is, is ? s.room[o][i - at] : Best{});
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // what every wave has keep / kBlockWaves of
+    const int share = (a.keep + kBlockWaves - 1) / kBlockWaves;
+    {
+        const float x = lane < n ? round_down(unordered(buf[lane].score)) : -INFINITY;
+        const float y = lane + 64 < n ? round_down(unordered(buf[lane + 64].score)) : -INFINITY;
+        const float own = kth_of_lanes<10>(x, y, share);
+        if (lane == 0) s.found[wave] = own;
     }
-    settle();
-    // each one's place: how many are above it
-    const int64_t out = (int64_t)group * a.keep;
-    for (int i = lane; i < a.keep; i += 64) {
-        if (i >= n) {
-            a.out_scores[out + i] = -INFINITY;
-            a.out_parents[out + i] = a.out_items[out + i] = -1;
-            continue;
-        }
-        const Best k = buf[i];
+    __syncthreads();
+    floor = s.found[0];
+#pragma unroll
+    for (int o = 1; o < kBlockWaves; ++o) floor = fminf(floor, s.found[o]);
+    int m = 0;                              // that reach it, moved to the front
+    for (int i0 = 0; i0 < n; i0 += 64) {
+        const Best k = i0 + lane < n ? buf[i0 + lane] : Best{};
+        const u64 go = __ballot(i0 + lane < n && unordered(k.score) >= (double)floor);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (go >> lane & 1) buf[m + __popcll(go & ((1ull << lane) - 1))] = k;
+        m += __popcll(go);
+    }
+    n = m;
+    if (lane == 0) s.count[wave] = n;
+    __syncthreads();
+    int first = 0, all = 0;
+#pragma unroll
+    for (int o = 0; o < kBlockWaves; ++o) {
+        first += o < wave ? s.count[o] : 0;
+        all += s.count[o];
+    }
+    if (all <= kPool) {
+        for (int i = lane; i < n; i += 64) s.pool[first + i] = buf[i];
+    } else if (wave == 0) {                 // many equal ones: the best of two waves at a time
+        for (int o = 1; o < kBlockWaves; ++o)
+            for (int i0 = 0; i0 < s.count[o]; i0 += 64) {
+                const int i = i0 + lane;
+                enter(i < s.count[o], i < s.count[o] ? s.room[o][i] : Best{});
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int i = lane; i < n; i += 64) s.pool[i] = buf[i];
+        if (lane == 0) s.count[0] = n;
+    }
+    for (int i = tid; i < kPool; i += 64 * kBlockWaves) s.place[i] = 0;
+    __syncthreads();
+    n = all <= kPool ? all : s.count[0];
+    // each one's place: how many are above it, counted by `split` threads
+    const int split = max(64 * kBlockWaves / max(n, 1), 1);
+    for (int i = tid; i < n * split; i += 64 * kBlockWaves) {
+        const int c = i / split, part = i % split;
+        const Best k = s.pool[c];
         int place = 0;
-#pragma unroll 8
-        for (int j = 0; j < n; ++j) place += above(buf[j], k) ? 1 : 0;
+#pragma unroll 4
+        for (int j = part; j < n; j += split) place += above(s.pool[j], k) ? 1 : 0;
+        atomicAdd(&s.place[c], place);
+    }
+    __syncthreads();
+    const int64_t out = (int64_t)group * a.keep;
+    for (int i = tid; i < n; i += 64 * kBlockWaves) {
+        const int place = s.place[i];
+        if (place >= a.keep) continue;
+        const Best k = s.pool[i];
         const int w = kMostBeams - 1 - (int)(k.rest >> 57);
         a.out_scores[out + place] = (float)unordered(k.score);
         a.out_parents[out + place] = w;
         a.out_items[out + place] = over(w) ? a.end_item : (1 << kItemBits) - 1 - (int)(k.rest & ((1u << kItemBits) - 1));
     }
+    for (int i = n + tid; i < a.keep; i += 64 * kBlockWaves) {
+        a.out_scores[out + i] = -INFINITY;
+        a.out_parents[out + i] = a.out_items[out + i] = -1;
+    }
 }
 
 template <typename T, bool MASKED>
-__global__ __launch_bounds__(64 * kSelectBlock, 4) void history_select_kernel(SelectArgs a, SelectWs ws) {
+__global__ __launch_bounds__(64 * kBlockWaves, 4) void history_select_kernel(SelectArgs a, SelectWs ws) {
     __shared__ SelectShared s;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    select_part<T, MASKED>(a, ws, (int64_t)blockIdx.x * kSelectBlock + wave, s);
+    select_part<T, MASKED>(a, ws, (int64_t)blockIdx.x * kBlockWaves + wave, s);
 }
 
-__global__ __launch_bounds__(64 * kJoinWaves) void history_select_join_kernel(SelectArgs a, SelectWs ws) {
+__global__ __launch_bounds__(64 * kBlockWaves) void history_select_join_kernel(SelectArgs a, SelectWs ws) {
     __shared__ JoinShared s;
     join_group(a, ws, blockIdx.x, s);
 }
 
-// Parts that a row is cut into: enough waves to fill the card, 2048 logits at least for each, and no more lists than
-// a block can join.  A power of two, or whole blocks, so that the waves of a block know each other's rows.
+// Parts that a row is cut into: enough waves to fill the card, 2048 logits at least for each.  A power of two, or whole
+// blocks, so that the waves of a block know each other's rows.
 static int segs_of(int64_t batch, int beams, int64_t items) {
     const int64_t rows = batch * beams, least = (items + 2047) / 2048;
     int64_t s = (kSelectWaves + rows - 1) / rows;
     s = s < least ? s : least;
+    s = s < kMostSegs ? s : kMostSegs;
     s = s < kMostLists / beams ? s : kMostLists / beams;
-    if (s >= kSelectBlock) return (int)(s / kSelectBlock * kSelectBlock);
+    if (s >= kBlockWaves) return (int)(s / kBlockWaves * kBlockWaves);
     return s >= 4 ? 4 : (s >= 2 ? 2 : 1);
 }
 
@@ -580,15 +636,15 @@ size_t select_workspace_bytes(int64_t batch, int beams, int64_t items, int keep)
 
 template <typename T>
 static void launch_select(const SelectArgs& a, const SelectWs& ws, int64_t blocks, hipStream_t s) {
-    if (a.allowed) hipLaunchKernelGGL((history_select_kernel<T, true>), dim3(blocks), dim3(64 * kSelectBlock), 0, s, a, ws);
-    else hipLaunchKernelGGL((history_select_kernel<T, false>), dim3(blocks), dim3(64 * kSelectBlock), 0, s, a, ws);
+    if (a.allowed) hipLaunchKernelGGL((history_select_kernel<T, true>), dim3(blocks), dim3(64 * kBlockWaves), 0, s, a, ws);
+    else hipLaunchKernelGGL((history_select_kernel<T, false>), dim3(blocks), dim3(64 * kBlockWaves), 0, s, a, ws);
 }
 
 hipError_t launch_history_select(const SelectArgs& args, int dtype, void* workspace, hipStream_t s) {
     SelectArgs a = args;
     a.segs = segs_of(a.batch, a.beams, a.items);
-    const int64_t units = (int64_t)a.batch * a.beams * a.segs, blocks = (units + kSelectBlock - 1) / kSelectBlock;
-    if (!grid_fits(blocks, 64 * kSelectBlock) || !grid_fits(a.batch, 64 * kJoinWaves)) return kTooLarge;
+    const int64_t units = (int64_t)a.batch * a.beams * a.segs, blocks = (units + kBlockWaves - 1) / kBlockWaves;
+    if (!grid_fits(blocks, 64 * kBlockWaves) || !grid_fits(a.batch, 64 * kBlockWaves)) return kTooLarge;
     SelectWs ws;
     ws.sums = (SelectSum*)workspace;
     ws.keys = (u64*)((char*)workspace + sums_bytes(units));
@@ -597,7 +653,7 @@ hipError_t launch_history_select(const SelectArgs& args, int dtype, void* worksp
     else launch_select<f16>(a, ws, blocks, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(history_select_join_kernel, dim3(a.batch), dim3(64 * kJoinWaves), 0, s, a, ws);
+    hipLaunchKernelGGL(history_select_join_kernel, dim3(a.batch), dim3(64 * kBlockWaves), 0, s, a, ws);
     return hipGetLastError();
 }
 
