@@ -17,6 +17,10 @@ constexpr int kSelectRoom = 512;         // candidates a wave has room for
 constexpr int kGroups = 16;              // groups of tiles in a wave's part
 constexpr int kSelectWaves = 4096;       // waves a launch aims at: sixteen on each CU
 constexpr int kBlockWaves = 8;
+// Groups of few logits, one part of a row for each wave of a block, and not more groups than CUs, take one launch.  4
+// beams of 500 to 5000 items, fp32: 64 groups 12.3 to 16.3 us, in two launches 13.9 to 17.3; 512 groups 22.4 to 32.1
+// against 21.2 to 28.9.  Blocks whose waves take several parts lose: 4 groups of 32000 logits 23.3, in two launches 17.5.
+constexpr int kOneLogits = 20480, kOneGroups = 256;
 constexpr int kMostSegs = 256;           // parts of a row, of all rows of a group
 constexpr int kMostLists = 4096;
 constexpr int kJoinRoom = 256;           // candidates a wave of the join has room for, and all of them together
@@ -143,18 +147,27 @@ __device__ __forceinline__ K keep_largest(K* buf, int n, int keep) {
     return n <= 128 ? keep_among<128>(buf, n, keep) : keep_among<ROOM>(buf, n, keep);
 }
 
-// The keep-th largest of two values per lane, 1 <= keep <= 128, or a little less: its
-// bits from LOW on.
-template <int LOW>
-__device__ __forceinline__ float kth_of_lanes(float a, float b, int keep) {
+// The keep-th largest of two values per lane, 1 <= keep <= 128, or less than that by
+// less than 2^-7 of it: the upper half of its bits, two at a time (each step waits some
+// 200 cycles for its counts).  ORDERS of them at once, for different `keep`.
+template <int ORDERS>
+__device__ __forceinline__ void kth_of_lanes(float a, float b, const int (&keep)[ORDERS], float (&r)[ORDERS]) {
     const unsigned x = ordered(a + 0.f), y = ordered(b + 0.f);
-    unsigned t = 0;
-    for (unsigned bit = 0x80000000u; bit >> LOW; bit >>= 1) {
-        const int count = __popcll(__ballot(x >= (t | bit))) + __popcll(__ballot(y >= (t | bit)));
-        if (count >= keep) t |= bit;
-        if (count == keep) break;
-    }
-    return unordered(t > 0x007fffffu ? t : 0x007fffffu);        // below -inf there are only NaN
+    unsigned t[ORDERS] = {};
+#pragma unroll
+    for (int at = 30; at >= 16; at -= 2)
+#pragma unroll
+        for (int k = 0; k < ORDERS; ++k) {
+            unsigned digit = 0;
+#pragma unroll
+            for (unsigned d = 1; d < 4; ++d) {
+                const unsigned c = t[k] | d << at;
+                digit += __popcll(__ballot(x >= c)) + __popcll(__ballot(y >= c)) >= keep[k] ? 1u : 0u;
+            }
+            t[k] |= digit << at;
+        }
+#pragma unroll
+    for (int k = 0; k < ORDERS; ++k) r[k] = unordered(t[k] > 0x007fffffu ? t[k] : 0x007fffffu);   // below -inf: NaN
 }
 
 // Sums of exponentials are held as sum x 2^whole(ref).  ref is a multiple of 512, so
@@ -226,7 +239,9 @@ __device__ __forceinline__ void values_of(const Eight<T>& r, float* f) {
     const Elements e = __builtin_bit_cast(Elements, r.w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        f[i] = (float)e.x[i];
+        // bf16 by its bits: a conversion lets the compiler take maxima in bf16, rounding each again
+        if constexpr (__is_same(T, bf16)) f[i] = __uint_as_float(i & 1 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
+        else f[i] = (float)e.x[i];
         if constexpr (MASKED) f[i] = ((i < 4 ? r.may.x : r.may.y) >> (8 * (i & 3)) & 0xffu) ? f[i] : -INFINITY;
     }
 }
@@ -255,28 +270,29 @@ struct SelectShared {
 template <typename T, bool MASKED>
 __device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs& ws, int64_t unit, SelectShared& s) {
     constexpr int HALVES = sizeof(T) == 2 ? 2 : 1, E = 8 * HALVES, TILE = kSelectHalf * HALVES;
-    constexpr int LOW = __is_same(T, bf16) ? 16 : (__is_same(T, f16) ? 13 : 10);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int64_t row = unit / a.segs;
     const int seg = (int)(unit - row * a.segs);
     const int sharing = a.segs < kBlockWaves ? a.segs : kBlockWaves, share = (a.keep + sharing - 1) / sharing;
-    // of a row without continuations nothing is read, here or by the join
-    const bool live = row < (int64_t)a.batch * a.beams && (!a.scores || fabsf(a.scores[row]) < INFINITY) &&
-                      !(a.ended && a.ended[row]);
+    const bool mine = unit >= 0 && row < (int64_t)a.batch * a.beams;
     const int tiles = (a.items + TILE - 1) / TILE;
-    const int t0 = (int)((int64_t)tiles * seg / a.segs), t1 = live ? (int)((int64_t)tiles * (seg + 1) / a.segs) : t0;
-    const int group = (t1 - t0 + kGroups - 1) / kGroups;        // tiles
+    const int t0 = (int)((int64_t)tiles * seg / a.segs);
+    int t1 = (int)((int64_t)tiles * (seg + 1) / a.segs);
     const T* x = (const T*)a.logits + row * a.ld_logits;
     const uint8_t* may = MASKED ? a.allowed + row * a.ld_allowed : nullptr;
+    Eight<T> next[HALVES];                  // on its way while the row's score is
+    if (mine && t0 < t1)
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+            next[h] = load_eight<T, MASKED>(x, may, t0 * TILE + h * kSelectHalf + lane * 8, a.items);
+    // of a row without continuations nothing else is read, here or by the join
+    const bool live = mine && (!a.scores || fabsf(a.scores[row]) < INFINITY) && !(a.ended && a.ended[row]);
+    if (!live) t1 = t0;
+    const int group = (t1 - t0 + kGroups - 1) / kGroups;        // tiles
 
     float ref = -3.4028235e38f, low = -INFINITY, high = -INFINITY, most = -INFINITY;
     double sum[2] = {0., 0.}, least_x = -INFINITY, shift = kShift;
     bool is_far = true;
-    Eight<T> next[HALVES];
-    if (t0 < t1)
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h)
-            next[h] = load_eight<T, MASKED>(x, may, t0 * TILE + h * kSelectHalf + lane * 8, a.items);
     int groups = 0, left = group;
     for (int t = t0; t < t1; ++t) {
         const int at = t * TILE + lane * 8;
@@ -319,10 +335,11 @@ __device__ __forceinline__ void select_part(const SelectArgs& a, const SelectWs&
             for (int i = 0; i < E; ++i) sum[i & 1] += power(fmax((double)f[i], least_x), shift);
         }
     }
-    float floor = kth_of_lanes<LOW>(low, high, a.keep);
+    float kth[2];
+    kth_of_lanes(low, high, {a.keep, share}, kth);
+    float floor = kth[0];
     if (sharing > 1) {
-        const float own = kth_of_lanes<LOW>(low, high, share);
-        if (lane == 0) s.found[wave] = own;
+        if (lane == 0) s.found[wave] = kth[1];
         __syncthreads();
         float every = INFINITY;
         for (int i = 0; i < sharing; ++i) every = fminf(every, s.found[wave / sharing * sharing + i]);
@@ -449,6 +466,7 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
     }
     if (tid == 0) s.lists = 0;
     __syncthreads();
+    const bool few = lists * a.keep <= 128;      // none is left out before they are ordered
     for (int w = tid; w < a.beams; w += 64 * kBlockWaves) {
         const double score = score_of(w);
         double to = NAN;
@@ -475,12 +493,17 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
         if (!in) s.held[i] = 0;
     }
     __syncthreads();
-    float low = -INFINITY, high = -INFINITY;
-    for (int i = lane; i < lists; i += 128) {
-        low = fmaxf(low, s.best[i]);
-        if (i + 64 < lists) high = fmaxf(high, s.best[i + 64]);
+    float floor = -INFINITY;
+    if (!few && lists >= a.keep) {
+        float low = -INFINITY, high = -INFINITY;
+        for (int i = lane; i < lists; i += 128) {
+            low = fmaxf(low, s.best[i]);
+            if (i + 64 < lists) high = fmaxf(high, s.best[i + 64]);
+        }
+        float kth[1];
+        kth_of_lanes(low, high, {a.keep}, kth);
+        floor = kth[0];
     }
-    float floor = lists < a.keep ? -INFINITY : kth_of_lanes<10>(low, high, a.keep);
     for (int i = tid; i < lists; i += 64 * kBlockWaves)
         if (s.held[i] && s.best[i] >= floor) s.list[atomicAdd(&s.lists, 1)] = (unsigned short)i;
     __syncthreads();
@@ -532,27 +555,26 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
             enter(carry && fabs(score) < INFINITY, Best{ordered(score + 0.), (u64)(kMostBeams - 1 - w) << 57});
         }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    // what every wave has keep / kBlockWaves of
-    const int share = (a.keep + kBlockWaves - 1) / kBlockWaves;
-    {
+    if (!few) {                             // what every wave has keep / kBlockWaves of
         const float x = lane < n ? round_down(unordered(buf[lane].score)) : -INFINITY;
         const float y = lane + 64 < n ? round_down(unordered(buf[lane + 64].score)) : -INFINITY;
-        const float own = kth_of_lanes<10>(x, y, share);
-        if (lane == 0) s.found[wave] = own;
-    }
-    __syncthreads();
-    floor = s.found[0];
+        float own[1];
+        kth_of_lanes(x, y, {(a.keep + kBlockWaves - 1) / kBlockWaves}, own);
+        if (lane == 0) s.found[wave] = own[0];
+        __syncthreads();
+        floor = s.found[0];
 #pragma unroll
-    for (int o = 1; o < kBlockWaves; ++o) floor = fminf(floor, s.found[o]);
-    int m = 0;                              // that reach it, moved to the front
-    for (int i0 = 0; i0 < n; i0 += 64) {
-        const Best k = i0 + lane < n ? buf[i0 + lane] : Best{};
-        const u64 go = __ballot(i0 + lane < n && unordered(k.score) >= (double)floor);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (go >> lane & 1) buf[m + __popcll(go & ((1ull << lane) - 1))] = k;
-        m += __popcll(go);
+        for (int o = 1; o < kBlockWaves; ++o) floor = fminf(floor, s.found[o]);
+        int m = 0;                          // that reach it, moved to the front
+        for (int i0 = 0; i0 < n; i0 += 64) {
+            const Best k = i0 + lane < n ? buf[i0 + lane] : Best{};
+            const u64 go = __ballot(i0 + lane < n && unordered(k.score) >= (double)floor);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (go >> lane & 1) buf[m + __popcll(go & ((1ull << lane) - 1))] = k;
+            m += __popcll(go);
+        }
+        n = m;
     }
-    n = m;
     if (lane == 0) s.count[wave] = n;
     __syncthreads();
     int first = 0, all = 0;
@@ -615,6 +637,21 @@ __global__ __launch_bounds__(64 * kBlockWaves) void history_select_join_kernel(S
     join_group(a, ws, blockIdx.x, s);
 }
 
+// Both steps in one launch, a block per group.
+template <typename T, bool MASKED>
+__global__ __launch_bounds__(64 * kBlockWaves) void history_select_one_kernel(SelectArgs a, SelectWs ws) {
+    __shared__ union Both {
+        SelectShared part;
+        JoinShared join;
+        __device__ Both() {}
+    } s;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), units = a.beams * a.segs;
+    select_part<T, MASKED>(a, ws, wave < units ? (int64_t)blockIdx.x * units + wave : -1, s.part);
+    __threadfence_block();                  // the sums and keys are read by other waves of the block
+    __syncthreads();
+    join_group(a, ws, blockIdx.x, s.join);
+}
+
 // Parts that a row is cut into: enough waves to fill the card, 2048 logits at least for each.  A power of two, or whole
 // blocks, so that the waves of a block know each other's rows.
 static int segs_of(int64_t batch, int beams, int64_t items) {
@@ -634,8 +671,17 @@ size_t select_workspace_bytes(int64_t batch, int beams, int64_t items, int keep)
     return sums_bytes(units) + (size_t)units * keep * sizeof(u64);
 }
 
+static bool in_one_launch(const SelectArgs& a) {
+    return a.beams * a.segs <= kBlockWaves && (int64_t)a.beams * a.items <= kOneLogits && a.batch <= kOneGroups;
+}
+
 template <typename T>
 static void launch_select(const SelectArgs& a, const SelectWs& ws, int64_t blocks, hipStream_t s) {
+    if (in_one_launch(a)) {
+        if (a.allowed) hipLaunchKernelGGL((history_select_one_kernel<T, true>), dim3(a.batch), dim3(64 * kBlockWaves), 0, s, a, ws);
+        else hipLaunchKernelGGL((history_select_one_kernel<T, false>), dim3(a.batch), dim3(64 * kBlockWaves), 0, s, a, ws);
+        return;
+    }
     if (a.allowed) hipLaunchKernelGGL((history_select_kernel<T, true>), dim3(blocks), dim3(64 * kBlockWaves), 0, s, a, ws);
     else hipLaunchKernelGGL((history_select_kernel<T, false>), dim3(blocks), dim3(64 * kBlockWaves), 0, s, a, ws);
 }
@@ -653,6 +699,7 @@ hipError_t launch_history_select(const SelectArgs& args, int dtype, void* worksp
     else launch_select<f16>(a, ws, blocks, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (in_one_launch(a)) return hipSuccess;
     hipLaunchKernelGGL(history_select_join_kernel, dim3(a.batch), dim3(64 * kBlockWaves), 0, s, a, ws);
     return hipGetLastError();
 }
