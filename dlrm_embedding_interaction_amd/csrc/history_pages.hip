@@ -604,7 +604,7 @@ constexpr int kReorderCols = 64;
 constexpr int kFreed = -1, kRefused = -2;
 
 __global__ __launch_bounds__(256) void history_reorder_kernel(ReorderArgs a) {
-    __shared__ int slot[kMostGroup], from[kMostGroup], len[kMostGroup];
+    __shared__ int slot[kMostGroup], from[kMostGroup], len[kMostGroup], twice[kMostGroup];
     __shared__ int page[kMostGroup][kReorderCols];
     const dlrm_history_cache_t& c = a.c;
     const int64_t first = (int64_t)blockIdx.x * a.group;
@@ -612,24 +612,29 @@ __global__ __launch_bounds__(256) void history_reorder_kernel(ReorderArgs a) {
     for (int i = tid; i < a.group; i += 256) {
         const int s = a.slots ? a.slots[first + i] : (int)(first + i);
         slot[i] = s >= 0 && s < c.n_slots ? s : -1;
+        twice[i] = 0;
         if (slot[i] >= 0 && blockIdx.y == 0) len[i] = c.lens[s];
+    }
+    __syncthreads();
+    for (int e = tid; e < a.group * a.group; e += 256) {
+        const int i = e / a.group, j = e % a.group;
+        if (j < i && slot[j] == slot[i]) twice[i] = 1;                      // a slot that came before
     }
     __syncthreads();
     for (int i = tid; i < a.group; i += 256) {
         const int p = a.parents[first + i];
-        bool ok = slot[i] >= 0 && (p == kFreed || (p >= 0 && p < a.group && slot[p] >= 0));
-        for (int j = 0; j < i; ++j) ok = ok && slot[j] != slot[i];          // a slot that came before
+        const bool ok = slot[i] >= 0 && !twice[i] && (p == kFreed || (p >= 0 && p < a.group && slot[p] >= 0));
         from[i] = ok ? p : kRefused;
     }
+    const int x = tid % kReorderCols, i0 = tid / kReorderCols;
     for (int64_t x0 = (int64_t)blockIdx.y * kReorderCols; x0 < c.max_pages; x0 += (int64_t)gridDim.y * kReorderCols) {
-        for (int e = tid; e < a.group * kReorderCols; e += 256) {
-            const int i = e / kReorderCols, x = e % kReorderCols;
-            if (slot[i] >= 0 && x0 + x < c.max_pages) page[i][x] = c.table[(int64_t)slot[i] * c.max_pages + x0 + x];
-        }
+        const bool in = x0 + x < c.max_pages;
+#pragma unroll 8
+        for (int i = i0; i < a.group; i += 256 / kReorderCols)
+            if (slot[i] >= 0 && in) page[i][x] = c.table[(int64_t)slot[i] * c.max_pages + x0 + x];
         __syncthreads();
-        for (int e = tid; e < a.group * kReorderCols; e += 256) {
-            const int i = e / kReorderCols, x = e % kReorderCols;
-            if (from[i] == kRefused || x0 + x >= c.max_pages) continue;
+        for (int i = i0; i < a.group; i += 256 / kReorderCols) {
+            if (from[i] == kRefused || !in) continue;
             const int p = from[i] == kFreed ? -1 : page[from[i]][x], o = page[i][x];
             if (p == o) continue;
             c.table[(int64_t)slot[i] * c.max_pages + x0 + x] = p;

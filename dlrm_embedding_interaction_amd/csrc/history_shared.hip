@@ -19,8 +19,8 @@
 
 namespace dlrm {
 
+constexpr int kTailBlocks = 512;          // rows' blocks of one wave from here on, of four below
 constexpr int kSharedWaves = 2048;       // waves the shared tiles' kernel aims at: two on each SIMD
-constexpr int kTailWaves = 4;
 
 // A group: its rows of the batch, the slot of one of its histories with events, and
 // the shared tiles: [0, lead) and [first, common), `count` in all.  All rows see all
@@ -95,10 +95,14 @@ __global__ __launch_bounds__(kGroupThreads) void history_group_kernel(SharedArgs
                 slot_of[tid] = slot >= 0 && slot < c.n_slots && c.lens[slot] > 0 ? slot : -1;
             }
             __syncthreads();
-#pragma unroll 4
-            for (int64_t e = tid; e < (int64_t)here * n; e += kGroupThreads) {
-                const int i = (int)(e % n), x = i < lead ? i : first + i - lead, slot = slot_of[e / n];
-                if (slot >= 0 && c.table[(int64_t)slot * c.max_pages + x] != one[x]) least = min(least, x);
+            for (int i = tid & 63; i < n; i += 64) {
+                const int x = i < lead ? i : first + i - lead, p = one[x];
+#pragma unroll 8
+                for (int k = tid >> 6; k < here; k += kGroupThreads / 64) {
+                    const int slot = slot_of[k];
+                    const int q = slot >= 0 ? c.table[(int64_t)slot * c.max_pages + x] : p;
+                    least = q != p ? min(least, x) : least;
+                }
             }
         }
         if (least < 0x7fffffff) atomicMin(&differs, least);
@@ -219,11 +223,11 @@ __global__ __launch_bounds__(256, 2) void history_shared_kernel(SharedArgs a, Sh
 }
 
 // A block per (history, kv head, chunk of its rows): the tiles that are its own, and the join.
-template <int D, int PE, typename T>
-__global__ __launch_bounds__(64 * kTailWaves, 2) void history_tail_kernel(SharedArgs a, SharedWs ws, int waves) {
+template <int D, int PE, typename T, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs a, SharedWs ws, int waves) {
     constexpr int NQ = Parts<T>::q, PT = kTile / PE, OP = D + 4;
-    __shared__ __attribute__((aligned(16))) float part_o[kTailWaves * 16 * OP];
-    __shared__ float part_m[16 * kTailWaves], part_l[16 * kTailWaves];
+    __shared__ __attribute__((aligned(16))) float part_o[WAVES > 1 ? WAVES * 16 * OP : 4];
+    __shared__ float part_m[16 * WAVES], part_l[16 * WAVES];
     const LookupArgs& l = a.l;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, g = lane >> 4, b = blockIdx.x;
@@ -258,8 +262,8 @@ __global__ __launch_bounds__(64 * kTailWaves, 2) void history_tail_kernel(Shared
         const float c = exponent_scale(l.scale);
         Tile<D> cur, nxt;
         load_tile<D, PE>(l.c, table, tile_of(wave) * PT, hk, n, g, cur);
-        for (int i = wave; i < count; i += kTailWaves) {
-            if (i + kTailWaves < count) load_tile<D, PE>(l.c, table, tile_of(i + kTailWaves) * PT, hk, n, g, nxt);
+        for (int i = wave; i < count; i += WAVES) {
+            if (i + WAVES < count) load_tile<D, PE>(l.c, table, tile_of(i + WAVES) * PT, hk, n, g, nxt);
             const int e0 = tile_of(i) * kTile;
             const bool whole = (e0 >= sp.low || e0 + kTile <= sp.lead_events) && e0 + kTile <= sp.len;
             use_tile<D, T>(cur, q, c, e0, whole, sp.low, sp.lead_events, sp.len, g, o, m, sum);
@@ -274,7 +278,7 @@ __global__ __launch_bounds__(64 * kTailWaves, 2) void history_tail_kernel(Shared
         const int64_t per = *ws.per;
         const int64_t row = (int64_t)(b - r.begin) * rows + (live ? y : 0), chunk = row / 16, block = chunk / waves;
         const int64_t t0 = at.tile + block * r.count, run0 = t0 / per, run1 = (t0 + r.count - 1) / per;
-        for (int64_t i = run0 + wave; __any(i <= run1); i += kTailWaves) {
+        for (int64_t i = run0 + wave; __any(i <= run1); i += WAVES) {
             const int64_t place = at.piece + block + i;
             if (i > run1 || place < 0 || place >= ws.pieces) continue;
             const float* part = ws.partial + ((place * l.c.n_kv_heads + hk) * waves + chunk % waves) * (16 * (D + 2));
@@ -288,23 +292,32 @@ __global__ __launch_bounds__(64 * kTailWaves, 2) void history_tail_kernel(Shared
             for (int j = 0; j < D / 16; ++j) o[j] = o[j] * f0 + *(const floatx4*)(part + col * D + 16 * j + 4 * g) * f1;
         }
     }
+    if constexpr (WAVES == 1) {
+        if (live) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            T* op = (T*)l.out + ((int64_t)b * l.queries + y / heads) * l.ld_out + (int64_t)(hk * heads + y % heads) * D;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) store4(op + 16 * j + 4 * g, o[j] * inv, l.wide);
+        }
+        return;
+    }
     if (g == 0) part_m[wave * 16 + n] = m;
     __syncthreads();
     float mx = part_m[n];
 #pragma unroll
-    for (int i = 1; i < kTailWaves; ++i) mx = fmaxf(mx, part_m[16 * i + n]);
+    for (int i = 1; i < WAVES; ++i) mx = fmaxf(mx, part_m[16 * i + n]);
     const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mx);
     if (g == 0) part_l[wave * 16 + n] = sum * f;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) *(floatx4*)&part_o[(wave * 16 + n) * OP + 16 * j + 4 * g] = o[j] * f;
     __syncthreads();
-    for (int x = tid; x < 4 * D; x += 64 * kTailWaves) {
+    for (int x = tid; x < 4 * D; x += 64 * WAVES) {
         const int i = x / (D / 4), d = x % (D / 4) * 4, row = r0 + i;
         if (row >= rows) break;
         float all = part_l[i];
         floatx4 v = *(const floatx4*)&part_o[i * OP + d];
 #pragma unroll
-        for (int w = 1; w < kTailWaves; ++w) {
+        for (int w = 1; w < WAVES; ++w) {
             all += part_l[16 * w + i];
             v += *(const floatx4*)&part_o[(16 * w + i) * OP + d];
         }
@@ -350,7 +363,7 @@ template <int D, int PE, typename T>
 static hipError_t launch_t(const SharedArgs& a, void* workspace, hipStream_t s) {
     const LookupArgs& l = a.l;
     const int rows = l.queries * (l.n_heads / l.c.n_kv_heads), waves = chunk_waves(l.batch, a.n_groups, rows);
-    if (!grid_fits(l.batch, 64 * kTailWaves) || !grid_fits(a.n_groups, kGroupThreads)) return kTooLarge;
+    if (!grid_fits(l.batch, 256) || !grid_fits(a.n_groups, kGroupThreads)) return kTooLarge;
     const SharedPlan p = plan_of(l.c, l.batch, a.n_groups, rows, waves);
     char* const w = (char*)workspace;
     const SharedWs ws = {(Group*)w, (Place*)(w + p.places), (int*)(w + p.group_of), (int64_t*)(w + p.per), p.pieces,
@@ -358,8 +371,12 @@ static hipError_t launch_t(const SharedArgs& a, void* workspace, hipStream_t s) 
     hipLaunchKernelGGL(history_group_kernel, dim3(a.n_groups), dim3(kGroupThreads), 0, s, a, ws);
     hipLaunchKernelGGL((history_shared_kernel<D, PE, T>), dim3(runs_of(l.c.n_kv_heads, waves), l.c.n_kv_heads),
                        dim3(64 * waves), 0, s, a, ws, waves);
-    hipLaunchKernelGGL((history_tail_kernel<D, PE, T>), dim3(l.batch, (rows + 15) / 16 * l.c.n_kv_heads),
-                       dim3(64 * kTailWaves), 0, s, a, ws, waves);
+    const int chunks = (rows + 15) / 16 * l.c.n_kv_heads;
+    const dim3 tails(l.batch, chunks);
+    if ((int64_t)l.batch * chunks > kTailBlocks)
+        hipLaunchKernelGGL((history_tail_kernel<D, PE, T, 1>), tails, dim3(64), 0, s, a, ws, waves);
+    else
+        hipLaunchKernelGGL((history_tail_kernel<D, PE, T, 4>), tails, dim3(256), 0, s, a, ws, waves);
     return hipGetLastError();
 }
 template <int D, int PE>
