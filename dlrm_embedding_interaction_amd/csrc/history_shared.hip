@@ -12,9 +12,11 @@
 // head and chunk of its rows, reads the tiles that are the history's own and joins
 // them with the pieces.
 //
-// A shared tile is one that every row of the group sees whole.  Where windows or sinks
-// of the histories end at different events, the tiles around these ends are each one's
-// own: a row that does not see an event must not meet its value, which may be a NaN.
+// Windows and sinks of a group's histories end at different events, so in the tiles
+// around these ends every row has a mask of its own.  The values there are the same for
+// all rows, and a row that does not see an event must not meet its value if that is a
+// NaN: in such tiles NaN codes are taken out of the product and given to the rows that
+// see them by a product of their places.
 #include "history_tile.h"
 
 namespace dlrm {
@@ -23,10 +25,10 @@ constexpr int kTailBlocks = 512;          // rows' blocks of one wave from here 
 constexpr int kSharedWaves = 2048;       // waves the shared tiles' kernel aims at: two on each SIMD
 
 // A group: its rows of the batch, the slot of one of its histories with events, and
-// the shared tiles: [0, lead) and [first, common), `count` in all.  All rows see all
-// of a shared tile, so that no row's mask is needed there.
+// the tiles on the same pages in all of them that any of them sees: [0, lead) and
+// [first, common), `count` in all.
 struct Group {
-    int begin, end, slot, lead, first, common, count;
+    int begin, end, slot, lead, first, common, count, unused;
 };
 // Where the group stands in the row of all tiles: of its tiles, and of its pieces.
 struct Place {
@@ -39,15 +41,15 @@ struct SharedWs {
     int* group_of;          // (batch)
     int64_t* per;           // tiles of a run
     int64_t pieces;         // that there is room for: as many as there can be while no two groups overlap
-    float* partial;         // (pieces, kv heads, waves of a block, 16 (head_dim + 2))
+    float* partial;         // (pieces, kv heads, waves of a block, columns (head_dim + 2))
+    int waves, cols;        // waves of a block, rows of a wave: 16 or 32
 };
 
-// A block per group: the tiles that lie on the same pages in all of its histories
-// and that all of them see whole.  Histories without events see nothing and do not
-// count.
+// A block per group: which tiles lie on the same pages in all of its histories.
+// Those without events see nothing and do not count.
 constexpr int kGroupThreads = 1024;
 __global__ __launch_bounds__(kGroupThreads) void history_group_kernel(SharedArgs a, SharedWs ws) {
-    __shared__ int len_min, lead_min, low_max, differs, some;
+    __shared__ int len_min, first_min, lead_max, differs, some;
     __shared__ int slot_of[kGroupThreads];
     const LookupArgs& l = a.l;
     const dlrm_history_cache_t& c = l.c;
@@ -62,8 +64,8 @@ __global__ __launch_bounds__(kGroupThreads) void history_group_kernel(SharedArgs
         end = begin + each;
     }
     if (tid == 0) {
-        len_min = lead_min = differs = 0x7fffffff;
-        low_max = 0;
+        len_min = first_min = differs = 0x7fffffff;
+        lead_max = 0;
         some = -1;
     }
     __syncthreads();
@@ -72,17 +74,17 @@ __global__ __launch_bounds__(kGroupThreads) void history_group_kernel(SharedArgs
         const Span s = span_of(l, b);
         if (!s.len) continue;
         atomicMin(&len_min, s.len);
-        atomicMin(&lead_min, s.low ? s.lead_events : s.len);
-        atomicMax(&low_max, s.low);
+        atomicMin(&first_min, s.first);
+        atomicMax(&lead_max, s.lead);
         atomicMax(&some, b);
     }
     __syncthreads();
-    Group r = {begin, end, 0, 0, 0, 0, 0};
+    Group r = {begin, end, 0, 0, 0, 0, 0, 0};
     if (some >= 0) {
         r.slot = l.slots ? l.slots[some] : some;
         const int pt = kTile / c.page_events, tiles = len_min / kTile;
-        r.first = min((low_max + kTile - 1) / kTile, tiles);
-        r.lead = min(lead_min / kTile, r.first);
+        r.first = min(first_min, tiles);
+        r.lead = min(lead_max, r.first);
         const int lead = r.lead * pt, first = r.first * pt;
         const int n = lead + tiles * pt - first;            // pages [0, lead) and [first, tiles pt)
         const int32_t* one = c.table + (int64_t)r.slot * c.max_pages;
@@ -115,9 +117,99 @@ __global__ __launch_bounds__(kGroupThreads) void history_group_kernel(SharedArgs
     if (tid == 0) ws.groups[g] = r;
 }
 
-// Blocks of `waves` chunks that the group's rows make.
-__device__ __forceinline__ int64_t blocks_of(const Group& g, int rows, int waves) {
-    return ((int64_t)(g.end - g.begin) * rows + 16 * waves - 1) / (16 * waves);
+// ---- tiles for 32 rows -----------------------------------------------------------
+//
+// As in history_tile.h, but with the 32x32x16 instruction, so that codes are decoded
+// once for 32 rows:
+//   S^T = K Q^T   two products of 32 events each.  Row m of product t is event
+//                 32 (m / 4 % 2) + 16 t + 4 (m / 8) + m % 4, so that half h of the wave
+//                 ends up with the scores of events 32 h .. 32 h + 31, in order.
+//   O^T += V^T P^T  four steps of 16 events, eight of each half.
+// K's registers take the next tile as soon as the first product is done, V's after the
+// second, so that one tile's registers are enough.
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+template <int D>
+struct Keys32 {
+    u32x4 k[2][D / 32];
+    float scale[2];
+};
+template <int D>
+struct Values32 {
+    u32x4 v[D / 32][2];
+    float scale[2];
+    bool in[2];
+};
+
+// The pages that a lane reads of a tile, -1 where there is none: found a tile ahead of
+// the codes, whose addresses would otherwise be waited for.
+template <int PE>
+struct Pages32 {
+    int k[2], v[2];
+    __device__ __forceinline__ void find(const dlrm_history_cache_t& c, const int32_t* table, int p0) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            k[u] = page(c, table, p0 + (32 * (lane >> 2 & 1) + 16 * u) / PE);
+            v[u] = page(c, table, p0 + (32 * (lane >> 5) + 16 * u) / PE);
+        }
+    }
+    __device__ __forceinline__ static int page(const dlrm_history_cache_t& c, const int32_t* table, int i) {
+        const int p = i < c.max_pages ? table[i] : -1;
+        return p >= 0 && p < c.n_pages ? p : -1;
+    }
+};
+
+template <int D, int PE>
+__device__ __forceinline__ void load_keys32(const dlrm_history_cache_t& c, const Pages32<PE>& p, int hk, Keys32<D>& t) {
+    const int lane = threadIdx.x & 63, m = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int e = 32 * (m >> 2 & 1) + 16 * u + 4 * (m >> 3) + (m & 3);
+        const int64_t at = (int64_t)(p.k[u] < 0 ? 0 : p.k[u]) * c.n_kv_heads + hk;
+        const uint8_t* k = c.k + (at * PE + e % PE) * D + h * 16;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) t.k[u][x] = *(const u32x4*)(k + 32 * x);
+        t.scale[u] = c.k_scale[at];
+    }
+}
+template <int D, int PE>
+__device__ __forceinline__ void load_values32(const dlrm_history_cache_t& c, const Pages32<PE>& p, int hk,
+                                              Values32<D>& t) {
+    const int lane = threadIdx.x & 63, m = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int e = 32 * h + 16 * u;
+        const int64_t at = (int64_t)(p.v[u] < 0 ? 0 : p.v[u]) * c.n_kv_heads + hk;
+        const uint8_t* v = c.v + (at * D + m) * PE + e % PE;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) t.v[j][u] = *(const u32x4*)(v + j * 32 * PE);
+        t.scale[u] = c.v_scale[at];
+        t.in[u] = p.v[u] >= 0;
+    }
+}
+
+// Bytes of a word that are the code of a NaN, as 0xff.
+__device__ __forceinline__ unsigned nan_bytes(unsigned w) {
+    return (((w & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xffu;
+}
+// Four bytes of 0xff or 0 as four bf16 of 1 or 0, in two words.
+__device__ __forceinline__ u32x2 ones_of(unsigned b) {
+    return u32x2{(b & 1u) * 0x3f80u | (b >> 8 & 1u) * 0x3f800000u, (b >> 16 & 1u) * 0x3f80u | (b >> 24 & 1u) * 0x3f800000u};
+}
+// Eight bits as eight bf16 of 1 or 0.
+__device__ __forceinline__ bf16x8 ones_of_bits(unsigned b) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = (b >> (2 * i) & 1u) * 0x3f80u | (b >> (2 * i + 1) & 1u) * 0x3f800000u;
+    return __builtin_bit_cast(bf16x8, w);
+}
+
+// ---- the shared tiles --------------------------------------------------------------
+
+// Blocks that the group's rows make, each taking so many of them.
+__device__ __forceinline__ int64_t blocks_of(const Group& g, int rows, int taken) {
+    return ((int64_t)(g.end - g.begin) * rows + taken - 1) / taken;
 }
 
 __device__ __forceinline__ int64_t wave_inclusive(int64_t v) {
@@ -130,13 +222,284 @@ __device__ __forceinline__ int64_t wave_inclusive(int64_t v) {
     return v;
 }
 
+// What a row sees of the tile at e0.
+struct Sight {
+    int low, lead;                       // events from low on and those below lead; the lane's row's
+    int low_max, lead_min;               // over the wave's rows
+    // Of tiles in rising order, those before number `from` and from number `to` on are seen whole by all rows.
+    __device__ __forceinline__ void edges(const Group& r, int* from, int* to) const {
+        auto before = [&](int tile) { return tile < r.first ? min(tile, r.lead) : r.lead + tile - r.first; };
+        *to = before(low_max / kTile + (low_max % kTile != 0));
+        *from = min(before(lead_min / kTile), *to);
+    }
+    template <int N>
+    __device__ __forceinline__ unsigned seen(int e) const {
+        unsigned s = 0;
+#pragma unroll
+        for (int x = 0; x < N; ++x) s |= e + x >= low || e + x < lead ? 1u << x : 0u;
+        return s;
+    }
+};
+
+// Sixteen rows of a group over a run of its tiles.
 template <int D, int PE, typename T>
-__global__ __launch_bounds__(256, 2) void history_shared_kernel(SharedArgs a, SharedWs ws, int waves) {
-    constexpr int NQ = Parts<T>::q, PT = kTile / PE;
+struct Rows16 {
+    static constexpr int COLS = 16;
+    bf16x8 q[D / 32][Parts<T>::q];
+    floatx4 o[D / 16];
+    float m = -INFINITY, sum = 0.f;
+
+    __device__ __forceinline__ static int column() { return threadIdx.x & 15; }
+    __device__ __forceinline__ void start(const T* qp, float scale, int wide) {
+        load_query<D>(qp, scale, wide, (threadIdx.x & 63) >> 4, q);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) o[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+    // Some rows do not see some events: masked, NaN values apart.
+    __device__ __forceinline__ void use_masked(Tile<D>& t, float c, int e0, const Sight& at) {
+        const int g = (threadIdx.x & 63) >> 4;
+        unsigned nan = 0;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) nan |= nan_bytes(t.v[j][x]);
+        if (__any(t.vin && nan)) {
+            const unsigned seen = t.vin ? at.seen<16>(e0 + 16 * g) : 0u;
+            const bf16x8 see[2] = {ones_of_bits(seen & 0xffu), ones_of_bits(seen >> 8)};
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                floatx4 n = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const unsigned b0 = nan_bytes(t.v[j][2 * h]), b1 = nan_bytes(t.v[j][2 * h + 1]);
+                    const u32x2 w0 = ones_of(b0), w1 = ones_of(b1);
+                    const u32x4 w = {w0[0], w0[1], w1[0], w1[1]};
+                    n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), see[h], n, 0, 0, 0);
+                    t.v[j][2 * h] &= ~b0;
+                    t.v[j][2 * h + 1] &= ~b1;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[j][i] += n[i] > 0.f ? NAN : 0.f;
+            }
+        }
+        use_tile<D, T, true>(t, q, c, e0, false, at.low, at.lead, 0x7fffffff, g, o, m, sum);
+    }
+    __device__ __forceinline__ void run(const dlrm_history_cache_t& c, const int32_t* table, const Group& r, int hk,
+                                        float scale, const Sight& at, int i0, int i1) {
+        constexpr bool TURNS = D < 128 || Parts<T>::q == 1;
+        const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+        auto tile_of = [&](int i) { return i < r.lead ? i : r.first + (i - r.lead); };
+        auto load = [&](int i, Tile<D>& t) { load_tile<D, PE>(c, table, tile_of(i) * (kTile / PE), hk, n, g, t); };
+        auto use = [&](Tile<D>& t) { use_tile<D, T>(t, q, scale, 0, true, 0, 0, kTile, g, o, m, sum); };
+        int from, to;
+        at.edges(r, &from, &to);
+        Tile<D> cur, nxt;
+        for (int i = max(i0, from); i < min(i1, to); ++i) {
+            load(i, cur);
+            use_masked(cur, scale, tile_of(i) * kTile, at);
+        }
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            const int stop = part ? i1 : min(i1, from);
+            int i = part ? max(i0, to) : i0;
+            if (i < stop) load(i, cur);
+            for (; i < stop; ++i) {
+                if (i + 1 < stop) load(i + 1, nxt);
+                use(cur);
+                if constexpr (TURNS) {
+                    if (++i >= stop) break;
+                    if (i + 1 < stop) load(i + 1, cur);
+                    use(nxt);
+                } else {
+                    cur = nxt;
+                }
+            }
+        }
+    }
+    // The weighted sums by column, then the maxima in powers of two, then the weights' sums.
+    __device__ __forceinline__ void leave(float* part, float c) {
+        const int n = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+        sum += swizzle_xor16(sum);
+        sum += __shfl_xor(sum, 32, 64);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) *(floatx4*)(part + n * D + 16 * j + 4 * g) = o[j];
+        if (g == 0) {
+            part[16 * D + n] = m * c;
+            part[16 * D + 16 + n] = sum;
+        }
+    }
+};
+
+template <int D, int PE, typename T>
+struct Rows32 {
+    static constexpr int COLS = 32, NQ = Parts<T>::q, NP = Parts<T>::p;
+    bf16x8 q[D / 16][NQ];
+    floatx16 o[D / 32];
+    float m = -INFINITY, sum = 0.f;
+
+    __device__ __forceinline__ static int column() { return threadIdx.x & 31; }
+    __device__ __forceinline__ void start(const T* qp, float scale, int wide) {
+        const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+            const int d0 = (s >> 1) * 32 + h * 16 + (s & 1) * 8;
+            const Raw<T> raw = wide ? load_raw<true>(qp + d0) : load_raw<false>(qp + d0);
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = scale < 0.f ? -(float)raw.x[i] : (float)raw.x[i];
+            split8<NQ>(x, q[s]);
+        }
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[j][i] = 0.f;
+    }
+    __device__ __forceinline__ void scores(const Keys32<D>& k, floatx16 (&s)[2]) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) s[u][x] = 0.f;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+                const bf16x8 kk = decode8(k.k[u][x / 2][x % 2 * 2], k.k[u][x / 2][x % 2 * 2 + 1], k.scale[u]);
+#pragma unroll
+                for (int y = 0; y < NQ; ++y) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kk, q[x][y], s[u], 0, 0, 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void weigh(const floatx16 (&s)[2], const Values32<D>& v, float scale) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) top = fmaxf(top, s[x >> 4][x & 15]);
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float mx = fmaxf(m, top);
+        if (__any(mx > m)) {
+            const float alpha = mx == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mx) * scale);
+            sum *= alpha;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) o[j] *= alpha;
+            m = mx;
+        }
+        const float mc = m == -INFINITY ? 0.f : m * scale;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float p[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                p[x] = __builtin_amdgcn_exp2f(fmaf(s[u >> 1][8 * (u & 1) + x], scale, -mc));
+                sum += p[x];
+            }
+            bf16x8 pp[NP];
+            split8<NP>(p, pp);
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                const bf16x8 vv = decode8(v.v[j][u >> 1][u % 2 * 2], v.v[j][u >> 1][u % 2 * 2 + 1], v.scale[u >> 1]);
+#pragma unroll
+                for (int y = 0; y < NP; ++y) o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vv, pp[y], o[j], 0, 0, 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void run(const dlrm_history_cache_t& c, const int32_t* table, const Group& r, int hk,
+                                        float scale, const Sight& at, int i0, int i1) {
+        constexpr int PT = kTile / PE;
+        const int h = (threadIdx.x & 63) >> 5;
+        auto tile_of = [&](int i) { return i < r.lead ? i : r.first + (i - r.lead); };
+        int from, to;
+        at.edges(r, &from, &to);
+        Pages32<PE> page;
+        Keys32<D> k;
+        Values32<D> v;
+        floatx16 s[2];
+        for (int i = max(i0, from); i < min(i1, to); ++i) {
+            page.find(c, table, tile_of(i) * PT);
+            load_keys32<D, PE>(c, page, hk, k);
+            load_values32<D, PE>(c, page, hk, v);
+            scores(k, s);
+            mask(s, v, at.seen<32>(tile_of(i) * kTile + 32 * h), true);
+            weigh(s, v, scale);
+        }
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            const int stop = part ? i1 : min(i1, from);
+            int i = part ? max(i0, to) : i0;
+            if (i >= stop) continue;
+            page.find(c, table, tile_of(i) * PT);
+            load_keys32<D, PE>(c, page, hk, k);
+            load_values32<D, PE>(c, page, hk, v);
+            page.find(c, table, tile_of(min(i + 1, stop - 1)) * PT);
+            for (; i < stop; ++i) {
+                Pages32<PE> later;
+                later.find(c, table, tile_of(min(i + 2, stop - 1)) * PT);
+                scores(k, s);
+                load_keys32<D, PE>(c, page, hk, k);
+                if (__builtin_expect(__any(!v.in[0] || !v.in[1]), 0)) mask(s, v, ~0u, false);
+                weigh(s, v, scale);
+                load_values32<D, PE>(c, page, hk, v);
+                page = later;
+            }
+        }
+    }
+    // Leaves out the events that a row does not see and those of pages that are not there; `apart`: NaN values leave
+    // the product for the rows that see them.
+    __device__ __forceinline__ void mask(floatx16 (&s)[2], Values32<D>& v, unsigned seen, bool apart) {
+        seen &= (v.in[0] ? 0xffffu : 0u) | (v.in[1] ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+            if (!(seen >> x & 1)) s[x >> 4][x & 15] = -INFINITY;
+        unsigned nan = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            v.scale[u] = v.in[u] ? v.scale[u] : 1.f;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    v.v[j][u][x] = v.in[u] ? v.v[j][u][x] : 0u;
+                    nan |= nan_bytes(v.v[j][u][x]);
+                }
+        }
+        if (!apart || !__any(nan)) return;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            floatx16 n;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) n[x] = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const unsigned b0 = nan_bytes(v.v[j][u >> 1][u % 2 * 2]), b1 = nan_bytes(v.v[j][u >> 1][u % 2 * 2 + 1]);
+                const u32x2 a0 = ones_of(b0), a1 = ones_of(b1);
+                const u32x4 w = {a0[0], a0[1], a1[0], a1[1]};
+                n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w),
+                                                            ones_of_bits(seen >> (8 * u) & 0xffu), n, 0, 0, 0);
+                v.v[j][u >> 1][u % 2 * 2] &= ~b0;
+                v.v[j][u >> 1][u % 2 * 2 + 1] &= ~b1;
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[j][x] += n[x] > 0.f ? NAN : 0.f;
+        }
+    }
+    __device__ __forceinline__ void leave(float* part, float c) {
+        const int n = threadIdx.x & 31, h = (threadIdx.x & 63) >> 5;
+        sum += __shfl_xor(sum, 32, 64);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+                *(floatx4*)(part + n * D + 32 * j + 8 * a + 4 * h) =
+                    floatx4{o[j][4 * a], o[j][4 * a + 1], o[j][4 * a + 2], o[j][4 * a + 3]};
+        if (h == 0) {
+            part[32 * D + n] = m * c;
+            part[32 * D + 32 + n] = sum;
+        }
+    }
+};
+
+template <int D, int PE, typename T, template <int, int, typename> class Rows>
+__global__ __launch_bounds__(256, 2) void history_shared_kernel(SharedArgs a, SharedWs ws) {
+    typedef Rows<D, PE, T> R;
     const LookupArgs& l = a.l;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int n = lane & 15, g = lane >> 4, hk = blockIdx.y;
-    const int heads = l.n_heads / l.c.n_kv_heads, rows = l.queries * heads;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), hk = blockIdx.y;
+    const int heads = l.n_heads / l.c.n_kv_heads, rows = l.queries * heads, taken = R::COLS * ws.waves;
 
     // tiles and pieces before each lane's share of the groups
     const int each = (a.n_groups + 63) / 64;
@@ -144,7 +507,7 @@ __global__ __launch_bounds__(256, 2) void history_shared_kernel(SharedArgs a, Sh
     int64_t tiles = 0, pieces = 0;
     for (int i = lo; i < hi; ++i) {
         const Group r = ws.groups[i];
-        const int64_t blocks = blocks_of(r, rows, waves);
+        const int64_t blocks = blocks_of(r, rows, taken);
         tiles += blocks * r.count;
         pieces += blocks;
     }
@@ -162,7 +525,7 @@ __global__ __launch_bounds__(256, 2) void history_shared_kernel(SharedArgs a, Sh
     const float c = exponent_scale(l.scale);
     while (at < stop) {
         const Group r = ws.groups[gi];
-        const int64_t blocks = blocks_of(r, rows, waves);
+        const int64_t blocks = blocks_of(r, rows, taken);
         if (start + blocks * r.count <= at) {
             start += blocks * r.count;
             piece += blocks;
@@ -174,57 +537,36 @@ __global__ __launch_bounds__(256, 2) void history_shared_kernel(SharedArgs a, Sh
         const int i0 = (int)(at - start - block * r.count);
         const int i1 = r.count - i0 < stop - at ? r.count : i0 + (int)(stop - at);
         at += i1 - i0;
-        const int64_t chunk = block * waves + wave;
-        const int64_t all = (int64_t)(r.end - r.begin) * rows;
-        const int64_t place = piece + block + blockIdx.x;
-        if (chunk * 16 >= all || place >= ws.pieces) continue;
+        const int64_t chunk = block * ws.waves + wave, first = chunk * R::COLS;
+        const int64_t all = (int64_t)(r.end - r.begin) * rows, place = piece + block + blockIdx.x;
+        if (first >= all || place >= ws.pieces) continue;
 
         // the lane's column: a row of one of the group's histories
-        const int64_t row = chunk * 16 + n < all ? chunk * 16 + n : chunk * 16;
+        const int64_t row = first + R::column() < all ? first + R::column() : first;
         const int b = r.begin + (int)(row / rows), y = (int)(row % rows);
-        bf16x8 q[D / 32][NQ];
-        load_query<D>((const T*)l.q + ((int64_t)b * l.queries + y / heads) * l.ld_q + (int64_t)(hk * heads + y % heads) * D,
-                      l.scale, l.wide, g, q);
-        const int32_t* table = l.c.table + (int64_t)r.slot * l.c.max_pages;
-        floatx4 o[D / 16];
+        const Span sp = span_of(l, b);
+        Sight sight;
+        sight.low = sp.low;                 // a history without events: as if it saw everything, and not read later
+        sight.lead = sp.low ? sp.lead_events : 0x7fffffff;
+        sight.low_max = sight.low, sight.lead_min = sight.lead;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) o[j] = floatx4{0.f, 0.f, 0.f, 0.f};
-        float m = -INFINITY, sum = 0.f;
-        auto tile_of = [&](int i) { return i < r.lead ? i : r.first + (i - r.lead); };
-        auto load = [&](int i, Tile<D>& t) { load_tile<D, PE>(l.c, table, tile_of(i) * PT, hk, n, g, t); };
-        auto use = [&](Tile<D>& t) {
-            use_tile<D, T>(t, q, c, 0, true, 0, 0, kTile, g, o, m, sum);       // all of it but pages that are not there
-        };
-        constexpr bool TURNS = D < 128 || NQ == 1;
-        Tile<D> cur, nxt;
-        load(i0, cur);
-        for (int i = i0; i < i1; ++i) {
-            if (i + 1 < i1) load(i + 1, nxt);
-            use(cur);
-            if constexpr (TURNS) {
-                if (++i >= i1) break;
-                if (i + 1 < i1) load(i + 1, cur);
-                use(nxt);
-            } else {
-                cur = nxt;
-            }
+        for (int d = 32; d; d >>= 1) {
+            sight.low_max = max(sight.low_max, __shfl_xor(sight.low_max, d, 64));
+            sight.lead_min = min(sight.lead_min, __shfl_xor(sight.lead_min, d, 64));
         }
-        sum += swizzle_xor16(sum);
-        sum += __shfl_xor(sum, 32, 64);
-        float* part = ws.partial +
-                      ((place * gridDim.y + hk) * waves + wave) * (16 * (D + 2));
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) *(floatx4*)(part + n * D + 16 * j + 4 * g) = o[j];
-        if (g == 0) {
-            part[16 * D + n] = m * c;
-            part[16 * D + 16 + n] = sum;
-        }
+        sight.low_max = __builtin_amdgcn_readfirstlane(sight.low_max);
+        sight.lead_min = __builtin_amdgcn_readfirstlane(sight.lead_min);
+        R sums;
+        sums.start((const T*)l.q + ((int64_t)b * l.queries + y / heads) * l.ld_q + (int64_t)(hk * heads + y % heads) * D,
+                   l.scale, l.wide);
+        sums.run(l.c, l.c.table + (int64_t)r.slot * l.c.max_pages, r, hk, c, sight, i0, i1);
+        sums.leave(ws.partial + ((place * gridDim.y + hk) * ws.waves + wave) * (R::COLS * (D + 2)), c);
     }
 }
 
 // A block per (history, kv head, chunk of its rows): the tiles that are its own, and the join.
 template <int D, int PE, typename T, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs a, SharedWs ws, int waves) {
+__global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs a, SharedWs ws) {
     constexpr int NQ = Parts<T>::q, PT = kTile / PE, OP = D + 4;
     __shared__ __attribute__((aligned(16))) float part_o[WAVES > 1 ? WAVES * 16 * OP : 4];
     __shared__ float part_m[16 * WAVES], part_l[16 * WAVES];
@@ -238,21 +580,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
     if (sp.count == 0 && l.slots && blockIdx.y == 0 && tid == 0) count_refused(l, b);
 
     const int gi = ws.group_of[b];
-    Group r = {0, 0, 0, 0, 0, 0, 0};
+    Group r = {0, 0, 0, 0, 0, 0, 0, 0};
     if (gi >= 0 && gi < a.n_groups) r = ws.groups[gi];
-    if (b < r.begin || b >= r.end || !sp.len) r.lead = r.first = r.common = r.count = 0;
-    // the tiles that are the history's own: of its sinks, of its window before the shared ones, and behind them
+    if (b < r.begin || b >= r.end || !sp.len) r.common = r.count = 0;
+    // the history's tiles behind the shared ones
+    auto tile_of = [&](int i) { return i < sp.lead ? i : sp.first + (i - sp.lead); };
     const int end = (sp.len + kTile - 1) / kTile;
-    const int n0 = max(sp.lead - r.lead, 0), b1 = max(sp.first, r.lead), n1 = max(min(r.first, end) - b1, 0);
-    const int b2 = max(sp.first, r.common), n2 = max(end - b2, 0);
-    auto tile_of = [&](int i) { return i < n0 ? r.lead + i : (i < n0 + n1 ? b1 + i - n0 : b2 + i - n0 - n1); };
-    const int count = n0 + n1 + n2;
+    const int shared = min(sp.lead, r.common) + max(min(end, r.common) - sp.first, 0), own = shared + wave;
 
     floatx4 o[D / 16];
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) o[j] = floatx4{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, sum = 0.f;
-    if (wave < count) {
+    if (own < sp.count) {
         bf16x8 q[D / 32][NQ];
         const int yy = live ? y : 0;
         load_query<D>((const T*)l.q + ((int64_t)b * l.queries + yy / heads) * l.ld_q + (int64_t)(hk * heads + yy % heads) * D,
@@ -261,9 +601,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
         const int32_t* table = l.c.table + (int64_t)slot * l.c.max_pages;
         const float c = exponent_scale(l.scale);
         Tile<D> cur, nxt;
-        load_tile<D, PE>(l.c, table, tile_of(wave) * PT, hk, n, g, cur);
-        for (int i = wave; i < count; i += WAVES) {
-            if (i + WAVES < count) load_tile<D, PE>(l.c, table, tile_of(i + WAVES) * PT, hk, n, g, nxt);
+        load_tile<D, PE>(l.c, table, tile_of(own) * PT, hk, n, g, cur);
+        for (int i = own; i < sp.count; i += WAVES) {
+            if (i + WAVES < sp.count) load_tile<D, PE>(l.c, table, tile_of(i + WAVES) * PT, hk, n, g, nxt);
             const int e0 = tile_of(i) * kTile;
             const bool whole = (e0 >= sp.low || e0 + kTile <= sp.lead_events) && e0 + kTile <= sp.len;
             use_tile<D, T>(cur, q, c, e0, whole, sp.low, sp.lead_events, sp.len, g, o, m, sum);
@@ -276,14 +616,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
     if (r.count) {
         const Place at = ws.places[gi];
         const int64_t per = *ws.per;
-        const int64_t row = (int64_t)(b - r.begin) * rows + (live ? y : 0), chunk = row / 16, block = chunk / waves;
+        const int64_t row = (int64_t)(b - r.begin) * rows + (live ? y : 0), chunk = row / ws.cols, block = chunk / ws.waves;
         const int64_t t0 = at.tile + block * r.count, run0 = t0 / per, run1 = (t0 + r.count - 1) / per;
+        const int col = (int)(row % ws.cols);
         for (int64_t i = run0 + wave; __any(i <= run1); i += WAVES) {
             const int64_t place = at.piece + block + i;
             if (i > run1 || place < 0 || place >= ws.pieces) continue;
-            const float* part = ws.partial + ((place * l.c.n_kv_heads + hk) * waves + chunk % waves) * (16 * (D + 2));
-            const int col = (int)(row % 16);
-            const float pm = part[16 * D + col], ps = part[16 * D + 16 + col];
+            const float* part =
+                ws.partial + ((place * l.c.n_kv_heads + hk) * ws.waves + chunk % ws.waves) * (ws.cols * (D + 2));
+            const float pm = part[ws.cols * D + col], ps = part[ws.cols * D + ws.cols + col];
             if (pm == -INFINITY) continue;
             const float mx = fmaxf(m, pm), f0 = __builtin_amdgcn_exp2f(m - mx), f1 = __builtin_amdgcn_exp2f(pm - mx);
             m = mx;
@@ -326,10 +667,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
     }
 }
 
-// Waves of a block, each with a chunk of 16 of its group's rows: as many as a group has chunks on average, up to four.
-static int chunk_waves(int64_t batch, int64_t n_groups, int rows) {
-    const int64_t chunks = ((batch + n_groups - 1) / n_groups * rows + 15) / 16;
-    return chunks > 2 ? 4 : (chunks > 1 ? 2 : 1);
+// Rows that a wave takes, and the waves of a block: as many as a group's rows need on average, up to four.
+struct Shape {
+    int cols, waves;
+};
+static Shape shape_of(int64_t batch, int64_t n_groups, int rows) {
+    const int64_t mean = (batch + n_groups - 1) / n_groups * rows;
+    Shape s;
+    s.cols = mean > 16 ? 32 : 16;
+    const int64_t chunks = (mean + s.cols - 1) / s.cols;
+    s.waves = chunks > 2 ? 4 : (chunks > 1 ? 2 : 1);
+    return s;
 }
 static int runs_of(int n_kv_heads, int waves) {
     const int n = kSharedWaves / (n_kv_heads * waves);
@@ -343,40 +691,43 @@ struct SharedPlan {
     size_t places, group_of, per, partial, end;
     int64_t pieces;
 };
-static SharedPlan plan_of(const dlrm_history_cache_t& c, int64_t batch, int64_t n_groups, int rows, int waves) {
+static SharedPlan plan_of(const dlrm_history_cache_t& c, int64_t batch, int64_t n_groups, int rows, Shape shape) {
     SharedPlan p;
     p.places = round256(n_groups * sizeof(Group));
     p.group_of = p.places + round256(n_groups * sizeof(Place));
     p.per = p.group_of + round256(batch * sizeof(int));
     p.partial = p.per + 256;
-    p.pieces = runs_of(c.n_kv_heads, waves) + batch * rows / (16 * waves) + n_groups;
-    p.end = p.partial + (size_t)p.pieces * c.n_kv_heads * waves * 16 * (c.head_dim + 2) * sizeof(float);
+    p.pieces = runs_of(c.n_kv_heads, shape.waves) + batch * rows / (shape.cols * shape.waves) + n_groups;
+    p.end = p.partial +
+            (size_t)p.pieces * c.n_kv_heads * shape.waves * shape.cols * (c.head_dim + 2) * sizeof(float);
     return p;
 }
 
 size_t shared_workspace_bytes(const dlrm_history_cache_t& c, int64_t batch, int64_t n_groups, int queries, int n_heads) {
     const int rows = queries * (n_heads / c.n_kv_heads);
-    return plan_of(c, batch, n_groups, rows, chunk_waves(batch, n_groups, rows)).end;
+    return plan_of(c, batch, n_groups, rows, shape_of(batch, n_groups, rows)).end;
 }
 
 template <int D, int PE, typename T>
 static hipError_t launch_t(const SharedArgs& a, void* workspace, hipStream_t s) {
     const LookupArgs& l = a.l;
-    const int rows = l.queries * (l.n_heads / l.c.n_kv_heads), waves = chunk_waves(l.batch, a.n_groups, rows);
+    const int rows = l.queries * (l.n_heads / l.c.n_kv_heads);
+    const Shape shape = shape_of(l.batch, a.n_groups, rows);
     if (!grid_fits(l.batch, 256) || !grid_fits(a.n_groups, kGroupThreads)) return kTooLarge;
-    const SharedPlan p = plan_of(l.c, l.batch, a.n_groups, rows, waves);
+    const SharedPlan p = plan_of(l.c, l.batch, a.n_groups, rows, shape);
     char* const w = (char*)workspace;
     const SharedWs ws = {(Group*)w, (Place*)(w + p.places), (int*)(w + p.group_of), (int64_t*)(w + p.per), p.pieces,
-                         (float*)(w + p.partial)};
+                         (float*)(w + p.partial), shape.waves, shape.cols};
     hipLaunchKernelGGL(history_group_kernel, dim3(a.n_groups), dim3(kGroupThreads), 0, s, a, ws);
-    hipLaunchKernelGGL((history_shared_kernel<D, PE, T>), dim3(runs_of(l.c.n_kv_heads, waves), l.c.n_kv_heads),
-                       dim3(64 * waves), 0, s, a, ws, waves);
+    const dim3 grid(runs_of(l.c.n_kv_heads, shape.waves), l.c.n_kv_heads), block(64 * shape.waves);
+    if (shape.cols == 32) hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows32>), grid, block, 0, s, a, ws);
+    else hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows16>), grid, block, 0, s, a, ws);
     const int chunks = (rows + 15) / 16 * l.c.n_kv_heads;
     const dim3 tails(l.batch, chunks);
     if ((int64_t)l.batch * chunks > kTailBlocks)
-        hipLaunchKernelGGL((history_tail_kernel<D, PE, T, 1>), tails, dim3(64), 0, s, a, ws, waves);
+        hipLaunchKernelGGL((history_tail_kernel<D, PE, T, 1>), tails, dim3(64), 0, s, a, ws);
     else
-        hipLaunchKernelGGL((history_tail_kernel<D, PE, T, 4>), tails, dim3(256), 0, s, a, ws, waves);
+        hipLaunchKernelGGL((history_tail_kernel<D, PE, T, 4>), tails, dim3(256), 0, s, a, ws);
     return hipGetLastError();
 }
 template <int D, int PE>

@@ -150,8 +150,9 @@ __device__ __forceinline__ void load_tile(const dlrm_history_cache_t& c, const i
 
 // The tile's part of the rows' results: o the weighted sums, m the largest score (before the scale c), l the lane's
 // share of the weights' sum.  Events below `len` that are not below `low`, or are below `lead`, are seen; `whole`, the
-// same for the wave: all of the tile.
-template <int D, typename T>
+// same for the wave: all of the tile.  ROWS: low and lead are each row's own, and the
+// values of events that some rows do not see are finite.
+template <int D, typename T, bool ROWS = false>
 __device__ __forceinline__ void use_tile(Tile<D>& t, const bf16x8 (&q)[D / 32][Parts<T>::q], float c, int e0, bool whole,
                                          int low, int lead, int len, int g, floatx4 (&o)[D / 16], float& m, float& l) {
     constexpr int NQ = Parts<T>::q, NP = Parts<T>::p;
@@ -181,6 +182,7 @@ __device__ __forceinline__ void use_tile(Tile<D>& t, const bf16x8 (&q)[D / 32][P
 #pragma unroll
         for (int x = 0; x < 16; ++x)
             if (!(seen >> x & 1)) s[x >> 2][x & 3] = -INFINITY;
+        if constexpr (ROWS) seen = t.vin ? 0xffffu : 0u;
         u32x4 keep;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
