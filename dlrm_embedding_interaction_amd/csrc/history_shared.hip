@@ -125,8 +125,8 @@ __global__ __launch_bounds__(kGroupThreads) void history_group_kernel(SharedArgs
 //                 32 (m / 4 % 2) + 16 t + 4 (m / 8) + m % 4, so that half h of the wave
 //                 ends up with the scores of events 32 h .. 32 h + 31, in order.
 //   O^T += V^T P^T  four steps of 16 events, eight of each half.
-// K's registers take the next tile as soon as the first product is done, V's after the
-// second, so that one tile's registers are enough.
+// K's registers take the next tile as soon as the first product is done, each half of
+// V's after its steps, so that one tile's registers are enough.
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 template <int D>
@@ -141,24 +141,24 @@ struct Values32 {
     bool in[2];
 };
 
-// The pages that a lane reads of a tile, -1 where there is none: found a tile ahead of
-// the codes, whose addresses would otherwise be waited for.
+// The pages that a lane reads of a tile, found a tile ahead of the codes, whose
+// addresses would otherwise be waited for.  A shared tile lies whole within every
+// list; an entry that is no page is only looked at when it is used, so that no load
+// under way has to be waited for here.
 template <int PE>
 struct Pages32 {
     int k[2], v[2];
-    __device__ __forceinline__ void find(const dlrm_history_cache_t& c, const int32_t* table, int p0) {
+    __device__ __forceinline__ void find(const int32_t* table, int p0) {
         const int lane = threadIdx.x & 63;
+        asm("" : "+v"(p0));     // a lane's value: one that is the wave's would be waited for, to reach scalar registers
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            k[u] = page(c, table, p0 + (32 * (lane >> 2 & 1) + 16 * u) / PE);
-            v[u] = page(c, table, p0 + (32 * (lane >> 5) + 16 * u) / PE);
+            k[u] = table[p0 + (32 * (lane >> 2 & 1) + 16 * u) / PE];
+            v[u] = table[p0 + (32 * (lane >> 5) + 16 * u) / PE];
         }
     }
-    __device__ __forceinline__ static int page(const dlrm_history_cache_t& c, const int32_t* table, int i) {
-        const int p = i < c.max_pages ? table[i] : -1;
-        return p >= 0 && p < c.n_pages ? p : -1;
-    }
 };
+__device__ __forceinline__ bool is_page(const dlrm_history_cache_t& c, int p) { return p >= 0 && p < c.n_pages; }
 
 template <int D, int PE>
 __device__ __forceinline__ void load_keys32(const dlrm_history_cache_t& c, const Pages32<PE>& p, int hk, Keys32<D>& t) {
@@ -166,27 +166,25 @@ __device__ __forceinline__ void load_keys32(const dlrm_history_cache_t& c, const
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int e = 32 * (m >> 2 & 1) + 16 * u + 4 * (m >> 3) + (m & 3);
-        const int64_t at = (int64_t)(p.k[u] < 0 ? 0 : p.k[u]) * c.n_kv_heads + hk;
+        const int64_t at = (int64_t)(is_page(c, p.k[u]) ? p.k[u] : 0) * c.n_kv_heads + hk;
         const uint8_t* k = c.k + (at * PE + e % PE) * D + h * 16;
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) t.k[u][x] = *(const u32x4*)(k + 32 * x);
         t.scale[u] = c.k_scale[at];
     }
 }
+// Half u of them: the events that the second product's steps 2 u and 2 u + 1 take.
 template <int D, int PE>
-__device__ __forceinline__ void load_values32(const dlrm_history_cache_t& c, const Pages32<PE>& p, int hk,
+__device__ __forceinline__ void load_values32(const dlrm_history_cache_t& c, const Pages32<PE>& p, int hk, int u,
                                               Values32<D>& t) {
     const int lane = threadIdx.x & 63, m = lane & 31, h = lane >> 5;
+    const int e = 32 * h + 16 * u;
+    t.in[u] = is_page(c, p.v[u]);
+    const int64_t at = (int64_t)(t.in[u] ? p.v[u] : 0) * c.n_kv_heads + hk;
+    const uint8_t* v = c.v + (at * D + m) * PE + e % PE;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int e = 32 * h + 16 * u;
-        const int64_t at = (int64_t)(p.v[u] < 0 ? 0 : p.v[u]) * c.n_kv_heads + hk;
-        const uint8_t* v = c.v + (at * D + m) * PE + e % PE;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) t.v[j][u] = *(const u32x4*)(v + j * 32 * PE);
-        t.scale[u] = c.v_scale[at];
-        t.in[u] = p.v[u] >= 0;
-    }
+    for (int j = 0; j < D / 32; ++j) t.v[j][u] = *(const u32x4*)(v + j * 32 * PE);
+    t.scale[u] = c.v_scale[at];
 }
 
 // Bytes of a word that are the code of a NaN, as 0xff.
@@ -367,7 +365,8 @@ struct Rows32 {
             }
         }
     }
-    __device__ __forceinline__ void weigh(const floatx16 (&s)[2], const Values32<D>& v, float scale) {
+    // The running maximum; what the exponents are taken against.
+    __device__ __forceinline__ float raise(const floatx16 (&s)[2], float scale) {
         float top = -INFINITY;
 #pragma unroll
         for (int x = 0; x < 32; ++x) top = fmaxf(top, s[x >> 4][x & 15]);
@@ -380,20 +379,23 @@ struct Rows32 {
             for (int j = 0; j < D / 32; ++j) o[j] *= alpha;
             m = mx;
         }
-        const float mc = m == -INFINITY ? 0.f : m * scale;
+        return m == -INFINITY ? 0.f : m * scale;
+    }
+    // The second product's steps 2 half and 2 half + 1.
+    __device__ __forceinline__ void weigh(const floatx16 (&s)[2], const Values32<D>& v, float scale, float mc, int half) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 2 * half; u < 2 * half + 2; ++u) {
             float p[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-                p[x] = __builtin_amdgcn_exp2f(fmaf(s[u >> 1][8 * (u & 1) + x], scale, -mc));
+                p[x] = __builtin_amdgcn_exp2f(fmaf(s[half][8 * (u & 1) + x], scale, -mc));
                 sum += p[x];
             }
             bf16x8 pp[NP];
             split8<NP>(p, pp);
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
-                const bf16x8 vv = decode8(v.v[j][u >> 1][u % 2 * 2], v.v[j][u >> 1][u % 2 * 2 + 1], v.scale[u >> 1]);
+                const bf16x8 vv = decode8(v.v[j][half][u % 2 * 2], v.v[j][half][u % 2 * 2 + 1], v.scale[half]);
 #pragma unroll
                 for (int y = 0; y < NP; ++y) o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vv, pp[y], o[j], 0, 0, 0);
             }
@@ -411,30 +413,37 @@ struct Rows32 {
         Values32<D> v;
         floatx16 s[2];
         for (int i = max(i0, from); i < min(i1, to); ++i) {
-            page.find(c, table, tile_of(i) * PT);
+            page.find(table, tile_of(i) * PT);
             load_keys32<D, PE>(c, page, hk, k);
-            load_values32<D, PE>(c, page, hk, v);
+            load_values32<D, PE>(c, page, hk, 0, v);
+            load_values32<D, PE>(c, page, hk, 1, v);
             scores(k, s);
             mask(s, v, at.seen<32>(tile_of(i) * kTile + 32 * h), true);
-            weigh(s, v, scale);
+            const float mc = raise(s, scale);
+            weigh(s, v, scale, mc, 0);
+            weigh(s, v, scale, mc, 1);
         }
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
             const int stop = part ? i1 : min(i1, from);
             int i = part ? max(i0, to) : i0;
             if (i >= stop) continue;
-            page.find(c, table, tile_of(i) * PT);
+            page.find(table, tile_of(i) * PT);
             load_keys32<D, PE>(c, page, hk, k);
-            load_values32<D, PE>(c, page, hk, v);
-            page.find(c, table, tile_of(min(i + 1, stop - 1)) * PT);
+            load_values32<D, PE>(c, page, hk, 0, v);
+            load_values32<D, PE>(c, page, hk, 1, v);
+            page.find(table, tile_of(min(i + 1, stop - 1)) * PT);
             for (; i < stop; ++i) {
                 Pages32<PE> later;
-                later.find(c, table, tile_of(min(i + 2, stop - 1)) * PT);
+                later.find(table, tile_of(min(i + 2, stop - 1)) * PT);
                 scores(k, s);
                 load_keys32<D, PE>(c, page, hk, k);
                 if (__builtin_expect(__any(!v.in[0] || !v.in[1]), 0)) mask(s, v, ~0u, false);
-                weigh(s, v, scale);
-                load_values32<D, PE>(c, page, hk, v);
+                const float mc = raise(s, scale);
+                weigh(s, v, scale, mc, 0);
+                load_values32<D, PE>(c, page, hk, 0, v);
+                weigh(s, v, scale, mc, 1);
+                load_values32<D, PE>(c, page, hk, 1, v);
                 page = later;
             }
         }
