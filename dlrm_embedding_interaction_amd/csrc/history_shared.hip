@@ -187,6 +187,73 @@ __device__ __forceinline__ void load_values32(const dlrm_history_cache_t& c, con
     t.scale[u] = c.v_scale[at];
 }
 
+// A tile as the waves of a block share it: every wave reads its part of the codes in
+// whole lines and writes it to LDS.  The 16-byte chunks of a row stand in an order that
+// follows from the row, so that the sixteen lanes that read at once meet every bank
+// once.
+template <int D, int PE, int WAVES>
+struct Staged {
+    static constexpr int CHUNKS = 64 * D / 16 / 64 / WAVES;      // of the keys, and of the values, per lane
+    static constexpr int ROW = D / 16;                           // chunks of a key row; a value row has four
+    static_assert(CHUNKS >= 1, "a tile has a chunk for every thread of the block");
+    u32x4 k[CHUNKS], v[CHUNKS];
+    // Place of a chunk within its row.
+    __device__ __forceinline__ static int key_place(int row, int chunk) {
+        return chunk ^ (ROW == 8 ? (row >> 1 & 3) | (row >> 5 & 1) << 2 : (ROW == 4 ? (row >> 2 & 1) | (row >> 5 & 1) << 1 : row >> 5 & 1));
+    }
+    __device__ __forceinline__ static int value_place(int d, int chunk) { return chunk ^ (d >> 2 & 3); }
+
+    struct Pages {
+        int k[CHUNKS], v[CHUNKS];
+        __device__ __forceinline__ void find(const int32_t* table, int p0) {
+            asm("" : "+v"(p0));     // as in Pages32
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                const int at = i * 64 * WAVES + threadIdx.x, d = at >> 2;
+                k[i] = table[p0 + at / ROW / PE];
+                v[i] = table[p0 + 16 * value_place(d, at & 3) / PE];
+            }
+        }
+    };
+    __device__ __forceinline__ void load(const dlrm_history_cache_t& c, const Pages& p, int hk) {
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int at = i * 64 * WAVES + threadIdx.x, row = at / ROW, d = at >> 2, e = 16 * value_place(d, at & 3);
+            const int64_t pk = (int64_t)(is_page(c, p.k[i]) ? p.k[i] : 0) * c.n_kv_heads + hk;
+            const int64_t pv = (int64_t)(is_page(c, p.v[i]) ? p.v[i] : 0) * c.n_kv_heads + hk;
+            k[i] = *(const u32x4*)(c.k + (pk * PE + row % PE) * D + 16 * key_place(row, at % ROW));
+            v[i] = *(const u32x4*)(c.v + (pv * D + d) * PE + e % PE);
+        }
+    }
+    __device__ __forceinline__ void store(u32x4* lds) const {
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int at = i * 64 * WAVES + threadIdx.x;
+            lds[at] = k[i];
+            lds[4 * D + at] = v[i];
+        }
+    }
+    __device__ __forceinline__ static void keys(const u32x4* lds, Keys32<D>& t) {
+        const int lane = threadIdx.x & 63, m = lane & 31, h = lane >> 5;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int e = 32 * (m >> 2 & 1) + 16 * u + 4 * (m >> 3) + (m & 3);
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) t.k[u][x] = lds[e * ROW + key_place(e, 2 * x + h)];
+        }
+    }
+    __device__ __forceinline__ static void values(const u32x4* lds, Values32<D>& t) {
+        const int lane = threadIdx.x & 63, m = lane & 31, h = lane >> 5;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                const int d = 32 * j + m;
+                t.v[j][u] = lds[4 * D + 4 * d + value_place(d, 2 * h + u)];
+            }
+    }
+};
+
 // Bytes of a word that are the code of a NaN, as 0xff.
 __device__ __forceinline__ unsigned nan_bytes(unsigned w) {
     return (((w & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xffu;
@@ -223,12 +290,21 @@ __device__ __forceinline__ int64_t wave_inclusive(int64_t v) {
 // What a row sees of the tile at e0.
 struct Sight {
     int low, lead;                       // events from low on and those below lead; the lane's row's
-    int low_max, lead_min;               // over the wave's rows
+    int low_max, lead_min;               // over the rows that read the tiles together
     // Of tiles in rising order, those before number `from` and from number `to` on are seen whole by all rows.
     __device__ __forceinline__ void edges(const Group& r, int* from, int* to) const {
         auto before = [&](int tile) { return tile < r.first ? min(tile, r.lead) : r.lead + tile - r.first; };
         *to = before(low_max / kTile + (low_max % kTile != 0));
         *from = min(before(lead_min / kTile), *to);
+    }
+    __device__ __forceinline__ void agree() {
+#pragma unroll
+        for (int d = 32; d; d >>= 1) {
+            low_max = max(low_max, __shfl_xor(low_max, d, 64));
+            lead_min = min(lead_min, __shfl_xor(lead_min, d, 64));
+        }
+        low_max = __builtin_amdgcn_readfirstlane(low_max);
+        lead_min = __builtin_amdgcn_readfirstlane(lead_min);
     }
     template <int N>
     __device__ __forceinline__ unsigned seen(int e) const {
@@ -408,21 +484,11 @@ struct Rows32 {
         auto tile_of = [&](int i) { return i < r.lead ? i : r.first + (i - r.lead); };
         int from, to;
         at.edges(r, &from, &to);
+        run_masked(c, table, r, hk, scale, at, max(i0, from), min(i1, to));
         Pages32<PE> page;
         Keys32<D> k;
         Values32<D> v;
         floatx16 s[2];
-        for (int i = max(i0, from); i < min(i1, to); ++i) {
-            page.find(table, tile_of(i) * PT);
-            load_keys32<D, PE>(c, page, hk, k);
-            load_values32<D, PE>(c, page, hk, 0, v);
-            load_values32<D, PE>(c, page, hk, 1, v);
-            scores(k, s);
-            mask(s, v, at.seen<32>(tile_of(i) * kTile + 32 * h), true);
-            const float mc = raise(s, scale);
-            weigh(s, v, scale, mc, 0);
-            weigh(s, v, scale, mc, 1);
-        }
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
             const int stop = part ? i1 : min(i1, from);
@@ -445,6 +511,94 @@ struct Rows32 {
                 weigh(s, v, scale, mc, 1);
                 load_values32<D, PE>(c, page, hk, 1, v);
                 page = later;
+            }
+        }
+    }
+    __device__ __forceinline__ void run_masked(const dlrm_history_cache_t& c, const int32_t* table, const Group& r, int hk,
+                                               float scale, const Sight& at, int i0, int i1) {
+        const int h = (threadIdx.x & 63) >> 5;
+        Pages32<PE> page;
+        Keys32<D> k;
+        Values32<D> v;
+        floatx16 s[2];
+        for (int i = i0; i < i1; ++i) {
+            const int tile = i < r.lead ? i : r.first + (i - r.lead);
+            page.find(table, tile * (kTile / PE));
+            load_keys32<D, PE>(c, page, hk, k);
+            load_values32<D, PE>(c, page, hk, 0, v);
+            load_values32<D, PE>(c, page, hk, 1, v);
+            scores(k, s);
+            mask(s, v, at.seen<32>(tile * kTile + 32 * h), true);
+            const float mc = raise(s, scale);
+            weigh(s, v, scale, mc, 0);
+            weigh(s, v, scale, mc, 1);
+        }
+    }
+    // The scales of the lane's pages, and whether they are there.
+    struct Scales {
+        float k[2], v[2];
+        bool in[2];
+        __device__ __forceinline__ void load(const dlrm_history_cache_t& c, const Pages32<PE>& p, int hk) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                in[u] = is_page(c, p.v[u]);
+                k[u] = c.k_scale[(int64_t)(is_page(c, p.k[u]) ? p.k[u] : 0) * c.n_kv_heads + hk];
+                v[u] = c.v_scale[(int64_t)(in[u] ? p.v[u] : 0) * c.n_kv_heads + hk];
+            }
+        }
+    };
+    // All waves of a block over the same tiles, through LDS: while one tile is used the next one is read into
+    // registers.  `live`: the wave has rows; `lds`: two tiles.
+    template <int WAVES>
+    __device__ __forceinline__ void run_staged(const dlrm_history_cache_t& c, const int32_t* table, const Group& r, int hk,
+                                               float scale, const Sight& at, int i0, int i1, bool live, u32x4* lds) {
+        constexpr int PT = kTile / PE;
+        typedef Staged<D, PE, WAVES> S;
+        auto tile_of = [&](int i) { return i < r.lead ? i : r.first + (i - r.lead); };
+        int from, to;
+        at.edges(r, &from, &to);
+        if (live) run_masked(c, table, r, hk, scale, at, max(i0, from), min(i1, to));
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            const int stop = part ? i1 : min(i1, from);
+            int i = part ? max(i0, to) : i0;
+            if (i >= stop) continue;
+            S staged;
+            typename S::Pages page;
+            Pages32<PE> mine;
+            Scales now, next;
+            page.find(table, tile_of(i) * PT);
+            mine.find(table, tile_of(i) * PT);
+            staged.load(c, page, hk);
+            now.load(c, mine, hk);
+            page.find(table, tile_of(min(i + 1, stop - 1)) * PT);
+            mine.find(table, tile_of(min(i + 1, stop - 1)) * PT);
+            __syncthreads();                // the tiles before may still be in use
+            staged.store(lds);
+            __syncthreads();
+            for (int which = 0; i < stop; ++i, which ^= 1) {
+                const u32x4* tile = lds + which * (8 * D);
+                staged.load(c, page, hk);
+                next.load(c, mine, hk);
+                page.find(table, tile_of(min(i + 2, stop - 1)) * PT);
+                mine.find(table, tile_of(min(i + 2, stop - 1)) * PT);
+                if (live) {
+                    Keys32<D> k;
+                    Values32<D> v;
+                    floatx16 s[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) k.scale[u] = now.k[u], v.scale[u] = now.v[u], v.in[u] = now.in[u];
+                    S::keys(tile, k);
+                    scores(k, s);
+                    S::values(tile, v);
+                    if (__builtin_expect(__any(!v.in[0] || !v.in[1]), 0)) mask(s, v, ~0u, false);
+                    const float mc = raise(s, scale);
+                    weigh(s, v, scale, mc, 0);
+                    weigh(s, v, scale, mc, 1);
+                }
+                staged.store(lds + (which ^ 1) * (8 * D));
+                now = next;
+                __syncthreads();
             }
         }
     }
@@ -503,12 +657,14 @@ struct Rows32 {
     }
 };
 
-template <int D, int PE, typename T, template <int, int, typename> class Rows>
-__global__ __launch_bounds__(256, 2) void history_shared_kernel(SharedArgs a, SharedWs ws) {
+// WAVES to a block; where there are more than one they share the tiles.
+template <int D, int PE, typename T, template <int, int, typename> class Rows, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void history_shared_kernel(SharedArgs a, SharedWs ws) {
     typedef Rows<D, PE, T> R;
+    __shared__ u32x4 lds[WAVES > 1 ? 2 * 8 * D : 1];
     const LookupArgs& l = a.l;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), hk = blockIdx.y;
-    const int heads = l.n_heads / l.c.n_kv_heads, rows = l.queries * heads, taken = R::COLS * ws.waves;
+    const int heads = l.n_heads / l.c.n_kv_heads, rows = l.queries * heads, taken = R::COLS * WAVES;
 
     // tiles and pieces before each lane's share of the groups
     const int each = (a.n_groups + 63) / 64;
@@ -546,30 +702,44 @@ __global__ __launch_bounds__(256, 2) void history_shared_kernel(SharedArgs a, Sh
         const int i0 = (int)(at - start - block * r.count);
         const int i1 = r.count - i0 < stop - at ? r.count : i0 + (int)(stop - at);
         at += i1 - i0;
-        const int64_t chunk = block * ws.waves + wave, first = chunk * R::COLS;
+        const int64_t chunk = block * WAVES + wave, first = chunk * R::COLS;
         const int64_t all = (int64_t)(r.end - r.begin) * rows, place = piece + block + blockIdx.x;
-        if (first >= all || place >= ws.pieces) continue;
+        if (place >= ws.pieces) continue;
+        const bool any = first < all;
+        if (WAVES == 1 && !any) continue;
 
         // the lane's column: a row of one of the group's histories
-        const int64_t row = first + R::column() < all ? first + R::column() : first;
+        const int64_t row = any ? (first + R::column() < all ? first + R::column() : first) : 0;
         const int b = r.begin + (int)(row / rows), y = (int)(row % rows);
         const Span sp = span_of(l, b);
         Sight sight;
         sight.low = sp.low;                 // a history without events: as if it saw everything, and not read later
         sight.lead = sp.low ? sp.lead_events : 0x7fffffff;
         sight.low_max = sight.low, sight.lead_min = sight.lead;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) {
-            sight.low_max = max(sight.low_max, __shfl_xor(sight.low_max, d, 64));
-            sight.lead_min = min(sight.lead_min, __shfl_xor(sight.lead_min, d, 64));
-        }
-        sight.low_max = __builtin_amdgcn_readfirstlane(sight.low_max);
-        sight.lead_min = __builtin_amdgcn_readfirstlane(sight.lead_min);
         R sums;
         sums.start((const T*)l.q + ((int64_t)b * l.queries + y / heads) * l.ld_q + (int64_t)(hk * heads + y % heads) * D,
                    l.scale, l.wide);
-        sums.run(l.c, l.c.table + (int64_t)r.slot * l.c.max_pages, r, hk, c, sight, i0, i1);
-        sums.leave(ws.partial + ((place * gridDim.y + hk) * ws.waves + wave) * (R::COLS * (D + 2)), c);
+        const int32_t* table = l.c.table + (int64_t)r.slot * l.c.max_pages;
+        float* const part = ws.partial + ((place * gridDim.y + hk) * WAVES + wave) * (R::COLS * (D + 2));
+        if constexpr (WAVES == 1) {
+            sight.agree();
+            sums.run(l.c, table, r, hk, c, sight, i0, i1);
+        } else {
+            __shared__ int low_max, lead_min;   // the same tiles are masked in all waves of the block
+            __syncthreads();
+            if (threadIdx.x == 0) low_max = 0, lead_min = 0x7fffffff;
+            __syncthreads();
+            sight.agree();
+            if (lane == 0 && any) {
+                atomicMax(&low_max, sight.low_max);
+                atomicMin(&lead_min, sight.lead_min);
+            }
+            __syncthreads();
+            sight.low_max = __builtin_amdgcn_readfirstlane(low_max);
+            sight.lead_min = __builtin_amdgcn_readfirstlane(lead_min);
+            sums.template run_staged<WAVES>(l.c, table, r, hk, c, sight, i0, i1, any, lds);
+        }
+        if (any) sums.leave(part, c);
     }
 }
 
@@ -676,16 +846,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
     }
 }
 
-// Rows that a wave takes, and the waves of a block: as many as a group's rows need on average, up to four.
+// Rows that a wave takes, and the waves of a block: as many as a group's rows need on average, up to four (heads of 32:
+// two, whose tiles have a chunk for each thread of no more).
 struct Shape {
     int cols, waves;
 };
-static Shape shape_of(int64_t batch, int64_t n_groups, int rows) {
+static Shape shape_of(int dim, int64_t batch, int64_t n_groups, int rows) {
     const int64_t mean = (batch + n_groups - 1) / n_groups * rows;
     Shape s;
     s.cols = mean > 16 ? 32 : 16;
     const int64_t chunks = (mean + s.cols - 1) / s.cols;
-    s.waves = chunks > 2 ? 4 : (chunks > 1 ? 2 : 1);
+    s.waves = chunks > 2 && dim > 32 ? 4 : (chunks > 1 ? 2 : 1);
     return s;
 }
 static int runs_of(int n_kv_heads, int waves) {
@@ -714,14 +885,14 @@ static SharedPlan plan_of(const dlrm_history_cache_t& c, int64_t batch, int64_t 
 
 size_t shared_workspace_bytes(const dlrm_history_cache_t& c, int64_t batch, int64_t n_groups, int queries, int n_heads) {
     const int rows = queries * (n_heads / c.n_kv_heads);
-    return plan_of(c, batch, n_groups, rows, shape_of(batch, n_groups, rows)).end;
+    return plan_of(c, batch, n_groups, rows, shape_of(c.head_dim, batch, n_groups, rows)).end;
 }
 
 template <int D, int PE, typename T>
 static hipError_t launch_t(const SharedArgs& a, void* workspace, hipStream_t s) {
     const LookupArgs& l = a.l;
     const int rows = l.queries * (l.n_heads / l.c.n_kv_heads);
-    const Shape shape = shape_of(l.batch, a.n_groups, rows);
+    const Shape shape = shape_of(D, l.batch, a.n_groups, rows);
     if (!grid_fits(l.batch, 256) || !grid_fits(a.n_groups, kGroupThreads)) return kTooLarge;
     const SharedPlan p = plan_of(l.c, l.batch, a.n_groups, rows, shape);
     char* const w = (char*)workspace;
@@ -729,8 +900,11 @@ static hipError_t launch_t(const SharedArgs& a, void* workspace, hipStream_t s) 
                          (float*)(w + p.partial), shape.waves, shape.cols};
     hipLaunchKernelGGL(history_group_kernel, dim3(a.n_groups), dim3(kGroupThreads), 0, s, a, ws);
     const dim3 grid(runs_of(l.c.n_kv_heads, shape.waves), l.c.n_kv_heads), block(64 * shape.waves);
-    if (shape.cols == 32) hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows32>), grid, block, 0, s, a, ws);
-    else hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows16>), grid, block, 0, s, a, ws);
+    if (shape.cols == 16) hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows16, 1>), grid, block, 0, s, a, ws);
+    else if (shape.waves == 1) hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows32, 1>), grid, block, 0, s, a, ws);
+    else if (shape.waves == 2) hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows32, 2>), grid, block, 0, s, a, ws);
+    else if constexpr (D > 32)
+        hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows32, 4>), grid, block, 0, s, a, ws);
     const int chunks = (rows + 15) / 16 * l.c.n_kv_heads;
     const dim3 tails(l.batch, chunks);
     if ((int64_t)l.batch * chunks > kTailBlocks)
