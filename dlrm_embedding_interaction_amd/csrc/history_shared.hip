@@ -26,10 +26,12 @@ constexpr int kSharedWaves = 2048;       // waves the shared tiles' kernel aims 
 
 // A group: its rows of the batch, the slot of one of its histories with events, and
 // the tiles on the same pages in all of them that any of them sees: [0, lead) and
-// [first, common), `count` in all.
+// [first, common), `count` in all.  As written, before the first page on which they
+// differ is known: up to the last tile that all have whole.
 struct Group {
     int begin, end, slot, lead, first, common, count, unused;
 };
+constexpr int kParts = 8;                  // blocks that compare the page lists of one group, at most
 // Where the group stands in the row of all tiles: of its tiles, and of its pieces.
 struct Place {
     int64_t tile, piece;
@@ -37,16 +39,30 @@ struct Place {
 
 struct SharedWs {
     Group* groups;          // (n_groups)
+    int* differs;           // (n_groups, parts): the first tile that a part found to differ
     Place* places;          // (n_groups)
     int* group_of;          // (batch)
     int64_t* per;           // tiles of a run
     int64_t pieces;         // that there is room for: as many as there can be while no two groups overlap
     float* partial;         // (pieces, kv heads, waves of a block, columns (head_dim + 2))
     int waves, cols;        // waves of a block, rows of a wave: 16 or 32
+    int parts;
 };
 
-// A block per group: which tiles lie on the same pages in all of its histories.
-// Those without events see nothing and do not count.
+__device__ __forceinline__ Group group_at(const SharedWs& ws, int g) {
+    Group r = ws.groups[g];
+    int differs = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) differs = min(differs, ws.differs[g * ws.parts + min(i, ws.parts - 1)]);
+    r.common = min(r.common, differs);
+    r.first = min(r.first, r.common);
+    r.lead = min(r.lead, r.common);
+    r.count = r.lead + r.common - r.first;
+    return r;
+}
+
+// Blocks of (group, part of its histories): which tiles lie on the same pages in all of
+// them.  Those without events see nothing and do not count.
 constexpr int kGroupThreads = 1024;
 __global__ __launch_bounds__(kGroupThreads) void history_group_kernel(SharedArgs a, SharedWs ws) {
     __shared__ int len_min, first_min, lead_max, differs, some;
@@ -70,7 +86,7 @@ __global__ __launch_bounds__(kGroupThreads) void history_group_kernel(SharedArgs
     }
     __syncthreads();
     for (int b = begin + tid; b < end; b += kGroupThreads) {
-        ws.group_of[b] = g;
+        if (blockIdx.y == 0) ws.group_of[b] = g;
         const Span s = span_of(l, b);
         if (!s.len) continue;
         atomicMin(&len_min, s.len);
@@ -82,39 +98,38 @@ __global__ __launch_bounds__(kGroupThreads) void history_group_kernel(SharedArgs
     Group r = {begin, end, 0, 0, 0, 0, 0, 0};
     if (some >= 0) {
         r.slot = l.slots ? l.slots[some] : some;
-        const int pt = kTile / c.page_events, tiles = len_min / kTile;
-        r.first = min(first_min, tiles);
+        const int pt = kTile / c.page_events;
+        r.common = len_min / kTile;
+        r.first = min(first_min, r.common);
         r.lead = min(lead_max, r.first);
         const int lead = r.lead * pt, first = r.first * pt;
-        const int n = lead + tiles * pt - first;            // pages [0, lead) and [first, tiles pt)
+        const int n = lead + r.common * pt - first;         // pages [0, lead) and [first, common pt)
         const int32_t* one = c.table + (int64_t)r.slot * c.max_pages;
         int least = 0x7fffffff;
-        for (int b0 = begin; b0 < end; b0 += kGroupThreads) {
-            const int here = min(end - b0, kGroupThreads);
+        for (int b0 = begin + blockIdx.y; b0 < end; b0 += kGroupThreads * ws.parts) {
+            const int here = min((end - b0 + ws.parts - 1) / ws.parts, kGroupThreads);
             __syncthreads();
             if (tid < here) {
-                const int slot = l.slots ? l.slots[b0 + tid] : b0 + tid;
-                slot_of[tid] = slot >= 0 && slot < c.n_slots && c.lens[slot] > 0 ? slot : -1;
+                const int b = b0 + tid * ws.parts, slot = l.slots ? l.slots[b] : b;
+                slot_of[tid] = slot >= 0 && slot < c.n_slots && c.lens[slot] > 0 ? slot : r.slot;
             }
             __syncthreads();
-            for (int i = tid & 63; i < n; i += 64) {
-                const int x = i < lead ? i : first + i - lead, p = one[x];
-#pragma unroll 8
-                for (int k = tid >> 6; k < here; k += kGroupThreads / 64) {
-                    const int slot = slot_of[k];
-                    const int q = slot >= 0 ? c.table[(int64_t)slot * c.max_pages + x] : p;
-                    least = q != p ? min(least, x) : least;
-                }
+            // a wave for each history and 64 of its pages
+            const int chunks = (n + 63) / 64, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+#pragma unroll 4
+            for (int w = wave; w < here * chunks; w += kGroupThreads / 64) {
+                const int i = w / here * 64 + (tid & 63), x = i < lead ? i : first + i - lead;
+                const int32_t* row = c.table + (int64_t)slot_of[w % here] * c.max_pages;
+                if (i < n) least = row[x] != one[x] ? min(least, x / pt) : least;
             }
         }
         if (least < 0x7fffffff) atomicMin(&differs, least);
         __syncthreads();
-        r.common = min(differs / pt, tiles);
-        r.first = min(r.first, r.common);
-        r.lead = min(r.lead, r.common);
-        r.count = r.lead + r.common - r.first;
     }
-    if (tid == 0) ws.groups[g] = r;
+    if (tid == 0) {
+        ws.differs[g * ws.parts + blockIdx.y] = differs;
+        if (blockIdx.y == 0) ws.groups[g] = r;
+    }
 }
 
 // ---- tiles for 32 rows -----------------------------------------------------------
@@ -428,17 +443,21 @@ struct Rows32 {
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[j][i] = 0.f;
     }
+    // Products that follow one another add to different sums: one that adds to the last one's result waits for it.
     __device__ __forceinline__ void scores(const Keys32<D>& k, floatx16 (&s)[2]) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int x = 0; x < 16; ++x) s[u][x] = 0.f;
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-                const bf16x8 kk = decode8(k.k[u][x / 2][x % 2 * 2], k.k[u][x / 2][x % 2 * 2 + 1], k.scale[u]);
+        for (int x = 0; x < D / 16; ++x) {
+            bf16x8 kk[2];
 #pragma unroll
-                for (int y = 0; y < NQ; ++y) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kk, q[x][y], s[u], 0, 0, 0);
-            }
+            for (int u = 0; u < 2; ++u) kk[u] = decode8(k.k[u][x / 2][x % 2 * 2], k.k[u][x / 2][x % 2 * 2 + 1], k.scale[u]);
+#pragma unroll
+            for (int y = 0; y < NQ; ++y)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kk[u], q[x][y], s[u], 0, 0, 0);
         }
     }
     // The running maximum; what the exponents are taken against.
@@ -469,12 +488,15 @@ struct Rows32 {
             }
             bf16x8 pp[NP];
             split8<NP>(p, pp);
+            bf16x8 vv[D / 32];
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                const bf16x8 vv = decode8(v.v[j][half][u % 2 * 2], v.v[j][half][u % 2 * 2 + 1], v.scale[half]);
+            for (int j = 0; j < D / 32; ++j)
+                vv[j] = decode8(v.v[j][half][u % 2 * 2], v.v[j][half][u % 2 * 2 + 1], v.scale[half]);
 #pragma unroll
-                for (int y = 0; y < NP; ++y) o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vv, pp[y], o[j], 0, 0, 0);
-            }
+            for (int y = 0; y < NP; ++y)
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+                    o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vv[j], pp[y], o[j], 0, 0, 0);
         }
     }
     __device__ __forceinline__ void run(const dlrm_history_cache_t& c, const int32_t* table, const Group& r, int hk,
@@ -671,7 +693,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_shared_kernel(SharedArg
     const int lo = lane * each, hi = lo + each < a.n_groups ? lo + each : a.n_groups;
     int64_t tiles = 0, pieces = 0;
     for (int i = lo; i < hi; ++i) {
-        const Group r = ws.groups[i];
+        const Group r = group_at(ws, i);
         const int64_t blocks = blocks_of(r, rows, taken);
         tiles += blocks * r.count;
         pieces += blocks;
@@ -689,7 +711,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_shared_kernel(SharedArg
 
     const float c = exponent_scale(l.scale);
     while (at < stop) {
-        const Group r = ws.groups[gi];
+        const Group r = group_at(ws, gi);
         const int64_t blocks = blocks_of(r, rows, taken);
         if (start + blocks * r.count <= at) {
             start += blocks * r.count;
@@ -758,9 +780,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
     const Span sp = span_of(l, b);
     if (sp.count == 0 && l.slots && blockIdx.y == 0 && tid == 0) count_refused(l, b);
 
-    const int gi = ws.group_of[b];
+    const int gi = a.groups ? ws.group_of[b] : b / (l.batch / a.n_groups);
     Group r = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (gi >= 0 && gi < a.n_groups) r = ws.groups[gi];
+    Place place_of = {0, 0};
+    const int64_t per = *ws.per;
+    if (gi >= 0 && gi < a.n_groups) {
+        r = group_at(ws, gi);
+        place_of = ws.places[gi];           // not written where nothing is shared
+    }
     if (b < r.begin || b >= r.end || !sp.len) r.common = r.count = 0;
     // the history's tiles behind the shared ones
     auto tile_of = [&](int i) { return i < sp.lead ? i : sp.first + (i - sp.lead); };
@@ -793,13 +820,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
         sum += __shfl_xor(sum, 32, 64);
     }
     if (r.count) {
-        const Place at = ws.places[gi];
-        const int64_t per = *ws.per;
         const int64_t row = (int64_t)(b - r.begin) * rows + (live ? y : 0), chunk = row / ws.cols, block = chunk / ws.waves;
-        const int64_t t0 = at.tile + block * r.count, run0 = t0 / per, run1 = (t0 + r.count - 1) / per;
+        const int64_t t0 = place_of.tile + block * r.count, run0 = t0 / per, run1 = (t0 + r.count - 1) / per;
         const int col = (int)(row % ws.cols);
         for (int64_t i = run0 + wave; __any(i <= run1); i += WAVES) {
-            const int64_t place = at.piece + block + i;
+            const int64_t place = place_of.piece + block + i;
             if (i > run1 || place < 0 || place >= ws.pieces) continue;
             const float* part =
                 ws.partial + ((place * l.c.n_kv_heads + hk) * ws.waves + chunk % ws.waves) * (ws.cols * (D + 2));
@@ -868,12 +893,13 @@ static size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Where the parts of the workspace begin.
 struct SharedPlan {
-    size_t places, group_of, per, partial, end;
+    size_t differs, places, group_of, per, partial, end;
     int64_t pieces;
 };
 static SharedPlan plan_of(const dlrm_history_cache_t& c, int64_t batch, int64_t n_groups, int rows, Shape shape) {
     SharedPlan p;
-    p.places = round256(n_groups * sizeof(Group));
+    p.differs = round256(n_groups * sizeof(Group));
+    p.places = p.differs + round256(n_groups * kParts * sizeof(int));
     p.group_of = p.places + round256(n_groups * sizeof(Place));
     p.per = p.group_of + round256(batch * sizeof(int));
     p.partial = p.per + 256;
@@ -896,9 +922,11 @@ static hipError_t launch_t(const SharedArgs& a, void* workspace, hipStream_t s) 
     if (!grid_fits(l.batch, 256) || !grid_fits(a.n_groups, kGroupThreads)) return kTooLarge;
     const SharedPlan p = plan_of(l.c, l.batch, a.n_groups, rows, shape);
     char* const w = (char*)workspace;
-    const SharedWs ws = {(Group*)w, (Place*)(w + p.places), (int*)(w + p.group_of), (int64_t*)(w + p.per), p.pieces,
-                         (float*)(w + p.partial), shape.waves, shape.cols};
-    hipLaunchKernelGGL(history_group_kernel, dim3(a.n_groups), dim3(kGroupThreads), 0, s, a, ws);
+    // enough blocks for every CU
+    const int parts = a.n_groups <= 256 / kParts ? kParts : (a.n_groups < 256 ? 256 / a.n_groups : 1);
+    const SharedWs ws = {(Group*)w, (int*)(w + p.differs), (Place*)(w + p.places), (int*)(w + p.group_of),
+                         (int64_t*)(w + p.per), p.pieces, (float*)(w + p.partial), shape.waves, shape.cols, parts};
+    hipLaunchKernelGGL(history_group_kernel, dim3(a.n_groups, parts), dim3(kGroupThreads), 0, s, a, ws);
     const dim3 grid(runs_of(l.c.n_kv_heads, shape.waves), l.c.n_kv_heads), block(64 * shape.waves);
     if (shape.cols == 16) hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows16, 1>), grid, block, 0, s, a, ws);
     else if (shape.waves == 1) hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows32, 1>), grid, block, 0, s, a, ws);
