@@ -460,21 +460,26 @@ struct Rows32 {
                 for (int u = 0; u < 2; ++u) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kk[u], q[x][y], s[u], 0, 0, 0);
         }
     }
-    // The running maximum; what the exponents are taken against.
+    // The running maximum, which may lag by 2^kLag, each row's for itself, so that the sums are rescaled in few tiles;
+    // what the exponents are taken against.  Weights stay below 1, as against the maximum itself.
+    static constexpr float kLag = 8.f;
     __device__ __forceinline__ float raise(const floatx16 (&s)[2], float scale) {
         float top = -INFINITY;
 #pragma unroll
         for (int x = 0; x < 32; ++x) top = fmaxf(top, s[x >> 4][x & 15]);
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float mx = fmaxf(m, top);
-        if (__any(mx > m)) {
-            const float alpha = mx == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mx) * scale);
+        const unsigned bits = __float_as_uint(top);
+        const auto both = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+        top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1]));
+        const bool up = (top - m) * scale > kLag;
+        if (__any(up)) {
+            const float mx = up ? top : m;
+            const float alpha = up ? __builtin_amdgcn_exp2f((m - mx) * scale) : 1.f;
             sum *= alpha;
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) o[j] *= alpha;
             m = mx;
         }
-        return m == -INFINITY ? 0.f : m * scale;
+        return m == -INFINITY ? 0.f : m * scale + kLag;
     }
     // The second product's steps 2 half and 2 half + 1.
     __device__ __forceinline__ void weigh(const floatx16 (&s)[2], const Values32<D>& v, float scale, float mc, int half) {
@@ -673,7 +678,7 @@ struct Rows32 {
                 *(floatx4*)(part + n * D + 32 * j + 8 * a + 4 * h) =
                     floatx4{o[j][4 * a], o[j][4 * a + 1], o[j][4 * a + 2], o[j][4 * a + 3]};
         if (h == 0) {
-            part[32 * D + n] = m * c;
+            part[32 * D + n] = m * c + kLag;
             part[32 * D + 32 + n] = sum;
         }
     }
