@@ -156,6 +156,12 @@ struct Values32 {
     bool in[2];
 };
 
+// A value that the whole wave reads, into scalar registers.
+template <typename T>
+__device__ __forceinline__ T read_scalar(const T* p, int64_t i) {
+    return ((const __attribute__((address_space(4))) T*)p)[i];
+}
+
 // The pages that a lane reads of a tile, found a tile ahead of the codes, whose
 // addresses would otherwise be waited for.  A shared tile lies whole within every
 // list; an entry that is no page is only looked at when it is used, so that no load
@@ -164,6 +170,10 @@ template <int PE>
 struct Pages32 {
     int k[2], v[2];
     __device__ __forceinline__ void find(const int32_t* table, int p0) {
+        if constexpr (PE == 64) {
+            k[0] = k[1] = v[0] = v[1] = read_scalar(table, p0);
+            return;
+        }
         const int lane = threadIdx.x & 63;
         asm("" : "+v"(p0));     // a lane's value: one that is the wave's would be waited for, to reach scalar registers
 #pragma unroll
@@ -218,26 +228,32 @@ struct Staged {
     }
     __device__ __forceinline__ static int value_place(int d, int chunk) { return chunk ^ (d >> 2 & 3); }
 
+    // A chunk's column of a value row, and so its page, is the same for all chunks of a lane.
+    __device__ __forceinline__ static int value_event() { return 16 * value_place(threadIdx.x >> 2, threadIdx.x & 3); }
+    // The page of each key chunk and of the value chunks.  A tile on one page: that page, in a scalar register, from
+    // which the addresses follow without vector instructions.
     struct Pages {
-        int k[CHUNKS], v[CHUNKS];
+        int k[PE == 64 ? 1 : CHUNKS], v;
         __device__ __forceinline__ void find(const int32_t* table, int p0) {
-            asm("" : "+v"(p0));     // as in Pages32
+            if constexpr (PE == 64) {
+                k[0] = v = read_scalar(table, p0);
+            } else {
+                asm("" : "+v"(p0));     // as in Pages32
 #pragma unroll
-            for (int i = 0; i < CHUNKS; ++i) {
-                const int at = i * 64 * WAVES + threadIdx.x, d = at >> 2;
-                k[i] = table[p0 + at / ROW / PE];
-                v[i] = table[p0 + 16 * value_place(d, at & 3) / PE];
+                for (int i = 0; i < CHUNKS; ++i) k[i] = table[p0 + (i * 64 * WAVES + (int)threadIdx.x) / ROW / PE];
+                v = table[p0 + value_event() / PE];
             }
         }
     };
     __device__ __forceinline__ void load(const dlrm_history_cache_t& c, const Pages& p, int hk) {
+        const int64_t pv = (int64_t)(is_page(c, p.v) ? p.v : 0) * c.n_kv_heads + hk;
+        const uint8_t* const vp = c.v + pv * D * PE;
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
-            const int at = i * 64 * WAVES + threadIdx.x, row = at / ROW, d = at >> 2, e = 16 * value_place(d, at & 3);
-            const int64_t pk = (int64_t)(is_page(c, p.k[i]) ? p.k[i] : 0) * c.n_kv_heads + hk;
-            const int64_t pv = (int64_t)(is_page(c, p.v[i]) ? p.v[i] : 0) * c.n_kv_heads + hk;
-            k[i] = *(const u32x4*)(c.k + (pk * PE + row % PE) * D + 16 * key_place(row, at % ROW));
-            v[i] = *(const u32x4*)(c.v + (pv * D + d) * PE + e % PE);
+            const int at = i * 64 * WAVES + threadIdx.x, row = at / ROW, d = at >> 2, pk = p.k[PE == 64 ? 0 : i];
+            const uint8_t* const kp = c.k + ((int64_t)(is_page(c, pk) ? pk : 0) * c.n_kv_heads + hk) * D * PE;
+            k[i] = *(const u32x4*)(kp + (unsigned)(row % PE * D + 16 * key_place(row, at % ROW)));
+            v[i] = *(const u32x4*)(vp + (unsigned)(d * PE + value_event() % PE));
         }
     }
     __device__ __forceinline__ void store(u32x4* lds) const {
@@ -568,9 +584,15 @@ struct Rows32 {
         __device__ __forceinline__ void load(const dlrm_history_cache_t& c, const Pages32<PE>& p, int hk) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
+                if (PE == 64 && u) {
+                    k[u] = k[0], v[u] = v[0], in[u] = in[0];
+                    break;
+                }
                 in[u] = is_page(c, p.v[u]);
-                k[u] = c.k_scale[(int64_t)(is_page(c, p.k[u]) ? p.k[u] : 0) * c.n_kv_heads + hk];
-                v[u] = c.v_scale[(int64_t)(in[u] ? p.v[u] : 0) * c.n_kv_heads + hk];
+                const int64_t ik = (int64_t)(is_page(c, p.k[u]) ? p.k[u] : 0) * c.n_kv_heads + hk;
+                const int64_t iv = (int64_t)(in[u] ? p.v[u] : 0) * c.n_kv_heads + hk;
+                k[u] = PE == 64 ? read_scalar(c.k_scale, ik) : c.k_scale[ik];
+                v[u] = PE == 64 ? read_scalar(c.v_scale, iv) : c.v_scale[iv];
             }
         }
     };
