@@ -850,18 +850,31 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
         const int64_t row = (int64_t)(b - r.begin) * rows + (live ? y : 0), chunk = row / ws.cols, block = chunk / ws.waves;
         const int64_t t0 = place_of.tile + block * r.count, run0 = t0 / per, run1 = (t0 + r.count - 1) / per;
         const int col = (int)(row % ws.cols);
-        for (int64_t i = run0 + wave; __any(i <= run1); i += WAVES) {
-            const int64_t place = place_of.piece + block + i;
-            if (i > run1 || place < 0 || place >= ws.pieces) continue;
-            const float* part =
-                ws.partial + ((place * l.c.n_kv_heads + hk) * ws.waves + chunk % ws.waves) * (ws.cols * (D + 2));
-            const float pm = part[ws.cols * D + col], ps = part[ws.cols * D + ws.cols + col];
-            if (pm == -INFINITY) continue;
-            const float mx = fmaxf(m, pm), f0 = __builtin_amdgcn_exp2f(m - mx), f1 = __builtin_amdgcn_exp2f(pm - mx);
-            m = mx;
-            sum = sum * f0 + ps * f1;
+        // two pieces at a time, all of their reads on the way together
+        for (int64_t i0 = run0 + wave; __any(i0 <= run1); i0 += 2 * WAVES) {
+            float pm[2], ps[2];
+            floatx4 po[2][D / 16];
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) o[j] = o[j] * f0 + *(const floatx4*)(part + col * D + 16 * j + 4 * g) * f1;
+            for (int u = 0; u < 2; ++u) {
+                const int64_t place = place_of.piece + block + i0 + u * WAVES;
+                const bool in = i0 + u * WAVES <= run1 && place >= 0 && place < ws.pieces;
+                const float* part = ws.partial +
+                                    (((in ? place : 0) * l.c.n_kv_heads + hk) * ws.waves + chunk % ws.waves) * (ws.cols * (D + 2));
+                pm[u] = part[ws.cols * D + col];
+                ps[u] = part[ws.cols * D + ws.cols + col];
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) po[u][j] = *(const floatx4*)(part + col * D + 16 * j + 4 * g);
+                pm[u] = in ? pm[u] : -INFINITY;
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (pm[u] == -INFINITY) continue;
+                const float mx = fmaxf(m, pm[u]), f0 = __builtin_amdgcn_exp2f(m - mx), f1 = __builtin_amdgcn_exp2f(pm[u] - mx);
+                m = mx;
+                sum = sum * f0 + ps[u] * f1;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) o[j] = o[j] * f0 + po[u][j] * f1;
+            }
         }
     }
     if constexpr (WAVES == 1) {
