@@ -339,14 +339,6 @@ static int direct_waves(int64_t blocks, int room) {
     return w;
 }
 
-// A history's visible tiles at most, as the host can tell.
-static int64_t most_tiles(const LookupArgs& a) {
-    const int64_t span = ((int64_t)a.c.max_pages * a.c.page_events + kTile - 1) / kTile;
-    if (a.window >= span * kTile || a.sinks >= span * kTile) return span;
-    const int64_t seen = (a.window + kTile - 1) / kTile + 1 + (a.sinks + kTile - 1) / kTile;
-    return seen < span ? seen : span;
-}
-
 template <int D, int PE, typename T>
 static hipError_t launch_t(LookupArgs a, hipStream_t s) {
     const int rows = a.queries * (a.n_heads / a.c.n_kv_heads);

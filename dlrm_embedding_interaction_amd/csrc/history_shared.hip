@@ -951,7 +951,9 @@ static SharedPlan plan_of(const dlrm_history_cache_t& c, int64_t batch, int64_t 
 
 size_t shared_workspace_bytes(const dlrm_history_cache_t& c, int64_t batch, int64_t n_groups, int queries, int n_heads) {
     const int rows = queries * (n_heads / c.n_kv_heads);
-    return plan_of(c, batch, n_groups, rows, shape_of(c.head_dim, batch, n_groups, rows)).end;
+    const size_t shared = plan_of(c, batch, n_groups, rows, shape_of(c.head_dim, batch, n_groups, rows)).end;
+    const size_t single = lookup_workspace_bytes(c, batch, queries, n_heads);
+    return shared > single ? shared : single;
 }
 
 template <int D, int PE, typename T>
@@ -994,7 +996,22 @@ static hipError_t launch_p(const SharedArgs& a, int dtype, void* ws, hipStream_t
     return launch_d<128, PE>(a, dtype, ws, s);
 }
 
+// Whether the groups' histories are looked up one by one: three kernels take 11 to 20 us before they save anything.
+// Tiles of all rows' chunks, one by one against shared: 4 kv heads of 32, fp32, 32 groups of 16, 16384 (500 events) 16
+// us to 23, 32768 (1000) 29 to 27, 65536 51 to 31; 8 of 128, bf16, 32 groups of 4, 16384 36 to 40, 32768 63 to 44; 4 groups
+// of 64, 32768 53 to 53.  Histories of few tiles have most of them to themselves: 32 groups of 64, 8 of 128, up to 204
+// events (4 tiles) 83 to 115, up to 504 (8) 154 to 133.
+static bool one_by_one(const LookupArgs& l) {
+    const int64_t tiles = most_tiles(l), rows = (int64_t)l.queries * (l.n_heads / l.c.n_kv_heads);
+    return tiles <= 5 || l.batch * tiles * l.c.n_kv_heads * ((rows + 15) / 16) <= 24576;
+}
+
 hipError_t launch_history_lookup_shared(const SharedArgs& a, int dtype, void* ws, hipStream_t s) {
+    if (one_by_one(a.l)) {
+        LookupArgs l = a.l;
+        l.partial = (float*)ws;
+        return launch_history_lookup(l, dtype, s);
+    }
     if (a.l.c.page_events == 16) return launch_p<16>(a, dtype, ws, s);
     if (a.l.c.page_events == 32) return launch_p<32>(a, dtype, ws, s);
     return launch_p<64>(a, dtype, ws, s);

@@ -35,6 +35,14 @@ __device__ __forceinline__ Span span_of(const LookupArgs& a, int b) {
     return s;
 }
 
+// A history's visible tiles at most, as the host can tell.
+inline int64_t most_tiles(const LookupArgs& a) {
+    const int64_t span = ((int64_t)a.c.max_pages * a.c.page_events + kTile - 1) / kTile;
+    if (a.window >= span * kTile || a.sinks >= span * kTile) return span;
+    const int64_t seen = (a.window + kTile - 1) / kTile + 1 + (a.sinks + kTile - 1) / kTile;
+    return seen < span ? seen : span;
+}
+
 // A slot that is none is counted, by one thread of the history's blocks.
 __device__ __forceinline__ void count_refused(const LookupArgs& a, int b) {
     if (a.slots[b] < 0 || a.slots[b] >= a.c.n_slots) atomicAdd(&a.c.counters[1], 1);

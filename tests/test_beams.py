@@ -241,10 +241,16 @@ class Beams(Pair):
         return got
 
 
+def roomy(page):
+    """Pages of a table so wide that a lookup without a window reads shared tiles once however small it is: calls
+    whose tables and windows hold little are looked up history by history."""
+    return 400000 // page
+
+
 def family(dtype, dim, page, kv=2, shared=150, beams=5, users=2, tails=(3, 1, 9, 2, 70), room=None):
     """`users` histories of `shared` events and more, each forked into `beams`, with events of their own behind."""
     most = -(-(shared + 40 * users + max(tails) + 8) // page)
-    p = Beams(users * (most + beams * 8) + 40, users * beams + 3, room or most + 1, kv, dim, page, dtype)
+    p = Beams(users * (most + beams * 8) + 40, users * beams + 3, room or roomy(page), kv, dim, page, dtype)
     firsts = [u * beams for u in range(users)]
     p.append(firsts, [shared + 40 * u for u in range(users)])
     p.fork([f for f in firsts for _ in range(beams - 1)], [f + 1 + i for f in firsts for i in range(beams - 1)])
@@ -255,7 +261,7 @@ def family(dtype, dim, page, kv=2, shared=150, beams=5, users=2, tails=(3, 1, 9,
 
 @pytest.mark.parametrize("page", [16, 64])
 def test_reorder(page):
-    p, every = family(torch.bfloat16, 32, page)
+    p, every = family(torch.bfloat16, 32, page, room=400 // page)
     groups = [every[:5], every[5:]]
     p.reorder(groups, [[1, 0, 2, 4, 3], [0, 0, 0, 3, 0]])          # a permutation; one beam takes over
     p.same()
@@ -305,7 +311,7 @@ def test_reorder_large_pools(n_pages):
 
 
 def test_reorder_without_slots():
-    p, every = family(torch.bfloat16, 32, 16)
+    p, every = family(torch.bfloat16, 32, 16, room=25)
     parents = [[2, 2, 1, 0, 4], [1, 0, 0, 1, 1]]
     p.cpu.reorder([every[:5], every[5:]], parents)
     p.gpu.reorder(p.slots(parents))
@@ -353,7 +359,7 @@ def test_shared_shapes(dtype, dim, page, users, shared, beams, heads, kv, querie
 
 
 def test_shared_histories_without_anything_in_common():
-    p = Beams(200, 6, 20, 2, 64, 32, torch.bfloat16)
+    p = Beams(200, 6, roomy(32), 2, 64, 32, torch.bfloat16)
     p.append(list(range(6)), [300, 301, 64, 1, 0, 500])
     p.shared(list(range(6)), 6, 4)
     p.shared(list(range(6)), 2, 4, 1, 100, 4)
@@ -372,6 +378,50 @@ def test_shared_trimmed_histories():
     p.shared(every, 5, 4, 1, 100, 20)
     p.shared(every, 5, 4, 1, 40, 0)
     p.shared(every, 5, 4)                          # some pages are there for one history and gone for the next
+
+
+@pytest.mark.parametrize("room", [30, 60])
+def test_shared_one_by_one(room):
+    """Tables and windows of few events: history by history, whatever the groups."""
+    p, every = family(torch.bfloat16, 64, 16, shared=200, room=room)
+    for window, sinks in ((ALL, 0), (100, 20), (1, 0)):
+        a = p.shared(every, 5, 4, 2, window, sinks)
+        p.seed -= 2
+        assert torch.equal(a, p.shared(every, torch.tensor([0, 3], device="cuda"), 4, 2, window, sinks))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,page,members,rows", [
+    (32, 16, 4, 4), (32, 64, 8, 4), (32, 32, 8, 8), (32, 16, 40, 4), (64, 32, 4, 4), (64, 64, 8, 4), (64, 16, 8, 8),
+    (64, 64, 40, 4), (128, 64, 4, 4), (128, 16, 8, 4), (128, 32, 8, 8), (128, 16, 40, 4), (128, 64, 40, 5)])
+def test_shared_windows(dtype, dim, page, members, rows):
+    """Windows and sinks that end in shared tiles, at another event for each row, and NaN events that some rows see and
+    others do not.  Histories stand in the batch many times, each time with other queries."""
+    kv, users = 8, 3
+    p = Beams(users * (700 // page + members * 8), users * members, 1000 // page, kv, dim, page, dtype)
+    firsts = [u * members for u in range(users)]
+
+    def edit(k, v):
+        v[180:190] = float("nan")                 # the first user's
+    p.append(firsts, [300, 410, 333], edit=edit)
+    p.fork([f for f in firsts for _ in range(members - 1)], [f + 1 + i for f in firsts for i in range(members - 1)])
+    every = list(range(users * members))
+    p.append(every, [(3, 1, 9, 2, 70, 0, 131)[i % 7] for i in every])
+    batch = every * (4400 // (kv * len(every)) + 1)
+    some = list(range(0, len(batch), 41)) + list(range(7))
+    for window, sinks in ((290, 0), (260, 10), (300, 70), (340, 1), (200, 181)):
+        p.seed += 2
+        q = randn((len(batch), 1, rows * kv, dim), p.seed, dtype)
+        got = p.gpu.lookup_shared(q.cuda(), members, window=window, sinks=sinks, slots=p.slots(batch))
+        got = f64(got)[some]
+        out, mag, big = p.cpu.lookup([batch[i] for i in some], f64(q)[some], window, sinks, dim ** -0.5)
+        seen = np.isnan(out)
+        assert np.array_equal(np.isnan(got), seen)
+        tol = bound(np.nan_to_num(out), np.nan_to_num(mag), big, dim, 700, dtype,
+                    2.0 ** -15 if dtype != torch.float32 else U, 0.0)
+        worst = float((np.abs(got - out)[~seen] / tol[~seen]).max())
+        print(f"window {window} sinks {sinks}: worst error / bar {worst:.3f}, {seen.mean():.2f} not numbers", flush=True)
+        assert worst <= 1.0
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -475,7 +525,7 @@ def test_beam_search_over_histories():
     of the shared histories, logits by a Linear layer, selection, reordering, and the taken items' events behind the
     histories."""
     users, beams, kv, heads, dim, items, page = 3, 4, 2, 4, 32, 700, 16
-    pairs = [Beams(400, users * beams, 30, kv, dim, page, torch.float32) for _ in range(2)]
+    pairs = [Beams(400, users * beams, roomy(page), kv, dim, page, torch.float32) for _ in range(2)]
     table = randn((items, heads * dim), 40, torch.float32, 0.3).cuda()
     keys, values = (randn((items, kv, dim), s, torch.float32).cuda() for s in (41, 42))
     zero = torch.zeros(items, device="cuda")
