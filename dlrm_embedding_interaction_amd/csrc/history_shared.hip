@@ -22,7 +22,7 @@
 namespace dlrm {
 
 constexpr int kTailBlocks = 512;          // rows' blocks of one wave from here on, of four below
-constexpr int kSharedWaves = 2048;       // waves the shared tiles' kernel aims at: two on each SIMD
+constexpr int kSharedWaves = 2048;       // waves of the shared tiles' kernel, where two are resident on each SIMD
 
 // A group: its rows of the batch, the slot of one of its histories with events, and
 // the tiles on the same pages in all of them that any of them sees: [0, lead) and
@@ -706,9 +706,19 @@ struct Rows32 {
     }
 };
 
+// Waves on a SIMD.  With 32 rows, heads of 128 pass 256 registers: in fp32, whose scores take three products, and in fp16
+// (two), unless four waves share the decoding, what is moved to memory costs more than a second wave gives.  32 groups of
+// 16 x 4 rows, 3000 events: fp32 146.5 -> 121.4 us, fp16 112.5 -> 101.7, but bf16 90.6 -> 97.5; four waves, 16 groups of
+// 256 rows: fp32 178 -> 165, but fp16 134 -> 143.
+template <int D, typename T>
+constexpr int resident(int cols, int waves) {
+    return D == 128 && cols == 32 && (Parts<T>::q == 3 || (Parts<T>::q == 2 && waves < 4)) ? 1 : 2;
+}
+
 // WAVES to a block; where there are more than one they share the tiles.
 template <int D, int PE, typename T, template <int, int, typename> class Rows, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void history_shared_kernel(SharedArgs a, SharedWs ws) {
+__global__ __launch_bounds__(64 * WAVES, (resident<D, T>(Rows<D, PE, T>::COLS, WAVES)))
+void history_shared_kernel(SharedArgs a, SharedWs ws) {
     typedef Rows<D, PE, T> R;
     __shared__ u32x4 lds[WAVES > 1 ? 2 * 8 * D : 1];
     const LookupArgs& l = a.l;
@@ -969,7 +979,9 @@ static hipError_t launch_t(const SharedArgs& a, void* workspace, hipStream_t s) 
     const SharedWs ws = {(Group*)w, (int*)(w + p.differs), (Place*)(w + p.places), (int*)(w + p.group_of),
                          (int64_t*)(w + p.per), p.pieces, (float*)(w + p.partial), shape.waves, shape.cols, parts};
     hipLaunchKernelGGL(history_group_kernel, dim3(a.n_groups, parts), dim3(kGroupThreads), 0, s, a, ws);
-    const dim3 grid(runs_of(l.c.n_kv_heads, shape.waves), l.c.n_kv_heads), block(64 * shape.waves);
+    // runs that are all resident at once: 32 groups of 8 x 4 rows, fp32 heads of 128, 1024 waves 60 us, 2048 70
+    const int all = runs_of(l.c.n_kv_heads, shape.waves), runs = resident<D, T>(shape.cols, shape.waves) == 1 ? (all + 1) / 2 : all;
+    const dim3 grid(runs, l.c.n_kv_heads), block(64 * shape.waves);
     if (shape.cols == 16) hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows16, 1>), grid, block, 0, s, a, ws);
     else if (shape.waves == 1) hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows32, 1>), grid, block, 0, s, a, ws);
     else if (shape.waves == 2) hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows32, 2>), grid, block, 0, s, a, ws);
