@@ -3,8 +3,8 @@
 //
 //   s(w, v) = score_w + x(w, v) - log sum_u exp x(w, u)       over the allowed u
 //
-// The `keep` largest s of a group, in descending order; equal ones by beam, then by
-// item.  Within a beam the order is that of the logits, so that a row's best items
+// The `keep` largest s of a group, in descending order; equal ones by beam, then
+// by logit and item.  Within a beam the order is that of the logits, so that a row's best items
 // are found without its sum, in the same pass over it.
 #include "history.h"
 
@@ -419,7 +419,7 @@ __device__ __forceinline__ float round_down(double x) {
 }
 
 struct JoinShared {
-    double base[kMostBeams];                // score - log of the sum; NaN: the beam gives no candidates
+    double score[kMostBeams], log_sum[kMostBeams];     // log_sum NaN: the beam gives no candidates
     Best room[kBlockWaves][kJoinRoom], pool[kPool];
     double part_sum[kMostLists / 8 + kMostBeams];
     float part_ref[kMostLists / 8 + kMostBeams], part_top[kMostLists / 8 + kMostBeams];
@@ -427,7 +427,7 @@ struct JoinShared {
     unsigned char held[kMostLists];         // its candidates
     unsigned short list[kMostLists];        // the lists that may hold one of the best
     int place[kPool];
-    int lists, count[kBlockWaves];
+    int lists, count[kBlockWaves], joined;  // joined: not one of count, which slower waves may yet read
     float found[kBlockWaves];
 };
 
@@ -481,15 +481,17 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
             // The logarithm in whole multiples of 2^-40: rows of the same logits tie, whatever their order and their
             // sums' last bits.
             const double l = (far(ref) ? (double)ref : whole(ref) * kLn2) + log(sum);
-            if (top < INFINITY) to = score - rint(l * 0x1p40) * 0x1p-40;
+            if (top < INFINITY) to = rint(l * 0x1p40) * 0x1p-40;
         }
-        s.base[w] = to;
+        s.score[w] = score;
+        s.log_sum[w] = to;
     }
     __syncthreads();
     for (int i = tid; i < lists; i += 64 * kBlockWaves) {
-        const double b = s.base[(unsigned)i / (unsigned)a.segs];
-        const bool in = b == b && s.best[i] > -INFINITY;
-        s.best[i] = in ? round_down(b + (double)s.best[i]) : -INFINITY;
+        const unsigned w = (unsigned)i / (unsigned)a.segs;
+        const double l = s.log_sum[w];
+        const bool in = l == l && s.best[i] > -INFINITY;
+        s.best[i] = in ? round_down(s.score[w] + ((double)s.best[i] - l)) : -INFINITY;
         if (!in) s.held[i] = 0;
     }
     __syncthreads();
@@ -539,7 +541,7 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
             for (int u = 0; u < 4; ++u) {
                 if (j0 >= held[u]) continue;
                 const int w = l[u] / a.segs;
-                const double score = s.base[w] + (double)unordered((unsigned)(key[u] >> 32)) + 0.;
+                const double score = s.score[w] + ((double)unordered((unsigned)(key[u] >> 32)) - s.log_sum[w]) + 0.;
                 const unsigned item = 0xffffffffu - (unsigned)key[u];
                 enter(key[u] && score >= (double)floor,
                       Best{ordered(score), (u64)(kMostBeams - 1 - w) << 57 | (key[u] >> 32) << kItemBits |
@@ -593,11 +595,11 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         for (int i = lane; i < n; i += 64) s.pool[i] = buf[i];
-        if (lane == 0) s.count[0] = n;
+        if (lane == 0) s.joined = n;
     }
     for (int i = tid; i < kPool; i += 64 * kBlockWaves) s.place[i] = 0;
     __syncthreads();
-    n = all <= kPool ? all : s.count[0];
+    n = all <= kPool ? all : s.joined;
     // each one's place: how many are above it, counted by `split` threads
     const int split = max(64 * kBlockWaves / max(n, 1), 1);
     for (int i = tid; i < n * split; i += 64 * kBlockWaves) {

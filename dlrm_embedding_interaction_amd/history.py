@@ -193,7 +193,7 @@ def history_select(logits: torch.Tensor, scores: Optional[torch.Tensor] = None, 
     ``logits`` (groups, beams, items), fp32, bf16 or fp16: of each beam's next item; rows may be columns of a wider
     tensor.  ``scores`` (groups, beams) fp32: the sums of log-probabilities so far (none: 0).  A continuation's score
     is its beam's plus the log-probability of its item; the ``keep`` (none: as many as there are beams) best of each
-    group come in descending order, equal ones by beam, then by item; what is missing is -inf, -1 and -1.
+    group come in descending order, equal ones by beam, then by logit and item; what is missing is -inf, -1 and -1.
     ``allowed`` (items,) or (groups, beams, items), truth values: items that may be taken.  ``ended`` (groups, beams),
     truth values: beams that are carried over as they are, with ``end_item`` as their item.  A beam whose score is not
     finite, or with NaN or +inf among its allowed logits, gives no continuations."""
@@ -203,7 +203,9 @@ def history_select(logits: torch.Tensor, scores: Optional[torch.Tensor] = None, 
         raise ValueError("logits must be (groups, beams, items)")
     dev = logits.device
     groups, beams, items = logits.shape
-    keep = beams if keep is None else int(keep)
+    keep, end_item = beams if keep is None else int(keep), int(end_item)
+    if not 0 <= keep < 2 ** 31 or not -2 ** 31 <= end_item < 2 ** 31:
+        raise ValueError("keep and end_item must fit 32 bits, and keep not be negative")
     ld = _item_rows(logits, "logits")
     if scores is not None:
         _dev(scores, torch.float32, "scores")
@@ -229,14 +231,18 @@ def history_select(logits: torch.Tensor, scores: Optional[torch.Tensor] = None, 
     key = (logits.dtype, beams, keep, end_item, items, groups)
     entry = _SELECT.get(key)
     if entry is None:
-        d = _Select(DTYPES[logits.dtype], beams, keep, int(end_item), items)
+        d = _Select(DTYPES[logits.dtype], beams, keep, end_item, items)
         if len(_SELECT) > 1024:
             _SELECT.clear()
         entry = _SELECT[key] = (ctypes.byref(d), int(load().dlrm_history_select_workspace_bytes(ctypes.byref(d),
                                                                                                 groups)))
+    if not entry[1]:                    # refused below, and nothing written
+        groups_out, keep_out = 1, 1
+    else:
+        groups_out, keep_out = groups, keep
     ws = torch.empty(max(entry[1], 256), dtype=torch.uint8, device=dev)
-    out_scores = torch.empty((groups, max(keep, 0)), dtype=torch.float32, device=dev)
-    out = torch.empty((2, groups, max(keep, 0)), dtype=torch.int32, device=dev)
+    out_scores = torch.empty((groups_out, keep_out), dtype=torch.float32, device=dev)
+    out = torch.empty((2, groups_out, keep_out), dtype=torch.int32, device=dev)
     rc = load().dlrm_history_select(entry[0], groups, logits.data_ptr(), ld,
                                     None if scores is None else scores.data_ptr(),
                                     None if allowed is None else allowed.data_ptr(), ld_allowed,
@@ -394,7 +400,8 @@ class HistoryCache:
 
         ``groups``: how many histories of the batch, one behind the other, each group has; or ascending offsets
         (n_groups,), group g being the histories [groups[g], groups[g + 1]).  What is shared is found in the page
-        lists, so that the result is ``lookup``'s whatever the groups are, up to the order of its sums."""
+        lists, so that the result is ``lookup``'s whatever the groups are, up to the order of its sums.  Where little
+        can be seen (by the table's width, the window and the batch) histories are looked up one by one."""
         a, batch, queries, heads, ld_q, out, ld_out = self._queries(q, window, sinks, scale, out)
         if isinstance(groups, torch.Tensor):
             ib, n_groups, at = _offsets(groups, self.device), groups.shape[0], groups.data_ptr()

@@ -583,8 +583,9 @@ dlrm_status_t dlrm_history_lookup(const dlrm_history_cache_t* c, const dlrm_atte
  * dlrm_history_lookup_shared -- the same for histories in groups that share what
  * came first, as forks do: events that lie on the same pages in all histories of a
  * group are read once for the group.  Which these are is found in the page lists:
- * the groups say only which histories to look at together.  Out is dlrm_history_lookup's, up to
- * the order of its sums.
+ * the groups say only which histories to look at together.  Out is
+ * dlrm_history_lookup's, up to the order of its sums; where little can be seen (by
+ * max_pages, the window and the batch) histories are looked up one by one.
  *   n_groups    >= 1
  *   groups      device (n_groups) ascending integers of index_bytes: group g is the
  *               histories [groups[g], groups[g+1]) of the batch, the last one
@@ -592,8 +593,7 @@ dlrm_status_t dlrm_history_lookup(const dlrm_history_cache_t* c, const dlrm_atte
  *               holds; groups may be empty.  NULL: groups of batch / n_groups,
  *               which has to be whole
  *   workspace   of dlrm_history_shared_workspace_bytes (host only; 0 on invalid
- *               arguments), a few MB and 64 head_dim bytes for each query row and
- *               each of a group's kv heads on top
+ *               arguments)
  */
 size_t dlrm_history_shared_workspace_bytes(const dlrm_history_cache_t* c, int64_t batch, int64_t n_groups,
                                            int32_t queries, int32_t n_heads);
@@ -648,8 +648,8 @@ dlrm_status_t dlrm_history_reorder(const dlrm_history_cache_t* c, int64_t n_grou
  * scores[b * beams + w] so far.  Its continuation by item v has the score
  *   score + logits[v] - log(sum over allowed u of exp(logits[u])).
  * Of each group the `keep` best are written in descending order: score, beam
- * (parent) and item; equal scores by the lowest beam, then the lowest item.  Where
- * there are fewer, the rest is -inf, -1 and -1.  With one beam and no scores: the
+ * (parent) and item; equal scores by the lowest beam, then the largest logit, then the
+ * lowest item.  Where there are fewer, the rest is -inf, -1 and -1.  With one beam and no scores: the
  * best items of a row and their log-probabilities.
  *   dtype     of logits; sums and scores are held in 64 bits, so that the order is
  *             that of the logits given, and scores are rounded when written

@@ -112,6 +112,72 @@ def test_select_values_at_the_ends_of_the_range(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_select_logits_far_from_zero_and_from_each_other(dtype):
+    """Rows that rise, fall and jump by thousands, around 0 and around values at which exponents lose their fractions."""
+    ramp = torch.linspace(-3000.0, 3000.0, 9001)
+    jumps = torch.cat([ramp[::7], 20 * ramp[::5], ramp[::11] - 2900, torch.full((4000,), -50000.0)])[:9001]
+    jumps = torch.cat([jumps, torch.full((9001 - len(jumps),), -1000.0)])
+    rows = torch.stack([ramp, ramp.flip(0), ramp[torch.randperm(9001, generator=gen(23))], jumps, jumps.flip(0)])[None]
+    s = torch.tensor([[0.0, -1.5, -0.75, -2.0, 1.0]])
+    check_select(rows.to(dtype), s, 64)
+    if dtype != torch.float16:                     # up to 65504
+        check_select((rows + 2.0 ** 21).to(dtype), s, 9)
+        check_select((rows - 2.0 ** 21).to(dtype), s, 9)
+        check_select((rows * 2.0 ** 90).to(dtype), s, 9)
+    check_select((rows * 2.0 ** -20).to(dtype), s, 100)
+
+
+@pytest.mark.parametrize("beams,items,keep", [(1, 3000, 4), (1, 600001, 3), (24, 66000, 24), (100, 20000, 128)])
+def test_select_many_parts(beams, items, keep):
+    """Rows cut into 2, 256, 32 and 8 parts."""
+    check_select(randn((1, beams, items), 24, torch.bfloat16, 2.0), some_scores(1, beams, 25), keep)
+
+
+@pytest.mark.parametrize("items", [300, 5003])
+def test_select_equal_scores_of_all_beams(items):
+    """More equal candidates than the join holds at once."""
+    same = torch.full((2, 128, items), 0.25)
+    check_select(same, torch.zeros(2, 128), 128)
+    ended = torch.zeros((2, 128), dtype=torch.bool)
+    ended[:, ::3] = True
+    check_select(same, torch.zeros(2, 128), 100, ended=ended)
+
+
+def test_beams_refusals():
+    x = torch.zeros((2, 3, 10), device="cuda")
+    s = torch.zeros((2, 3), device="cuda")
+    for args in ((x[0], ), (x, s[:1]), (x.transpose(1, 2), ), (x[:, :, ::2], ), (x, s, -1), (x, s, 2 ** 32 + 1),
+                 (x, s, 3, s[0] > 0), (x, s, 3, None, s[0] > 0), (x, s, 3, None, None, 2 ** 31)):
+        with pytest.raises(ValueError):
+            dl.history_select(*args)
+    for args in ((x.double(), ), (x, s.double()), (x, s, 3, x), (x, s, 3, None, s), (x.cpu(), )):
+        with pytest.raises(TypeError):
+            dl.history_select(*args)
+    for args in ((x, s, 0), (x, s, 129), (x, s, 2 ** 31 - 1), (x[:, :0], s[:, :0], 1), (x[:, :, :0], s), (x[:0], s[:0]),
+                 (x[:, :1].expand(2, 3, 10), s), (x[:1, :1].expand(2, 3, 10), s)):
+        with pytest.raises((RuntimeError, ValueError)):
+            dl.history_select(*args)
+    h = dl.HistoryCache(20, 6, 4, 1, 32, 16)
+    p = torch.zeros((2, 3), dtype=torch.int32, device="cuda")
+    for parents, slots in ((p[0], None), (p, p[:1]), (p.cpu(), None)):
+        with pytest.raises((ValueError, TypeError)):
+            h.reorder(parents, slots)
+    for parents in (p[:, :0], p[:0], torch.zeros((3, 3), dtype=torch.int32, device="cuda")):
+        with pytest.raises(RuntimeError):
+            h.reorder(parents)
+    with pytest.raises(RuntimeError):
+        h.reorder(torch.zeros((1, 129), dtype=torch.int32, device="cuda"),
+                  torch.zeros((1, 129), dtype=torch.int32, device="cuda"))
+    q = torch.zeros((6, 2, 32), device="cuda")
+    for groups in (0, -1, 4, p, torch.zeros((2, 4), dtype=torch.int64, device="cuda")[:, 0]):
+        with pytest.raises((ValueError, TypeError)):
+            h.lookup_shared(q, groups)
+    with pytest.raises(RuntimeError):
+        h.lookup_shared(q, p[0, :0])
+    assert h.n_free == 20 and h.n_refused == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("items", [3, 1003, 9001])
 def test_select_allowed_and_ended(dtype, items):
     x = randn((4, 6, items), 8, dtype, 2.0)
@@ -446,6 +512,24 @@ def test_shared_events_that_a_row_does_not_see_do_not_reach_it(dtype):
                 assert torch.equal(got[b], want[b])
             else:
                 assert torch.isnan(got[b]).all()
+
+
+def test_shared_offsets_that_are_none():
+    """Offsets that fall or lie outside the batch give some result, touch nothing else and hold nothing up; more groups
+    than histories are all right."""
+    p, every = family(torch.bfloat16, 64, 16, shared=300, users=3)
+    q = randn((15, 2, 8, 64), 33, torch.bfloat16).cuda()
+    want = p.shared(every, 5, 8, 2, q=q)
+    for offs in ([0, 10, 5], [7, 3, 12, 1], [0, 10 ** 6, 2], [-5, -9, 4], [2 ** 31 - 1, -2 ** 31, 3], [9, 0] * 40,
+                 [0, 2 ** 40 + 3, -2 ** 60]):
+        room = torch.full((17, 2, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        itype = torch.int64 if max(offs) > 2 ** 31 else torch.int32
+        p.gpu.lookup_shared(q, torch.tensor(offs, dtype=itype, device="cuda"), slots=p.slots(every), out=room[1:16])
+        assert torch.all(room[0] == 7) and torch.all(room[16] == 7)
+        assert torch.equal(p.gpu.lookup_shared(q, 5, slots=p.slots(every)), want)
+    for offs in ([0] * 100, list(range(0, 300, 3)), [0, 10 ** 6, 10 ** 6]):
+        p.shared(every, torch.tensor(offs, dtype=torch.int32, device="cuda"), 8)
+    p.same()
 
 
 def test_shared_bad_pages_are_not_seen():
