@@ -8,7 +8,9 @@ values go to the 8-bit cache, and at serving time
 * the result joins the dense features and the candidate's own row in the pairwise-dot interaction, and the
   top MLP gives the click probability,
 * "what if the user had clicked this one" is a fork of the history, an append to it, and a lookup; the fork is
-  freed afterwards, and the pool compacted now and then.
+  freed afterwards, and the pool compacted now and then,
+* "what may come next" is a beam search over forks of each user's history: a lookup that reads what the forks share
+  once, logits over all items, the best continuations of each user's beams, and the histories reordered to them.
 
 Every step runs in the library's kernels.  Run: python examples/history_ranking.py
 """
@@ -37,6 +39,7 @@ class HistoryRanker:
         self.items = draw(items, dim, scale=dim ** -0.5)
         self.w_qkv, self.b_qkv = draw(3 * dim, dim, scale=dim ** -0.5 * 4), draw(3 * dim, scale=0.1)
         self.w_bot, self.b_bot = draw(dim, n_dense, scale=n_dense ** -0.5), draw(dim, scale=0.1)
+        self.b_items = torch.zeros(items, device=device)
         width = dim + 3                                   # x and the dots of [x, candidate, history]
         self.w_top = [draw(32, width, scale=width ** -0.5), draw(1, 32, scale=32 ** -0.5)]
         self.b_top = [draw(32, scale=0.1), draw(1, scale=0.1)]
@@ -46,7 +49,7 @@ class HistoryRanker:
 
     def rows(self, idx):
         """(N, dim) rows of the item table, as bags of one index."""
-        off = torch.arange(idx.numel(), device=self.device)
+        off = torch.arange(idx.numel(), dtype=idx.dtype, device=self.device)
         return dl.embbag_sum([self.items], [idx.reshape(-1).contiguous()], [off])[:, 0]
 
     def project(self, idx):
@@ -89,6 +92,28 @@ class HistoryRanker:
         self.cache.free(spare)
         return p
 
+    def suggest(self, last, slots, spare, steps=3):
+        """The likeliest next `steps` items behind each of B histories that end with `last` -> log-probabilities
+        (B, beams) and items (B, beams, steps), with spare (B, beams) slots that are used in between."""
+        B, beams = spare.shape
+        forks, every = spare.flatten(), torch.arange(spare.numel(), device=self.device)
+        self.cache.fork(slots.repeat_interleave(beams), forks)
+        scores = torch.full((B, beams), -float("inf"), device=self.device)
+        scores[:, 0] = 0                              # all beams are alike yet: one of them goes on
+        items, path = last.repeat_interleave(beams), torch.empty((B, beams, 0), dtype=torch.int32, device=self.device)
+        for _ in range(steps):
+            q = next(self.project(items))
+            seen = self.cache.lookup_shared(q, beams, window=self.window, sinks=self.sinks, slots=forks)
+            logits = dl.linear_bias_act(seen.flatten(1), self.items, self.b_items, dl.ACT_NONE)
+            scores, parents, took = dl.history_select(logits.unflatten(0, (B, beams)), scores)
+            self.cache.reorder(parents, slots=spare)
+            came = path.gather(1, parents.long()[:, :, None].expand(-1, -1, path.shape[2]))
+            path, items = torch.cat([came, took[:, :, None]], 2), took.flatten()
+            _, k, v = self.project(items)
+            self.cache.append(k, v, every, slots=forks)
+        self.cache.free(forks)
+        return scores, path
+
 
 def main(users=16, candidates=8, device="cuda"):
     r = HistoryRanker(device=device)
@@ -110,12 +135,15 @@ def main(users=16, candidates=8, device="cuda"):
     r.cache.trim(slots, window=r.window, sinks=r.sinks)
     r.cache.compact()
     trimmed = r.score(dense, cand, slots)
+    spare = torch.arange(users, 4 * users, dtype=torch.int32, device=device).unflatten(0, (users, 3))
+    likely, paths = r.suggest(click, slots, spare)
     torch.cuda.synchronize()
     print(f"{users} users, {sum(lens)} events encoded, {r.cache.n_free} pages free, {r.cache.n_refused} refused")
     print(f"first user's probabilities: {[round(p, 4) for p in before[0].tolist()]}")
     print(f"after the click: largest change {float((after - before).abs().max()):.4f}")
+    print(f"first user's likeliest next items: {paths[0, 0].tolist()}, log-probability {float(likely[0, 0]):.4f}")
     return dict(encoded=encoded, before=before, tried=tried, again=again, after=after, trimmed=trimmed, ranker=r,
-                events=events, lens=lens, slots=slots, candidates=cand, click=click)
+                events=events, lens=lens, slots=slots, candidates=cand, click=click, likely=likely, paths=paths)
 
 
 if __name__ == "__main__":

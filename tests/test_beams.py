@@ -7,6 +7,9 @@ Bars, derived before the first run.
 * Lookups: the bars of test_history; the shared part adds one more join to the corrections that they count for each 64
   keys of the history's length.
 """
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -661,3 +664,32 @@ def test_beam_search_over_histories():
         assert torch.equal(state[0][1], state[1][1]) and torch.equal(state[0][0], state[1][0])
         for n in ("table", "lens", "refs", "counters"):
             assert torch.equal(getattr(eager.gpu, n), getattr(replayed.gpu, n)), n
+
+
+def test_the_example_suggests_what_a_walk_along_the_path_scores():
+    """examples/history_ranking.py: a suggested path's score is the sum of its items' log-probabilities, each looked up
+    behind the items before it, and the users' own histories stay as they are."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "history_ranking.py")
+    spec = importlib.util.spec_from_file_location("history_ranking", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    got = module.main(users=5)
+    r, slots, likely, paths = got["ranker"], got["slots"], got["likely"], got["paths"]
+    free = r.cache.n_free
+    assert torch.isfinite(likely).all() and torch.all(likely[:, :-1] >= likely[:, 1:])
+    total = torch.zeros(15, dtype=torch.float64, device="cuda")
+    spare = torch.arange(30, 45, dtype=torch.int32, device="cuda")
+    r.cache.fork(slots.repeat_interleave(3), spare)
+    item = got["click"].repeat_interleave(3)         # as many rows as there, so that their projections are the same
+    for t in range(paths.shape[2]):
+        seen = r.cache.lookup(next(r.project(item)), window=r.window, sinks=r.sinks, slots=spare)
+        logits = dl.linear_bias_act(seen.flatten(1), r.items, r.b_items, dl.ACT_NONE).double()
+        item = paths[:, :, t].flatten().long()
+        total += (logits - torch.logsumexp(logits, 1, keepdim=True)).gather(1, item[:, None])[:, 0]
+        r.click(item, spare)
+    r.cache.free(spare)
+    # logits: fp32 sums of 64 products below 8 in all, in another order for the lookup's part: 2 x 64 x 2^-24 x 8 each;
+    # three of them and as many of their rows' largest
+    assert float((total - likely.flatten().double()).abs().max()) < 6 * 2 * 64 * 2.0 ** -24 * 8
+    assert r.cache.n_free == free and r.cache.n_refused == 0
+    assert len({tuple(p) for p in paths[0].tolist()}) == 3
