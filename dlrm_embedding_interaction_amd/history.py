@@ -389,7 +389,8 @@ class HistoryCache:
         ws = self._workspace(s, batch, queries, heads)
         rc = load().dlrm_history_lookup(self._ref, a, batch, self._slots(slots, batch), queries,
                                         q.data_ptr(), ld_q, out.data_ptr(), ld_out, ws[0], ws[1], s)
-        _check(rc, "dlrm_history_lookup")
+        if rc != DLRM_OK:
+            _check(rc, "dlrm_history_lookup")
         return out
 
     def lookup_shared(self, q: torch.Tensor, groups: Union[int, torch.Tensor], window: int = ALL_EVENTS, sinks: int = 0,
