@@ -971,7 +971,6 @@ static hipError_t launch_t(const SharedArgs& a, void* workspace, hipStream_t s) 
     const LookupArgs& l = a.l;
     const int rows = l.queries * (l.n_heads / l.c.n_kv_heads);
     const Shape shape = shape_of(D, l.batch, a.n_groups, rows);
-    if (!grid_fits(l.batch, 256) || !grid_fits(a.n_groups, kGroupThreads)) return kTooLarge;
     const SharedPlan p = plan_of(l.c, l.batch, a.n_groups, rows, shape);
     char* const w = (char*)workspace;
     // enough blocks for every CU
@@ -1019,6 +1018,7 @@ static bool one_by_one(const LookupArgs& l) {
 }
 
 hipError_t launch_history_lookup_shared(const SharedArgs& a, int dtype, void* ws, hipStream_t s) {
+    if (!grid_fits(a.l.batch, 256) || !grid_fits(a.n_groups, kGroupThreads)) return kTooLarge;
     if (one_by_one(a.l)) {
         LookupArgs l = a.l;
         l.partial = (float*)ws;
