@@ -843,23 +843,27 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
         const int slot = l.slots ? l.slots[b] : b;
         const int32_t* table = l.c.table + (int64_t)slot * l.c.max_pages;
         const float c = exponent_scale(l.scale);
+        // One wave to a block: without a second tile's registers 64 instead of 80 (heads of 64) and eight waves a SIMD, which
+        // hide more (1500 sessions' own tiles 54 -> 48 us; with the pieces' reads before the tiles, too, 65).
         Tile<D> cur, nxt;
-        load_tile<D, PE>(l.c, table, tile_of(own) * PT, hk, n, g, cur);
+        if (WAVES > 1) load_tile<D, PE>(l.c, table, tile_of(own) * PT, hk, n, g, cur);
         for (int i = own; i < sp.count; i += WAVES) {
-            if (i + WAVES < sp.count) load_tile<D, PE>(l.c, table, tile_of(i + WAVES) * PT, hk, n, g, nxt);
+            if (WAVES == 1) load_tile<D, PE>(l.c, table, tile_of(i) * PT, hk, n, g, cur);
+            else if (i + WAVES < sp.count) load_tile<D, PE>(l.c, table, tile_of(i + WAVES) * PT, hk, n, g, nxt);
             const int e0 = tile_of(i) * kTile;
             const bool whole = (e0 >= sp.low || e0 + kTile <= sp.lead_events) && e0 + kTile <= sp.len;
             use_tile<D, T>(cur, q, c, e0, whole, sp.low, sp.lead_events, sp.len, g, o, m, sum);
-            cur = nxt;
+            if (WAVES > 1) cur = nxt;
         }
         m *= c;                                          // from here on in powers of two
         sum += swizzle_xor16(sum);
         sum += __shfl_xor(sum, 32, 64);
     }
     if (r.count) {
-        const int64_t row = (int64_t)(b - r.begin) * rows + (live ? y : 0), chunk = row / ws.cols, block = chunk / ws.waves;
+        const int64_t row = (int64_t)(b - r.begin) * rows + (live ? y : 0);
+        const int64_t chunk = row >> (ws.cols == 32 ? 5 : 4), block = chunk >> (ws.waves >> 1);     // of 16 or 32; 1, 2 or 4
         const int64_t t0 = place_of.tile + block * r.count, run0 = t0 / per, run1 = (t0 + r.count - 1) / per;
-        const int col = (int)(row % ws.cols);
+        const int col = (int)row & (ws.cols - 1);
         // two pieces at a time, all of their reads on the way together
         for (int64_t i0 = run0 + wave; __any(i0 <= run1); i0 += 2 * WAVES) {
             float pm[2], ps[2];
@@ -869,7 +873,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
                 const int64_t place = place_of.piece + block + i0 + u * WAVES;
                 const bool in = i0 + u * WAVES <= run1 && place >= 0 && place < ws.pieces;
                 const float* part = ws.partial +
-                                    (((in ? place : 0) * l.c.n_kv_heads + hk) * ws.waves + chunk % ws.waves) * (ws.cols * (D + 2));
+                                    (((in ? place : 0) * l.c.n_kv_heads + hk) * ws.waves + (chunk & (ws.waves - 1))) * (ws.cols * (D + 2));
                 pm[u] = part[ws.cols * D + col];
                 ps[u] = part[ws.cols * D + ws.cols + col];
 #pragma unroll
