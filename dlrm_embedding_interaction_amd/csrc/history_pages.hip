@@ -594,7 +594,9 @@ static hipError_t release(const ReleaseArgs& a, int32_t* counts, hipStream_t s) 
 // all at once.  Column x of the page lists depends on column x alone, so a block takes
 // COLS columns of one group: it reads them all before it writes any, and nothing has to
 // be set aside in memory.  Pages that a history keeps, like those that all of a group
-// share, cost their reading alone.
+// share, cost their reading alone.  It is bound by those reads' latency and by the
+// counts' atomics: 64 groups of 8, 32 pages each, 4.8 us; 16 of 64, up to 500 pages,
+// 13 us; the free list after it 4 to 5.
 struct ReorderArgs {
     dlrm_history_cache_t c;
     const int32_t *slots, *parents;

