@@ -876,23 +876,26 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
         // two pieces at a time, all of their reads on the way together
         for (int64_t i0 = run0 + wave; __any(i0 <= run1); i0 += 2 * WAVES) {
             float pm[2], ps[2];
+            bool in[2];
             floatx4 po[2][D / 16];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int64_t place = place_of.piece + block + i0 + u * WAVES;
-                const bool in = i0 + u * WAVES <= run1 && place >= 0 && place < ws.pieces;
+                in[u] = i0 + u * WAVES <= run1 && place >= 0 && place < ws.pieces;
                 const float* part = ws.partial +
-                                    (((in ? place : 0) * l.c.n_kv_heads + hk) * ws.waves + (chunk & (ws.waves - 1))) * (ws.cols * (D + 2));
+                                    (((in[u] ? place : 0) * l.c.n_kv_heads + hk) * ws.waves + (chunk & (ws.waves - 1))) * (ws.cols * (D + 2));
                 pm[u] = part[ws.cols * D + col];
                 ps[u] = part[ws.cols * D + ws.cols + col];
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) po[u][j] = *(const floatx4*)(part + col * D + 16 * j + 4 * g);
-                pm[u] = in ? pm[u] : -INFINITY;
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                if (pm[u] == -INFINITY) continue;
-                const float mx = fmaxf(m, pm[u]), f0 = __builtin_amdgcn_exp2f(m - mx), f1 = __builtin_amdgcn_exp2f(pm[u] - mx);
+                if (!in[u]) continue;
+                // A maximum of -inf is that of a piece without a number among its scores, too: its sums are NaN, and a
+                // factor of 0 keeps them so.
+                const float mx = fmaxf(m, pm[u]), to = mx == -INFINITY ? 0.f : mx;
+                const float f0 = __builtin_amdgcn_exp2f(m - to), f1 = __builtin_amdgcn_exp2f(pm[u] - to);
                 m = mx;
                 sum = sum * f0 + ps[u] * f1;
 #pragma unroll
