@@ -183,6 +183,8 @@ constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453;
 constexpr double kShift = 0x1.8p52;      // adding and taking away: a whole number
 __device__ __forceinline__ bool far(float ref) { return !(fabsf(ref) <= 0x1p20f); }
 __device__ __forceinline__ double whole(float ref) { return rint((double)ref * kLog2e); }
+// The logarithm of what a sum against `ref` is a multiple of, less ref.
+__device__ __forceinline__ double beside(float ref) { return far(ref) ? 0. : fma(whole(ref), kLn2, -(double)ref); }
 
 // e^x 2^-w with shift = kShift - w, to 2^-29 of its value, where the result has an
 // exponent within double's.  x log2 e is split into a whole number and a rest of at most
@@ -201,7 +203,7 @@ __device__ __forceinline__ double power(double x, double shift) {
 }
 // What a sum against `from` has to be multiplied by to stand against `to`.
 __device__ __forceinline__ double moved(float from, float to) {
-    if (far(from) || far(to)) return power(fmax((double)from - (double)to, -690.), kShift);
+    if (far(from) || far(to)) return power(fmax((double)from - (double)to + (beside(from) - beside(to)), -690.), kShift);
     const double d = fmax(whole(from) - whole(to), -1000.);
     return __hiloint2double((1023 + (int)d) << 20, 0);
 }
