@@ -485,10 +485,13 @@ __device__ __forceinline__ void join_group(const SelectArgs& a, const SelectWs& 
             }
             double sum = 0;
             for (int i = 0; i < parts; ++i) sum += s.part_sum[w * parts + i] * moved(s.part_ref[w * parts + i], ref);
-            // The logarithm in whole multiples of 2^-40: rows of the same logits tie, whatever their order and their
-            // sums' last bits.
-            const double l = (far(ref) ? (double)ref : whole(ref) * kLn2) + log(sum);
-            if (top < INFINITY) to = rint(l * 0x1p40) * 0x1p-40;
+            // Rows of the same logits in another order tie, as far as 64 bits tell: their sums are the same but for the
+            // additions' rounding and a power of two, which follows from the reference and is taken out first; and the
+            // logarithm is rounded to whole multiples of 2^-32, far above its last bits and below the exponentials' 2^-29.
+            int up;
+            const double part = frexp(sum, &up);
+            const double l = far(ref) ? (double)ref + log(sum) : fma(whole(ref) + up, kLn2, log(part));
+            if (top < INFINITY) to = rint(l * 0x1p32) * 0x1p-32;
         }
         s.score[w] = score;
         s.log_sum[w] = to;

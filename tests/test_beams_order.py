@@ -45,3 +45,29 @@ def test_logits_on_both_sides_of_the_border(sign):
     x += 0.125 * torch.randint(-8, 5, x.shape, generator=gen(71))
     x[1] = x[1].flip(1)
     check_select(x + sign * BORDER, None, 64)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("items", [1900, 3001, 20000])
+def test_rows_of_the_same_logits_tie_in_any_order(dtype, items):
+    """Beams of one score whose rows hold the same logits in other orders, a rising one among them: what a sum stands
+    against follows the order of the row, its logarithm may not.  Equal scores go by beam, logit and item."""
+    tops = [512.0 * k + 280.0 for k in (*range(-24, 25), -100, -77, 50, 70, 88, 99)]      # fp16 holds 65504
+    groups, beams, keep = len(tops), 4, 60
+    rows = torch.empty((groups, beams, items), dtype=dtype)
+    for g, top in enumerate(tops):
+        x = torch.rand(items, generator=gen(72 + g)) * -800.0
+        x[-40:] *= 4.0 / 800.0
+        x = (x + top).sort().values.to(dtype)
+        for w in range(beams):
+            rows[g, w] = x if w == 1 else x[torch.randperm(items, generator=gen(200 + 4 * g + w))]
+    got = dl.history_select(rows.cuda(), torch.full((groups, beams), -2.0).cuda(), keep)
+    s, p, i = (t.cpu() for t in got)
+    for g in range(groups):
+        want = sorted((-v, w, at) for w in range(beams) for at, v in enumerate(rows[g, w].tolist()))[:keep]
+        assert p[g].tolist() == [w for _, w, _ in want], tops[g]
+        assert i[g].tolist() == [at for _, _, at in want], tops[g]
+        x = rows[g, 0].double()
+        exact = -2.0 + (rows[g, p[g].long(), i[g].long()].double() - x.max() - torch.log(torch.exp(x - x.max()).sum()))
+        # as test_beams; the logarithm's spacing at 52000 and its last rounding are below 2^-32 both
+        assert float(((s[g].double() - exact).abs() - 2.0 ** -24 * exact.abs()).max()) <= 2.0 ** -27
