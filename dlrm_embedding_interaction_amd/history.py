@@ -196,7 +196,9 @@ def history_select(logits: torch.Tensor, scores: Optional[torch.Tensor] = None, 
     group come in descending order, equal ones by beam, then by logit and item; what is missing is -inf, -1 and -1.
     ``allowed`` (items,) or (groups, beams, items), truth values: items that may be taken.  ``ended`` (groups, beams),
     truth values: beams that are carried over as they are, with ``end_item`` as their item.  A beam whose score is not
-    finite, or with NaN or +inf among its allowed logits, gives no continuations."""
+    finite, or with NaN or +inf among its allowed logits, gives no continuations.  Scores of different beams that lie
+    within 4e-9 may come in either order.  Items are masked by -inf or ``allowed``: in a row of nothing but the lowest
+    value of fp32 or bf16 every item has the log-probability 0, since the logarithm of its sum is one 64-bit number."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in DTYPES or not logits.is_cuda:
         raise TypeError("logits must be a CUDA (HIP) tensor of fp32, bf16 or fp16")
     if logits.dim() != 3:

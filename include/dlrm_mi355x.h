@@ -651,18 +651,27 @@ dlrm_status_t dlrm_history_reorder(const dlrm_history_cache_t* c, int64_t n_grou
  * (parent) and item; equal scores by the lowest beam, then the largest logit, then the
  * lowest item.  Where there are fewer, the rest is -inf, -1 and -1.  With one beam and no scores: the
  * best items of a row and their log-probabilities.
- *   dtype     of logits; sums and scores are held in 64 bits, so that the order is
- *             that of the logits given, and scores are rounded when written
+ *   dtype     of logits; exponentials are taken to 2^-29 of their value, sums and
+ *             scores are held in 64 bits, and scores are rounded when written.  Within
+ *             a beam the order is that of the logits given; continuations of different
+ *             beams whose scores lie within 4e-9 may come in either order, but beams
+ *             with one score and the same logits, within 2^20 of 0 and in whatever
+ *             order, tie (but for rare ones whose sums' last bits straddle a rounding)
  *   beams, keep  1 to 128; n_items up to 2^25
- *   logits    device (batch * beams, ld_logits).  -inf: an item that is never taken
+ *   logits    device (batch * beams, ld_logits).  -inf: an item that is never taken.
+ *             The logarithm of a row's sum is one 64-bit number, as large as the row's
+ *             largest logit: what is below 2^-53 of that is lost.  In a row of n
+ *             logits at the lowest value of fp32 or bf16, as of a mask that leaves
+ *             nothing, each item so has the log-probability 0, not -log n: mask with
+ *             -inf or with `allowed`, which leave such a beam without continuations
  *   scores    device (batch * beams) or NULL (all 0).  A beam whose score is not
- *             finite gives no continuations, and its logits are not read
+ *             finite gives no continuations, whatever its logits hold
  *   allowed   device bytes (batch * beams, ld_allowed), or one row for all
  *             (ld_allowed 0), or NULL: an item whose byte is 0 is not taken, and
  *             whatever its logit holds changes nothing
  *   ended     device (batch * beams) bytes or NULL: a beam whose byte is not 0 is
- *             carried over: its only continuation is end_item at its own score.
- *             Its logits are not read
+ *             carried over: its only continuation is end_item at its own score,
+ *             whatever its logits hold
  * A beam with NaN or +inf among its allowed logits, or without a finite one, gives
  * no continuations.
  *
