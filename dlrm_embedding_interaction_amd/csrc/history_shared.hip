@@ -18,10 +18,11 @@
 // NaN: in such tiles NaN codes are taken out of the product and given to the rows that
 // see them by a product of their places.
 //
-// What bounds it, and what it reaches: 32 users' 16 beams over up to 32000 events, bf16, 32 / 8 heads of 128, 360 us, of
-// which the shared tiles are 305 us: 1.35 GB read once (4.4 TB/s), matrix instructions in 46% and vector instructions in 55%
-// of the cycles.  64 users' 8 beams over up to 8000 events, 16 / 4 heads of 64, 68 us: 37 and the tail 16.  One row to a
-// history and kv head, 1500 sessions: 100 us, where the decoding of tiles is the work (37, and 46 for the sessions' own).
+// What bounds it, and what it reaches: 32 users' 16 beams over up to 32000 events, bf16, 32 / 8 heads of 128, 357 us, of
+// which the page lists take 6, the shared tiles 299 and the tail 32 (shortest launches; one behind the other the clock falls,
+// and they take 9, 422 and 42): 1.35 GB read once (4.5 TB/s), matrix instructions in 46% and vector instructions in 55% of
+// the cycles.  64 users' 8 beams over up to 8000 events, 16 / 4 heads of 64, 67 us: 37 and the tail 15.  One row to a history
+// and kv head, 1500 sessions: 98 us, where the decoding of tiles is the work (38, and 46 for the sessions' own).
 #include "history_tile.h"
 
 namespace dlrm {
@@ -532,7 +533,6 @@ struct Rows32 {
     __device__ __forceinline__ void run(const dlrm_history_cache_t& c, const int32_t* table, const Group& r, int hk,
                                         float scale, const Sight& at, int i0, int i1) {
         constexpr int PT = kTile / PE;
-        const int h = (threadIdx.x & 63) >> 5;
         auto tile_of = [&](int i) { return i < r.lead ? i : r.first + (i - r.lead); };
         int from, to;
         at.edges(r, &from, &to);
@@ -716,9 +716,10 @@ struct Rows32 {
 };
 
 // Waves on a SIMD.  With 32 rows, heads of 128 pass 256 registers: in fp32, whose scores take three products, and in fp16
-// (two), unless four waves share the decoding, what is moved to memory costs more than a second wave gives.  32 groups of
-// 16 x 4 rows, 3000 events: fp32 146.5 -> 121.4 us, fp16 112.5 -> 101.7, but bf16 90.6 -> 97.5; four waves, 16 groups of
-// 256 rows: fp32 178 -> 165, but fp16 134 -> 143.
+// (two) with up to two waves to a block, what is moved to memory costs more than a second wave gives.  Whole calls with two
+// waves on a SIMD and with one (and half the runs, see launch_t), 8 kv heads, 3000 events: 32 groups of 16 x 4 rows, fp32 176
+// and 125 us, fp16 129 and 95; 16 groups of 64 x 4 rows, whose blocks have four waves, fp32 217 and 190, fp16 148 and 148,
+// bf16 122 and 138.  bf16 with fewer waves to a block would gain, too (102 and 86), and is left at two.
 template <int D, typename T>
 constexpr int resident(int cols, int waves) {
     return D == 128 && cols == 32 && (Parts<T>::q == 3 || (Parts<T>::q == 2 && waves < 4)) ? 1 : 2;
@@ -853,7 +854,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void history_tail_kernel(SharedArgs 
         const int32_t* table = l.c.table + (int64_t)slot * l.c.max_pages;
         const float c = exponent_scale(l.scale);
         // One wave to a block: without a second tile's registers 64 instead of 80 (heads of 64) and eight waves a SIMD, which
-        // hide more (1500 sessions' own tiles 54 -> 48 us; with the pieces' reads before the tiles, too, 65).
+        // hide more (1500 sessions' own tiles 53 -> 46 us; with the pieces' reads before the tiles, too, 65).
         Tile<D> cur, nxt;
         if (WAVES > 1) load_tile<D, PE>(l.c, table, tile_of(own) * PT, hk, n, g, cur);
         for (int i = own; i < sp.count; i += WAVES) {
