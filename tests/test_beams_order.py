@@ -1,12 +1,10 @@
 """Selections at the borders of how sums are held, on the GPU.  Bars as in test_beams."""
-import numpy as np
 import pytest
 import torch
 
-import beams_oracle as bo
 import dlrm_embedding_interaction_amd as dl
 from test_beams import check_select
-from test_history import gen, randn
+from test_history import gen
 
 pytestmark = pytest.mark.gpu
 
